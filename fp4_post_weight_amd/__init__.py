@@ -25,6 +25,11 @@ Calls (same names as the C ABI, without the ``focus_`` prefix):
   ``quantize_mixfp4``, ``quantize_mixfp4_many``, ``dequantize_mixfp4``; the
   NVFP4 linear layer: ``nvfp4_linear``, ``nvfp4_linear_grouped`` (several
   weights sharing one X); ``abi_version``, ``status_string``.
+* Between the linear layers: ``rmsnorm`` (with the residual's addition) and
+  ``silu_mul``, each with a BF16 result or, as ``..._nvfp4`` and
+  ``..._mxfp8``, a quantized one; ``quantize_mxfp8``
+* ``mxfp4_linear`` (MXFP8 activations, MXFP4 weights) and ``w4a16_linear``
+  (BF16 activations, NVFP4 or MXFP4 weights)
 
 BF16 inputs are ``torch.bfloat16`` tensors; codes and scales are ``uint8``
 ([rows, cols/2] with element 2j in the low nibble, and [rows, cols/16] E4M3
@@ -44,6 +49,9 @@ __all__ = ["tensor_scale", "quantize", "dequantize", "quantize_act_per_token", "
            "quantize_mixfp4", "quantize_mixfp4_many", "dequantize_mixfp4", "nvfp4_linear",
            "nvfp4_linear_workspace_bytes", "nvfp4_linear_grouped", "nvfp4_linear_noalloc", "nvfp4_linear_scratch_bytes",
            "quantize_mx", "quantize_mx_many", "dequantize_mx",
+           "rmsnorm", "rmsnorm_nvfp4", "rmsnorm_mxfp8", "silu_mul", "silu_mul_nvfp4", "silu_mul_mxfp8",
+           "quantize_mxfp8", "mxfp4_linear", "mxfp4_linear_workspace_bytes", "w4a16_linear",
+           "w4a16_linear_workspace_bytes",
            "tensor_scale_many", "quantize_many", "dequantize_many", "Batch",
            "FocusError", "FocusLibraryMissing", "abi_version", "status_string", "library_path"]
 
@@ -557,6 +565,281 @@ def nvfp4_linear_noalloc(x: Quantized, w: Quantized, out: torch.Tensor) -> torch
                                                      _p(w.scales), _p(w.s2), N, K, _p(out),
                                                      0 if out.dtype == torch.float32 else 1, _stream(x.codes)))
     return out
+
+
+# ---------------------------------------------------------------------------
+# between the linear layers: norm, gated activation, MXFP8
+# ---------------------------------------------------------------------------
+
+def _launch(fn, dev, *args):
+    """Call ``fn`` with ``dev`` current and its current stream as the last
+    argument."""
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            _lib.check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+    else:
+        _lib.check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+
+
+def _rows_2d(name, t, unit):
+    _check_dev(name, t, torch.bfloat16)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D [tokens, hidden]")
+    if t.shape[1] % unit:
+        raise ValueError(f"hidden must be a multiple of {unit}")
+    return t.shape
+
+
+def _bf16_out(out, rows, cols, dev, label="out"):
+    if out is None:
+        return torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+    _check_buf(label, out, torch.bfloat16, dev, rows * cols)
+    return out
+
+
+def _mxfp8_outs(out, rows, cols, dev, dequant):
+    """Output buffers of an MXFP8 quantizer call: codes [rows, cols], scales
+    [rows, cols/32], deq [rows, cols] when dequant."""
+    if out is None:
+        return Quantized(torch.empty((rows, cols), dtype=torch.uint8, device=dev),
+                         torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev),
+                         torch.empty((rows, cols), dtype=torch.bfloat16, device=dev) if dequant else None, None)
+    if not isinstance(out, Quantized):
+        raise TypeError("out must be a Quantized tuple of buffers")
+    _check_buf("out.codes", out.codes, torch.uint8, dev, rows * cols)
+    _check_buf("out.scales", out.scales, torch.uint8, dev, rows * cols // 32)
+    if dequant:
+        if out.deq is None:
+            raise ValueError("dequant=True needs out.deq")
+        _check_buf("out.deq", out.deq, torch.bfloat16, dev, rows * cols)
+    return Quantized(out.codes, out.scales, out.deq if dequant else None, None)
+
+
+def _token_nvfp4_outs(out, rows, cols, dev, dequant):
+    """Output buffers of a per-token NVFP4 result (s2 [rows], also for no rows)."""
+    codes, scales, deq, s2 = _quant_outs(out, rows, cols, dev, dequant, s2_rows=rows)
+    return Quantized(codes, scales, deq, torch.empty(0, dtype=torch.float32, device=dev) if s2 is None else s2)
+
+
+def _norm_inputs(x, weight, residual, residual_out, unit):
+    """Checks a norm's inputs; returns (tokens, hidden, device, residual_out)."""
+    t, h = _rows_2d("x", x, unit)
+    dev = x.device
+    _check_dev("weight", weight, torch.bfloat16, dev)
+    if weight.numel() != h:
+        raise ValueError(f"weight holds {weight.numel()} elements, expected {h}")
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out needs a residual")
+        return t, h, dev, None
+    _check_dev("residual", residual, torch.bfloat16, dev)
+    if residual.shape != x.shape:
+        raise ValueError(f"residual must be [{t}, {h}]")
+    return t, h, dev, _bf16_out(residual_out, t, h, dev, "residual_out")
+
+
+def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual: Optional[torch.Tensor] = None,
+            out: Optional[torch.Tensor] = None, residual_out: Optional[torch.Tensor] = None):
+    """Root-mean-square norm of h = BF16(x + residual) (of x without a
+    residual) over X [tokens, hidden] (BF16, hidden % 8 == 0) with ``weight``
+    [hidden] BF16.  Returns (y [tokens, hidden] BF16, h or None);
+    ``residual_out``, which receives h, may be ``x`` or ``residual`` itself and
+    is allocated when None."""
+    t, h, dev, res = _norm_inputs(x, weight, residual, residual_out, 8)
+    y = _bf16_out(out, t, h, dev)
+    _launch(_lib.lib().focus_rmsnorm, dev, _p(x), _p(residual), _p(weight), eps, t, h, _p(res), _p(y))
+    return y, res
+
+
+def rmsnorm_nvfp4(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
+                  residual: Optional[torch.Tensor] = None, dequant: bool = False,
+                  out: Optional[Quantized] = None, residual_out: Optional[torch.Tensor] = None):
+    """``rmsnorm`` with the result in per-token NVFP4 (hidden % 16 == 0), the
+    input of ``nvfp4_linear``.  Returns (Quantized, h or None)."""
+    t, h, dev, res = _norm_inputs(x, weight, residual, residual_out, 16)
+    q = _token_nvfp4_outs(out, t, h, dev, dequant)
+    _launch(_lib.lib().focus_rmsnorm_nvfp4, dev, _p(x), _p(residual), _p(weight), eps, t, h, _p(res), _p(q.codes),
+            _p(q.scales), _p(q.s2), _p(q.deq))
+    return q, res
+
+
+def rmsnorm_mxfp8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
+                  residual: Optional[torch.Tensor] = None, dequant: bool = False,
+                  out: Optional[Quantized] = None, residual_out: Optional[torch.Tensor] = None):
+    """``rmsnorm`` with the result in MXFP8 (hidden % 32 == 0), the input of
+    ``mxfp4_linear``.  Returns (Quantized with codes [tokens, hidden], scales
+    [tokens, hidden/32] and s2 None, h or None)."""
+    t, h, dev, res = _norm_inputs(x, weight, residual, residual_out, 32)
+    q = _mxfp8_outs(out, t, h, dev, dequant)
+    _launch(_lib.lib().focus_rmsnorm_mxfp8, dev, _p(x), _p(residual), _p(weight), eps, t, h, _p(res), _p(q.codes),
+            _p(q.scales), _p(q.deq))
+    return q, res
+
+
+def _gated_input(name, t):
+    """A gate or up operand: 2-D with contiguous elements in a row and rows a
+    fixed distance apart (for example half the columns of a wider tensor)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on a HIP device")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D [tokens, hidden]")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"the elements of {name}'s rows must be contiguous")
+    stride = t.stride(0) if rows > 1 else cols
+    if stride < cols or stride % 8:
+        raise ValueError(f"{name}'s rows must be at least {cols} elements apart, by a multiple of 8")
+    return stride
+
+
+def _gated_inputs(gate, up, unit):
+    gs, us = _gated_input("gate", gate), _gated_input("up", up)
+    t, h = gate.shape
+    if up.shape != gate.shape:
+        raise ValueError(f"up must be [{t}, {h}]")
+    if up.device != gate.device:
+        raise ValueError(f"up is on {up.device}, expected {gate.device}")
+    if h % unit:
+        raise ValueError(f"hidden must be a multiple of {unit}")
+    return t, h, gate.device, gs, us
+
+
+def silu_mul(gate: torch.Tensor, up: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gated activation (gate * sigmoid(gate)) * up of two [tokens, hidden]
+    BF16 tensors (hidden % 8 == 0; rows may lie a multiple of 8 elements
+    apart, as the halves of one product's rows do) -> BF16 [tokens, hidden]."""
+    t, h, dev, gs, us = _gated_inputs(gate, up, 8)
+    y = _bf16_out(out, t, h, dev)
+    _launch(_lib.lib().focus_silu_mul, dev, _p(gate), gs, _p(up), us, t, h, _p(y))
+    return y
+
+
+def silu_mul_nvfp4(gate: torch.Tensor, up: torch.Tensor, dequant: bool = False,
+                   out: Optional[Quantized] = None) -> Quantized:
+    """``silu_mul`` with the result in per-token NVFP4 (hidden % 16 == 0)."""
+    t, h, dev, gs, us = _gated_inputs(gate, up, 16)
+    q = _token_nvfp4_outs(out, t, h, dev, dequant)
+    _launch(_lib.lib().focus_silu_mul_nvfp4, dev, _p(gate), gs, _p(up), us, t, h, _p(q.codes), _p(q.scales),
+            _p(q.s2), _p(q.deq))
+    return q
+
+
+def silu_mul_mxfp8(gate: torch.Tensor, up: torch.Tensor, dequant: bool = False,
+                   out: Optional[Quantized] = None) -> Quantized:
+    """``silu_mul`` with the result in MXFP8 (hidden % 32 == 0)."""
+    t, h, dev, gs, us = _gated_inputs(gate, up, 32)
+    q = _mxfp8_outs(out, t, h, dev, dequant)
+    _launch(_lib.lib().focus_silu_mul_mxfp8, dev, _p(gate), gs, _p(up), us, t, h, _p(q.codes), _p(q.scales),
+            _p(q.deq))
+    return q
+
+
+def quantize_mxfp8(x: torch.Tensor, dequant: bool = False, out: Optional[Quantized] = None) -> Quantized:
+    """MXFP8 of activations X [tokens, hidden] BF16 (hidden % 32 == 0): E4M3
+    codes [tokens, hidden], E8M0 scale bytes [tokens, hidden/32]."""
+    t, h = _rows_2d("x", x, 32)
+    q = _mxfp8_outs(out, t, h, x.device, dequant)
+    _launch(_lib.lib().focus_quantize_mxfp8, x.device, _p(x), t, h, _p(q.codes), _p(q.scales), _p(q.deq))
+    return q
+
+
+# ---------------------------------------------------------------------------
+# linear layers with 4-bit weights and 8- or 16-bit activations
+# ---------------------------------------------------------------------------
+
+def _w4_out(out, M, N, out_dtype, dev):
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("out_dtype must be bfloat16 or float32")
+    if out is None:
+        return torch.empty((M, N), dtype=out_dtype, device=dev)
+    _check_dev("out", out, out_dtype, dev)
+    if tuple(out.shape) != (M, N):
+        raise ValueError(f"out must be a contiguous [{M}, {N}] tensor")
+    return out
+
+
+def _w4_workspace(workspace, query, M, N, K, dev):
+    if isinstance(workspace, str):
+        if workspace != "auto":
+            raise ValueError("workspace must be 'auto', None or a float32 tensor")
+        nbytes = query(M, N, K)
+        workspace = torch.empty(nbytes // 4, dtype=torch.float32, device=dev) if nbytes else None
+    if workspace is None:
+        return 0, 0, None
+    _check_dev("workspace", workspace, torch.float32, dev)
+    return _p(workspace), workspace.numel() * 4, workspace
+
+
+def _w4_query(fn, M, N, K):
+    n = int(fn(M, N, K))
+    if n < 0:
+        raise FocusError(4, "the device query of the split model failed")
+    return n
+
+
+def mxfp4_linear_workspace_bytes(M: int, N: int, K: int) -> int:
+    """Workspace bytes for ``mxfp4_linear`` to split the sum over k (0: none)."""
+    return _w4_query(_lib.lib().focus_mxfp4_linear_workspace_bytes, M, N, K)
+
+
+def mxfp4_linear(x: Quantized, w: Quantized, out_dtype: torch.dtype = torch.bfloat16,
+                 out: Optional[torch.Tensor] = None, workspace="auto") -> torch.Tensor:
+    """Y = X' W'^T for MXFP8 activations ``x`` (codes [M, K], scales [M, K/32])
+    and MXFP4 weights ``w`` (codes [N, K/2], scales [N, K/32]) on the matrix
+    cores; Y [M, N] in ``out_dtype`` (bfloat16 or float32).  ``workspace`` as
+    for ``nvfp4_linear``."""
+    _check_dev("x.codes", x.codes, torch.uint8)
+    dev = x.codes.device
+    for name, t in (("x.scales", x.scales), ("w.codes", w.codes), ("w.scales", w.scales)):
+        _check_dev(name, t, torch.uint8, dev)
+    if x.codes.dim() != 2 or w.codes.dim() != 2:
+        raise ValueError("x.codes must be [M, K] and w.codes [N, K/2]")
+    M, K = x.codes.shape
+    N = w.codes.shape[0]
+    if K % 32 or w.codes.shape[1] * 2 != K or x.scales.shape != (M, K // 32) or w.scales.shape != (N, K // 32):
+        raise ValueError("operand shapes do not match: x [M, K], w [N, K] with K % 32 == 0")
+    y = _w4_out(out, M, N, out_dtype, dev)
+    ws, nbytes, keep = _w4_workspace(workspace, mxfp4_linear_workspace_bytes, M, N, K, dev)
+    _launch(_lib.lib().focus_mxfp4_linear, dev, _p(x.codes), _p(x.scales), M, _p(w.codes), _p(w.scales), N, K, _p(y),
+            0 if out_dtype == torch.float32 else 1, ws, nbytes)
+    return y
+
+
+def w4a16_linear_workspace_bytes(M: int, N: int, K: int) -> int:
+    """Workspace bytes for ``w4a16_linear`` to split the sum over k (0: none)."""
+    return _w4_query(_lib.lib().focus_w4a16_linear_workspace_bytes, M, N, K)
+
+
+def w4a16_linear(x: torch.Tensor, w: Quantized, out_dtype: torch.dtype = torch.bfloat16,
+                 out: Optional[torch.Tensor] = None, workspace="auto") -> torch.Tensor:
+    """Y = X W'^T for BF16 activations X [M, K] and 4-bit weights ``w``: NVFP4
+    (codes [N, K/2], scales [N, K/16], one s2; K % 16 == 0) or, where ``w.s2``
+    is None, MXFP4 (scales [N, K/32]; K % 32 == 0).  Y [M, N] in ``out_dtype``
+    (bfloat16 or float32).  ``workspace`` as for ``nvfp4_linear``."""
+    _check_dev("x", x, torch.bfloat16)
+    dev = x.device
+    _check_dev("w.codes", w.codes, torch.uint8, dev)
+    _check_dev("w.scales", w.scales, torch.uint8, dev)
+    if x.dim() != 2 or w.codes.dim() != 2:
+        raise ValueError("x must be [M, K] and w.codes [N, K/2]")
+    M, K = x.shape
+    N = w.codes.shape[0]
+    block = 32 if w.s2 is None else 16
+    if K % block or w.codes.shape[1] * 2 != K or w.scales.shape != (N, K // block):
+        raise ValueError(f"operand shapes do not match: x [M, K], w [N, K] with K % {block} == 0")
+    if w.s2 is not None:
+        _check_dev("w.s2", w.s2, torch.float32, dev)
+        if w.s2.numel() != 1:
+            raise ValueError("w.s2 must hold one float")
+    y = _w4_out(out, M, N, out_dtype, dev)
+    ws, nbytes, keep = _w4_workspace(workspace, w4a16_linear_workspace_bytes, M, N, K, dev)
+    _launch(_lib.lib().focus_w4a16_linear, dev, _p(x), M, 1 if w.s2 is None else 0, _p(w.codes), _p(w.scales),
+            _p(w.s2), N, K, _p(y), 0 if out_dtype == torch.float32 else 1, ws, nbytes)
+    return y
 
 
 # ---------------------------------------------------------------------------

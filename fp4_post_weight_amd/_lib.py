@@ -15,6 +15,7 @@ LIB_PATH = os.path.join(PKG, "libfocus_nvfp4.so")
 _VP = ct.c_void_p
 _I64 = ct.c_int64
 _INT = ct.c_int
+_F32 = ct.c_float
 
 class ScaleDesc(ct.Structure):
     _fields_ = [("w_bf16", _VP), ("numel", _I64), ("s2_out", _VP), ("amax_out", _VP)]
@@ -67,6 +68,17 @@ _SIGNATURES = {
     "focus_nvfp4_linear_noalloc": (_INT, [_VP, _VP, _VP, _INT, _I64, _VP, _VP, _VP, _I64, _I64, _VP, _INT,
                                           _VP]),
     "focus_nvfp4_linear_scratch_bytes": (_I64, []),
+    "focus_rmsnorm": (_INT, [_VP, _VP, _VP, _F32, _I64, _I64, _VP, _VP, _VP]),
+    "focus_rmsnorm_nvfp4": (_INT, [_VP, _VP, _VP, _F32, _I64, _I64, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "focus_rmsnorm_mxfp8": (_INT, [_VP, _VP, _VP, _F32, _I64, _I64, _VP, _VP, _VP, _VP, _VP]),
+    "focus_silu_mul": (_INT, [_VP, _I64, _VP, _I64, _I64, _I64, _VP, _VP]),
+    "focus_silu_mul_nvfp4": (_INT, [_VP, _I64, _VP, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP]),
+    "focus_silu_mul_mxfp8": (_INT, [_VP, _I64, _VP, _I64, _I64, _I64, _VP, _VP, _VP, _VP]),
+    "focus_quantize_mxfp8": (_INT, [_VP, _I64, _I64, _VP, _VP, _VP, _VP]),
+    "focus_mxfp4_linear": (_INT, [_VP, _VP, _I64, _VP, _VP, _I64, _I64, _VP, _INT, _VP, _I64, _VP]),
+    "focus_mxfp4_linear_workspace_bytes": (_I64, [_I64, _I64, _I64]),
+    "focus_w4a16_linear": (_INT, [_VP, _I64, _INT, _VP, _VP, _VP, _I64, _I64, _VP, _INT, _VP, _I64, _VP]),
+    "focus_w4a16_linear_workspace_bytes": (_I64, [_I64, _I64, _I64]),
 }
 
 EXPORTED = tuple(_SIGNATURES)

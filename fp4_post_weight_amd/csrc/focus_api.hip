@@ -2,7 +2,8 @@
 //
 // Every entry point validates all of its arguments on the host before the
 // first HIP call (so every error path runs without a GPU), then launches the
-// kernels of focus_kernels.hip on the caller's stream.  Nothing is allocated
+// kernels of focus_kernels.hip, focus_gemm.hip, focus_rows.hip and
+// focus_w4.hip on the caller's stream.  Nothing is allocated
 // and no state is kept.  Batched calls read their descriptor arrays during
 // the call only and launch one kernel (one per phase for the tensor scale)
 // per run of up to focus::kBatch tensors.  The declarations, with the
@@ -12,6 +13,8 @@
 #include "focus_nvfp4.h"
 #include "focus_gemm.h"
 #include "focus_internal.h"
+#include "focus_rows.h"
+#include "focus_w4.h"
 
 namespace {
 
@@ -540,5 +543,163 @@ int focus_nvfp4_linear_noalloc(const uint8_t* x_codes, const uint8_t* x_scales, 
     return run_linear(x_codes, x_scales, x_s2, x_s2_per_row, M, w_codes, w_scales, w_s2, N, K, y, y_dtype,
                       scratch, focus::kLinearScratchBytes, (hipStream_t)stream);
 }
+
+namespace {
+
+// hidden: a multiple of the output format's block; rows of at most 2^31.
+int check_rows(int64_t tokens, int64_t hidden, int64_t unit) {
+    if (tokens < 0 || hidden < 0 || hidden % unit != 0) return FOCUS_ERR_SHAPE;
+    if (tokens > kMaxTokens || hidden > kMaxTokens) return FOCUS_ERR_RANGE;
+    return FOCUS_OK;
+}
+
+constexpr int64_t row_unit(focus::RowOutput out) {
+    return out == focus::kRowBf16 ? 8 : out == focus::kRowNvfp4 ? 16 : 32;
+}
+
+// The output pointers of a row operator.
+int check_row_out(focus::RowOutput out, const focus::RowArgs& a) {
+    if (out == focus::kRowBf16) {
+        if (!a.y) return FOCUS_ERR_NULL;
+    } else if (!a.codes || !a.scales || (out == focus::kRowNvfp4 && !a.s2)) {
+        return FOCUS_ERR_NULL;
+    }
+    if (!aligned(a.codes, 8) || !aligned(a.s2, 4) || !aligned(a.y, 16)) return FOCUS_ERR_ALIGN;
+    return FOCUS_OK;
+}
+
+int run_norm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, float eps, int64_t tokens,
+             int64_t hidden, uint16_t* residual_out, focus::RowOutput out, uint8_t* codes, uint8_t* scales,
+             float* s2, uint16_t* y, void* stream) {
+    int st = check_rows(tokens, hidden, row_unit(out));
+    if (st != FOCUS_OK) return st;
+    if (!(eps > 0.0f) || eps > 3.4028234e38f || (residual_out && !residual)) return FOCUS_ERR_RANGE;
+    if (tokens == 0 || hidden == 0) return FOCUS_OK;
+    const focus::RowArgs a = {x,   residual, weight, hidden, hidden, residual_out, eps, tokens, hidden,
+                              codes, scales, s2,     y};
+    if (!x || !weight) return FOCUS_ERR_NULL;
+    st = check_row_out(out, a);
+    if (st != FOCUS_OK) return st;
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(residual_out, 16))
+        return FOCUS_ERR_ALIGN;
+    return hip_status(focus::launch_rows(a, focus::kRowNorm, out, (hipStream_t)stream));
+}
+
+int run_silu(const uint16_t* gate, int64_t gate_stride, const uint16_t* up, int64_t up_stride, int64_t tokens,
+             int64_t hidden, focus::RowOutput out, uint8_t* codes, uint8_t* scales, float* s2, uint16_t* y,
+             void* stream) {
+    int st = check_rows(tokens, hidden, row_unit(out));
+    if (st != FOCUS_OK) return st;
+    if (gate_stride < hidden || up_stride < hidden || gate_stride % 8 != 0 || up_stride % 8 != 0)
+        return FOCUS_ERR_SHAPE;
+    if (tokens == 0 || hidden == 0) return FOCUS_OK;
+    if (gate_stride > kMaxElems / tokens || up_stride > kMaxElems / tokens) return FOCUS_ERR_SHAPE;
+    const focus::RowArgs a = {gate,  up,     nullptr, gate_stride, up_stride, nullptr, 0.0f, tokens, hidden,
+                              codes, scales, s2,      y};
+    if (!gate || !up) return FOCUS_ERR_NULL;
+    st = check_row_out(out, a);
+    if (st != FOCUS_OK) return st;
+    if (!aligned(gate, 16) || !aligned(up, 16)) return FOCUS_ERR_ALIGN;
+    if (out == focus::kRowNvfp4) return hip_status(focus::launch_rows(a, focus::kRowSilu, out, (hipStream_t)stream));
+    return hip_status(focus::launch_flat(a, focus::kRowSilu, out, (hipStream_t)stream));
+}
+
+}  // namespace
+
+int focus_rmsnorm(const uint16_t* x_bf16, const uint16_t* residual, const uint16_t* weight, float eps,
+                  int64_t tokens, int64_t hidden, uint16_t* residual_out, uint16_t* y, void* stream) {
+    return run_norm(x_bf16, residual, weight, eps, tokens, hidden, residual_out, focus::kRowBf16, nullptr, nullptr,
+                    nullptr, y, stream);
+}
+
+int focus_rmsnorm_nvfp4(const uint16_t* x_bf16, const uint16_t* residual, const uint16_t* weight, float eps,
+                        int64_t tokens, int64_t hidden, uint16_t* residual_out, uint8_t* codes, uint8_t* scales,
+                        float* s2_out, uint16_t* y_deq, void* stream) {
+    return run_norm(x_bf16, residual, weight, eps, tokens, hidden, residual_out, focus::kRowNvfp4, codes, scales,
+                    s2_out, y_deq, stream);
+}
+
+int focus_rmsnorm_mxfp8(const uint16_t* x_bf16, const uint16_t* residual, const uint16_t* weight, float eps,
+                        int64_t tokens, int64_t hidden, uint16_t* residual_out, uint8_t* codes, uint8_t* scales,
+                        uint16_t* y_deq, void* stream) {
+    return run_norm(x_bf16, residual, weight, eps, tokens, hidden, residual_out, focus::kRowMxfp8, codes, scales,
+                    nullptr, y_deq, stream);
+}
+
+int focus_silu_mul(const uint16_t* gate, int64_t gate_stride, const uint16_t* up, int64_t up_stride, int64_t tokens,
+                   int64_t hidden, uint16_t* y, void* stream) {
+    return run_silu(gate, gate_stride, up, up_stride, tokens, hidden, focus::kRowBf16, nullptr, nullptr, nullptr, y,
+                    stream);
+}
+
+int focus_silu_mul_nvfp4(const uint16_t* gate, int64_t gate_stride, const uint16_t* up, int64_t up_stride,
+                         int64_t tokens, int64_t hidden, uint8_t* codes, uint8_t* scales, float* s2_out,
+                         uint16_t* y_deq, void* stream) {
+    return run_silu(gate, gate_stride, up, up_stride, tokens, hidden, focus::kRowNvfp4, codes, scales, s2_out, y_deq,
+                    stream);
+}
+
+int focus_silu_mul_mxfp8(const uint16_t* gate, int64_t gate_stride, const uint16_t* up, int64_t up_stride,
+                         int64_t tokens, int64_t hidden, uint8_t* codes, uint8_t* scales, uint16_t* y_deq,
+                         void* stream) {
+    return run_silu(gate, gate_stride, up, up_stride, tokens, hidden, focus::kRowMxfp8, codes, scales, nullptr, y_deq,
+                    stream);
+}
+
+int focus_quantize_mxfp8(const uint16_t* x_bf16, int64_t tokens, int64_t hidden, uint8_t* codes, uint8_t* scales,
+                         uint16_t* x_deq, void* stream) {
+    int st = check_rows(tokens, hidden, 32);
+    if (st != FOCUS_OK) return st;
+    if (tokens == 0 || hidden == 0) return FOCUS_OK;
+    const focus::RowArgs a = {x_bf16, nullptr, nullptr, hidden, 0, nullptr, 0.0f, tokens, hidden, codes, scales, nullptr, x_deq};
+    if (!x_bf16) return FOCUS_ERR_NULL;
+    st = check_row_out(focus::kRowMxfp8, a);
+    if (st != FOCUS_OK) return st;
+    if (!aligned(x_bf16, 16)) return FOCUS_ERR_ALIGN;
+    return hip_status(focus::launch_flat(a, focus::kRowPlain, focus::kRowMxfp8, (hipStream_t)stream));
+}
+
+namespace {
+
+// One launch's grid holds every column tile of a row of tiles.
+constexpr int64_t kMaxW4N = (int64_t)1 << 26;
+
+int run_w4(const focus::W4Args& a, focus::W4Kind kind, int64_t unit, int y_dtype, const float* workspace,
+           int64_t workspace_bytes, void* stream) {
+    if (a.M < 0 || a.N < 0 || a.K < 0 || a.K % unit != 0) return FOCUS_ERR_SHAPE;
+    if (a.M > kMaxTokens || a.K > kMaxTokens || a.N > kMaxW4N) return FOCUS_ERR_RANGE;
+    if ((y_dtype != 0 && y_dtype != 1) || workspace_bytes < 0) return FOCUS_ERR_RANGE;
+    if (a.M == 0 || a.N == 0) return FOCUS_OK;
+    if (!a.y || (a.K > 0 && (!a.x || !a.wc || !a.ws || (kind == focus::kW4Mx && !a.xs))) ||
+        (kind == focus::kW4Bf16Nvfp4 && !a.ws2))
+        return FOCUS_ERR_NULL;
+    if (!aligned(a.x, 16) || !aligned(a.wc, 16) || !aligned(a.ws2, 4) || !aligned(a.y, y_dtype == 0 ? 4 : 2) ||
+        !aligned(workspace, 16))
+        return FOCUS_ERR_ALIGN;
+    return hip_status(focus::launch_w4_linear(a, kind, y_dtype == 1, (hipStream_t)stream));
+}
+
+}  // namespace
+
+int focus_mxfp4_linear(const uint8_t* x_codes, const uint8_t* x_scales, int64_t M, const uint8_t* w_codes,
+                       const uint8_t* w_scales, int64_t N, int64_t K, void* y, int y_dtype, float* workspace,
+                       int64_t workspace_bytes, void* stream) {
+    const focus::W4Args a = {x_codes, x_scales, M, w_codes, w_scales, nullptr, N, K, y};
+    return run_w4(a, focus::kW4Mx, 32, y_dtype, workspace, workspace_bytes, stream);
+}
+
+int focus_w4a16_linear(const uint16_t* x_bf16, int64_t M, int w_format, const uint8_t* w_codes,
+                       const uint8_t* w_scales, const float* w_s2, int64_t N, int64_t K, void* y, int y_dtype,
+                       float* workspace, int64_t workspace_bytes, void* stream) {
+    if (w_format != 0 && w_format != 1) return FOCUS_ERR_RANGE;
+    const focus::W4Args a = {reinterpret_cast<const uint8_t*>(x_bf16), nullptr, M, w_codes, w_scales,
+                             w_format == 0 ? w_s2 : nullptr, N, K, y};
+    return run_w4(a, w_format == 0 ? focus::kW4Bf16Nvfp4 : focus::kW4Bf16Mxfp4, w_format == 0 ? 16 : 32, y_dtype,
+                  workspace, workspace_bytes, stream);
+}
+
+int64_t focus_mxfp4_linear_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
+
+int64_t focus_w4a16_linear_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
 
 }  // extern "C"
