@@ -50,8 +50,7 @@ __all__ = ["tensor_scale", "quantize", "dequantize", "quantize_act_per_token", "
            "nvfp4_linear_workspace_bytes", "nvfp4_linear_grouped", "nvfp4_linear_noalloc", "nvfp4_linear_scratch_bytes",
            "quantize_mx", "quantize_mx_many", "dequantize_mx",
            "rmsnorm", "rmsnorm_nvfp4", "rmsnorm_mxfp8", "silu_mul", "silu_mul_nvfp4", "silu_mul_mxfp8",
-           "quantize_mxfp8", "mxfp4_linear", "mxfp4_linear_workspace_bytes", "w4a16_linear",
-           "w4a16_linear_workspace_bytes",
+           "quantize_mxfp8", "mxfp4_linear", "w4a16_linear",
            "tensor_scale_many", "quantize_many", "dequantize_many", "Batch",
            "FocusError", "FocusLibraryMissing", "abi_version", "status_string", "library_path"]
 
@@ -762,36 +761,11 @@ def _w4_out(out, M, N, out_dtype, dev):
     return out
 
 
-def _w4_workspace(workspace, query, M, N, K, dev):
-    if isinstance(workspace, str):
-        if workspace != "auto":
-            raise ValueError("workspace must be 'auto', None or a float32 tensor")
-        nbytes = query(M, N, K)
-        workspace = torch.empty(nbytes // 4, dtype=torch.float32, device=dev) if nbytes else None
-    if workspace is None:
-        return 0, 0, None
-    _check_dev("workspace", workspace, torch.float32, dev)
-    return _p(workspace), workspace.numel() * 4, workspace
-
-
-def _w4_query(fn, M, N, K):
-    n = int(fn(M, N, K))
-    if n < 0:
-        raise FocusError(4, "the device query of the split model failed")
-    return n
-
-
-def mxfp4_linear_workspace_bytes(M: int, N: int, K: int) -> int:
-    """Workspace bytes for ``mxfp4_linear`` to split the sum over k (0: none)."""
-    return _w4_query(_lib.lib().focus_mxfp4_linear_workspace_bytes, M, N, K)
-
-
 def mxfp4_linear(x: Quantized, w: Quantized, out_dtype: torch.dtype = torch.bfloat16,
-                 out: Optional[torch.Tensor] = None, workspace="auto") -> torch.Tensor:
+                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Y = X' W'^T for MXFP8 activations ``x`` (codes [M, K], scales [M, K/32])
     and MXFP4 weights ``w`` (codes [N, K/2], scales [N, K/32]) on the matrix
-    cores; Y [M, N] in ``out_dtype`` (bfloat16 or float32).  ``workspace`` as
-    for ``nvfp4_linear``."""
+    cores; Y [M, N] in ``out_dtype`` (bfloat16 or float32)."""
     _check_dev("x.codes", x.codes, torch.uint8)
     dev = x.codes.device
     for name, t in (("x.scales", x.scales), ("w.codes", w.codes), ("w.scales", w.scales)):
@@ -803,23 +777,17 @@ def mxfp4_linear(x: Quantized, w: Quantized, out_dtype: torch.dtype = torch.bflo
     if K % 32 or w.codes.shape[1] * 2 != K or x.scales.shape != (M, K // 32) or w.scales.shape != (N, K // 32):
         raise ValueError("operand shapes do not match: x [M, K], w [N, K] with K % 32 == 0")
     y = _w4_out(out, M, N, out_dtype, dev)
-    ws, nbytes, keep = _w4_workspace(workspace, mxfp4_linear_workspace_bytes, M, N, K, dev)
     _launch(_lib.lib().focus_mxfp4_linear, dev, _p(x.codes), _p(x.scales), M, _p(w.codes), _p(w.scales), N, K, _p(y),
-            0 if out_dtype == torch.float32 else 1, ws, nbytes)
+            0 if out_dtype == torch.float32 else 1)
     return y
 
 
-def w4a16_linear_workspace_bytes(M: int, N: int, K: int) -> int:
-    """Workspace bytes for ``w4a16_linear`` to split the sum over k (0: none)."""
-    return _w4_query(_lib.lib().focus_w4a16_linear_workspace_bytes, M, N, K)
-
-
 def w4a16_linear(x: torch.Tensor, w: Quantized, out_dtype: torch.dtype = torch.bfloat16,
-                 out: Optional[torch.Tensor] = None, workspace="auto") -> torch.Tensor:
+                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Y = X W'^T for BF16 activations X [M, K] and 4-bit weights ``w``: NVFP4
     (codes [N, K/2], scales [N, K/16], one s2; K % 16 == 0) or, where ``w.s2``
     is None, MXFP4 (scales [N, K/32]; K % 32 == 0).  Y [M, N] in ``out_dtype``
-    (bfloat16 or float32).  ``workspace`` as for ``nvfp4_linear``."""
+    (bfloat16 or float32)."""
     _check_dev("x", x, torch.bfloat16)
     dev = x.device
     _check_dev("w.codes", w.codes, torch.uint8, dev)
@@ -836,9 +804,8 @@ def w4a16_linear(x: torch.Tensor, w: Quantized, out_dtype: torch.dtype = torch.b
         if w.s2.numel() != 1:
             raise ValueError("w.s2 must hold one float")
     y = _w4_out(out, M, N, out_dtype, dev)
-    ws, nbytes, keep = _w4_workspace(workspace, w4a16_linear_workspace_bytes, M, N, K, dev)
     _launch(_lib.lib().focus_w4a16_linear, dev, _p(x), M, 1 if w.s2 is None else 0, _p(w.codes), _p(w.scales),
-            _p(w.s2), N, K, _p(y), 0 if out_dtype == torch.float32 else 1, ws, nbytes)
+            _p(w.s2), N, K, _p(y), 0 if out_dtype == torch.float32 else 1)
     return y
 
 

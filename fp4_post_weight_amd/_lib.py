@@ -75,10 +75,8 @@ _SIGNATURES = {
     "focus_silu_mul_nvfp4": (_INT, [_VP, _I64, _VP, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP]),
     "focus_silu_mul_mxfp8": (_INT, [_VP, _I64, _VP, _I64, _I64, _I64, _VP, _VP, _VP, _VP]),
     "focus_quantize_mxfp8": (_INT, [_VP, _I64, _I64, _VP, _VP, _VP, _VP]),
-    "focus_mxfp4_linear": (_INT, [_VP, _VP, _I64, _VP, _VP, _I64, _I64, _VP, _INT, _VP, _I64, _VP]),
-    "focus_mxfp4_linear_workspace_bytes": (_I64, [_I64, _I64, _I64]),
-    "focus_w4a16_linear": (_INT, [_VP, _I64, _INT, _VP, _VP, _VP, _I64, _I64, _VP, _INT, _VP, _I64, _VP]),
-    "focus_w4a16_linear_workspace_bytes": (_I64, [_I64, _I64, _I64]),
+    "focus_mxfp4_linear": (_INT, [_VP, _VP, _I64, _VP, _VP, _I64, _I64, _VP, _INT, _VP]),
+    "focus_w4a16_linear": (_INT, [_VP, _I64, _INT, _VP, _VP, _VP, _I64, _I64, _VP, _INT, _VP]),
 }
 
 EXPORTED = tuple(_SIGNATURES)

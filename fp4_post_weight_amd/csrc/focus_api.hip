@@ -664,17 +664,15 @@ namespace {
 // One launch's grid holds every column tile of a row of tiles.
 constexpr int64_t kMaxW4N = (int64_t)1 << 26;
 
-int run_w4(const focus::W4Args& a, focus::W4Kind kind, int64_t unit, int y_dtype, const float* workspace,
-           int64_t workspace_bytes, void* stream) {
+int run_w4(const focus::W4Args& a, focus::W4Kind kind, int64_t unit, int y_dtype, void* stream) {
     if (a.M < 0 || a.N < 0 || a.K < 0 || a.K % unit != 0) return FOCUS_ERR_SHAPE;
-    if (a.M > kMaxTokens || a.K > kMaxTokens || a.N > kMaxW4N) return FOCUS_ERR_RANGE;
-    if ((y_dtype != 0 && y_dtype != 1) || workspace_bytes < 0) return FOCUS_ERR_RANGE;
+    if (a.M > kMaxTokens || a.K > focus::kMaxW4K || a.N > kMaxW4N) return FOCUS_ERR_RANGE;
+    if (y_dtype != 0 && y_dtype != 1) return FOCUS_ERR_RANGE;
     if (a.M == 0 || a.N == 0) return FOCUS_OK;
     if (!a.y || (a.K > 0 && (!a.x || !a.wc || !a.ws || (kind == focus::kW4Mx && !a.xs))) ||
         (kind == focus::kW4Bf16Nvfp4 && !a.ws2))
         return FOCUS_ERR_NULL;
-    if (!aligned(a.x, 16) || !aligned(a.wc, 16) || !aligned(a.ws2, 4) || !aligned(a.y, y_dtype == 0 ? 4 : 2) ||
-        !aligned(workspace, 16))
+    if (!aligned(a.x, 16) || !aligned(a.wc, 16) || !aligned(a.ws2, 4) || !aligned(a.y, y_dtype == 0 ? 4 : 2))
         return FOCUS_ERR_ALIGN;
     return hip_status(focus::launch_w4_linear(a, kind, y_dtype == 1, (hipStream_t)stream));
 }
@@ -682,24 +680,19 @@ int run_w4(const focus::W4Args& a, focus::W4Kind kind, int64_t unit, int y_dtype
 }  // namespace
 
 int focus_mxfp4_linear(const uint8_t* x_codes, const uint8_t* x_scales, int64_t M, const uint8_t* w_codes,
-                       const uint8_t* w_scales, int64_t N, int64_t K, void* y, int y_dtype, float* workspace,
-                       int64_t workspace_bytes, void* stream) {
+                       const uint8_t* w_scales, int64_t N, int64_t K, void* y, int y_dtype, void* stream) {
     const focus::W4Args a = {x_codes, x_scales, M, w_codes, w_scales, nullptr, N, K, y};
-    return run_w4(a, focus::kW4Mx, 32, y_dtype, workspace, workspace_bytes, stream);
+    return run_w4(a, focus::kW4Mx, 32, y_dtype, stream);
 }
 
 int focus_w4a16_linear(const uint16_t* x_bf16, int64_t M, int w_format, const uint8_t* w_codes,
                        const uint8_t* w_scales, const float* w_s2, int64_t N, int64_t K, void* y, int y_dtype,
-                       float* workspace, int64_t workspace_bytes, void* stream) {
+                       void* stream) {
     if (w_format != 0 && w_format != 1) return FOCUS_ERR_RANGE;
     const focus::W4Args a = {reinterpret_cast<const uint8_t*>(x_bf16), nullptr, M, w_codes, w_scales,
                              w_format == 0 ? w_s2 : nullptr, N, K, y};
     return run_w4(a, w_format == 0 ? focus::kW4Bf16Nvfp4 : focus::kW4Bf16Mxfp4, w_format == 0 ? 16 : 32, y_dtype,
-                  workspace, workspace_bytes, stream);
+                  stream);
 }
-
-int64_t focus_mxfp4_linear_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
-
-int64_t focus_w4a16_linear_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
 
 }  // extern "C"

@@ -24,6 +24,9 @@ struct W4Args {
     void* y;             // [M, N] FP32 or BF16
 };
 
+// Largest K: a workgroup's rows (at most 256) are addressed by 32-bit offsets.
+constexpr int64_t kMaxW4K = (int64_t)1 << 22;
+
 hipError_t launch_w4_linear(const W4Args& a, W4Kind kind, bool bf16_out, hipStream_t stream);
 
 }  // namespace focus

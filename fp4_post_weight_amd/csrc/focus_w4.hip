@@ -31,6 +31,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "focus_gemm.h"
 #include "focus_launch.h"
 #include "focus_numerics.h"
 #include "focus_w4.h"
@@ -58,7 +59,7 @@ __device__ __forceinline__ uint32_t ld4_a1(const uint8_t* p) { return *reinterpr
 
 // 16 code bytes whose first code is k, of a row that ends at K (K % 16 == 0):
 // absent codes are zeros.
-__device__ __forceinline__ uint4 codes_until(const uint8_t* p, int64_t k, int64_t K) {
+__device__ __forceinline__ uint4 codes_until(const uint8_t* p, int k, int K) {
     uint4 v = make_uint4(0, 0, 0, 0);
     if (k + 32 <= K) {
         v = ld16_a8(p);
@@ -72,7 +73,7 @@ __device__ __forceinline__ uint4 codes_until(const uint8_t* p, int64_t k, int64_
 
 // Four scale bytes of blocks b, b+1, ... of a row of nb: absent ones are
 // `one`, the byte of scale 1.
-__device__ __forceinline__ uint32_t scales_until(const uint8_t* p, int64_t b, int64_t nb, uint32_t one) {
+__device__ __forceinline__ uint32_t scales_until(const uint8_t* p, int b, int nb, uint32_t one) {
     if (b + 4 <= nb) return ld4_a1(p);
     uint32_t v = 0;
 #pragma unroll
@@ -89,6 +90,10 @@ __device__ __forceinline__ f32x4 mfma_mx(const uint4& lo, const uint4& hi, const
 }
 
 __device__ __forceinline__ uint32_t pick(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+// E4M3 and E8M0 (0..254) scale values of the low byte of v.
+__device__ __forceinline__ float e4m3_f32(uint32_t v) { return __builtin_amdgcn_cvt_f32_fp8((int)v, 0); }
+__device__ __forceinline__ float e8m0_f32(uint32_t v) { return __uint_as_float(max((v & 0xFFu) << 23, 0x00400000u)); }
 
 // Eight MXFP4 codes times the scale S (a power of two), in BF16.
 __device__ __forceinline__ bf16x8 widen_mx(uint32_t c, float S) {
@@ -110,51 +115,78 @@ __device__ __forceinline__ bf16x8 widen_nv(uint32_t c, float S) {
     return __builtin_bit_cast(bf16x8, v);
 }
 
+// Loads take a uniform address and a 32-bit offset of the lane (K <= kMaxW4K,
+// and a workgroup's rows are at most 128).  MASK: the last step, of which only
+// the first `left` < kStep values of k exist.
+
 // One wavefront step's W: 4 T row pieces as loaded, and the scale bytes of
 // the lane's blocks (4 of 32 elements, or 8 of 16).
 template <int KIND, int T>
 struct StepW {
+    static constexpr bool kNv = KIND == kW4Bf16Nvfp4;
+    static constexpr int kDwords = kNv ? 2 : 1;  // of scale bytes per lane
     uint4 c[4 * T];
-    uint32_t s[T][KIND == kW4Bf16Nvfp4 ? 2 : 1];
+    uint32_t s[T][kDwords];
+
+    template <bool MASK>
+    __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales, const uint32_t (&coff)[4 * T],
+                                         const uint32_t (&soff)[T], int left, int lane) {
+#pragma unroll
+        for (int r = 0; r < 4 * T; ++r) c[r] = MASK ? codes_until(codes + coff[r], 32 * (lane & 15), left) : ld16_a8(codes + coff[r]);
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+#pragma unroll
+            for (int i = 0; i < kDwords; ++i)
+                s[t][i] = MASK ? scales_until(scales + soff[t] + 4 * i, 4 * (kDwords * (lane >> 4) + i), left / (kNv ? 16 : 32),
+                                              kNv ? 0x38u : 127u)
+                               : ld4_a1(scales + soff[t] + 4 * i);
+    }
 };
 
-template <int KIND, int T>
-__device__ __forceinline__ void load_w(StepW<KIND, T>& o, const W4Args& a, int64_t n0, int64_t k0, int lane) {
-    constexpr bool kNv = KIND == kW4Bf16Nvfp4;
-    const int c16 = lane & 15, g = lane >> 4;
-    const bool whole = k0 + kStep <= a.K;
+// X fragments of a quarter step (quarter j: the lane's W piece j, 32 codes):
+// 2 pieces of 16 bytes per token tile for MXFP8, 4 for BF16.
+//
+// MXFP8: logical block b of product j is block 4 b + j of the step.  A lane's
+// halves of the X row are logical k 16 g.. and 64 + 16 g.., i.e. half g % 2 of
+// logical blocks g / 2 and 2 + g / 2.  BF16: product 4 j + i takes
+// k = 128 g + 32 j + 8 i .. + 7 in lane group g.
+template <int KIND, int MT>
+struct QuarterX {
+    static constexpr bool kMx = KIND == kW4Mx;
+    static constexpr int kPieces = kMx ? 2 : 4, kEach = kMx ? 256 : 8;  // k from piece to piece
+    uint4 v[MT][kPieces];
+
+    // the lane's first k within a step
+    static __device__ __forceinline__ int first(int g) { return kMx ? 128 * (g >> 1) + 16 * (g & 1) : 128 * g; }
+
+    // off: of the row, plus the lane's first k, in bytes
+    template <bool MASK>
+    __device__ __forceinline__ void load(const uint8_t* x, const uint32_t (&off)[MT], int j, int left, int g) {
 #pragma unroll
-    for (int r = 0; r < 4 * T; ++r) {
-        const int64_t row = n0 + 4 * r + g;
-        const int64_t k = k0 + 32 * c16;
-        const uint8_t* p = a.wc + (row < a.N ? row : a.N - 1) * (a.K / 2) + k / 2;
-        o.c[r] = whole ? ld16_a8(p) : codes_until(p, k, a.K);
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                if (MASK) v[m][i] = make_uint4(0, 0, 0, 0);
+                if (!MASK || first(g) + 32 * j + kEach * i < left)
+                    v[m][i] = *reinterpret_cast<const uint4*>(x + off[m] + (kMx ? 1 : 2) * (32 * j + kEach * i));
+            }
     }
-#pragma unroll
-    for (int t = 0; t < T; ++t) {
-        const int64_t row = n0 + 16 * t + c16;
-        const int64_t rr = row < a.N ? row : a.N - 1;
-        constexpr int kPer = kNv ? 8 : 4;  // scale bytes per lane
-        const int64_t nb = a.K / (kNv ? 16 : 32), b = k0 / (kNv ? 16 : 32) + kPer * g;
-        const uint8_t* p = a.ws + rr * nb + b;
-#pragma unroll
-        for (int i = 0; i < (kNv ? 2 : 1); ++i)
-            o.s[t][i] = whole ? ld4_a1(p + 4 * i) : scales_until(p + 4 * i, b + 4 * i, nb, kNv ? 0x38u : 127u);
-    }
-}
+};
 
 template <int KIND, bool BF16_OUT, int WAVES, int T, int MT>
 __global__ __launch_bounds__(64 * WAVES) void k_w4_decode(W4Args a, int64_t tiles_n) {
     constexpr bool kMx = KIND == kW4Mx, kNv = KIND == kW4Bf16Nvfp4;
+    constexpr int kScaleDwords = StepW<KIND, T>::kDwords;
     constexpr int kStage = WAVES * 16 * T * kStageRow;
     constexpr int kRed = WAVES * MT * T * 256 * 4;
     __shared__ __attribute__((aligned(16))) uint8_t lds[kRed > kStage ? kRed : kStage];
     float(*red)[MT * T * 256] = reinterpret_cast<float(*)[MT * T * 256]>(lds);
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c16 = lane & 15, g = lane >> 4;
     const int64_t n0 = ((int64_t)blockIdx.x % tiles_n) * (16 * T);
     const int64_t m0 = ((int64_t)blockIdx.x / tiles_n) * (16 * MT);
-    const int64_t nsteps = (a.K + kStep - 1) / kStep;
+    const int K = (int)a.K, full = K / kStep;
 
     f32x4 acc[MT][T];
 #pragma unroll
@@ -162,94 +194,120 @@ __global__ __launch_bounds__(64 * WAVES) void k_w4_decode(W4Args a, int64_t tile
 #pragma unroll
         for (int t = 0; t < T; ++t) acc[m][t] = (f32x4){};
 
-    int64_t xrow[MT];
+    // Rows past an operand's end read its last row and feed outputs that are
+    // never stored.
+    const int mlast = (int)(a.M - 1 - m0 < 16 * MT ? a.M - 1 - m0 : 16 * MT);
+    const int nlast = (int)(a.N - 1 - n0 < 16 * T ? a.N - 1 - n0 : 16 * T);
+    const int nb = K / (kNv ? 16 : 32);
+    const uint8_t* xb = a.x + m0 * K * (kMx ? 1 : 2);
+    const uint8_t* xsb = a.xs + m0 * nb;
+    const uint8_t* wb = a.wc + n0 * (K / 2);
+    const uint8_t* wsb = a.ws + n0 * nb;
+    uint32_t xoff[MT], xsoff[MT], coff[4 * T], soff[T];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-        const int64_t row = m0 + 16 * m + c16;
-        xrow[m] = row < a.M ? row : a.M - 1;  // such rows feed outputs that are never stored
+        const uint32_t row = (uint32_t)min(16 * m + c16, mlast);
+        xoff[m] = (row * (uint32_t)K + QuarterX<KIND, MT>::first(g)) * (kMx ? 1 : 2);
+        xsoff[m] = row * (uint32_t)nb + 4 * g;
     }
+#pragma unroll
+    for (int r = 0; r < 4 * T; ++r) coff[r] = (uint32_t)min(4 * r + g, nlast) * (uint32_t)(K / 2) + 16 * c16;
+#pragma unroll
+    for (int t = 0; t < T; ++t) soff[t] = (uint32_t)min(16 * t + c16, nlast) * (uint32_t)nb + (kNv ? 8 : 4) * g;
+
     uint8_t* st = lds + wave * (16 * T * kStageRow);
     StepW<KIND, T> w;
-    if (wave < nsteps) load_w<KIND, T>(w, a, n0, (int64_t)wave * kStep, lane);
-    for (int64_t s = wave; s < nsteps; s += WAVES) {
-        const int64_t k0 = s * kStep;
-        const bool whole = k0 + kStep <= a.K;
-        uint32_t sc[T][kNv ? 2 : 1];
+    QuarterX<KIND, MT> x0, x1;
+    uint32_t sc[T][kScaleDwords], xsc[MT], xsn[MT];
+
+    auto load_w = [&](int s) {
+        w.template load<false>(wb + (int64_t)s * (kStep / 2), wsb + s * (kStep / (kNv ? 16 : 32)), coff, soff, 0, lane);
+        if (kMx) {
 #pragma unroll
-        for (int r = 0; r < 4 * T; ++r)
-            *reinterpret_cast<uint4*>(st + (4 * r + g) * kStageRow + 16 * c16) = w.c[r];
+            for (int m = 0; m < MT; ++m) xsn[m] = ld4_a1(xsb + s * (kStep / 32) + xsoff[m]);
+        }
+    };
+    auto xat = [&](int s) { return xb + (int64_t)s * kStep * (kMx ? 1 : 2); };
+    // W in registers -> the wavefront's LDS area, scales -> sc, xsc
+    auto stage_w = [&]() {
+#pragma unroll
+        for (int r = 0; r < 4 * T; ++r) *reinterpret_cast<uint4*>(st + (4 * r + g) * kStageRow + 16 * c16) = w.c[r];
 #pragma unroll
         for (int t = 0; t < T; ++t)
 #pragma unroll
-            for (int i = 0; i < (kNv ? 2 : 1); ++i) sc[t][i] = w.s[t][i];
+            for (int i = 0; i < kScaleDwords; ++i) sc[t][i] = w.s[t][i];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) xsc[m] = xsn[m];
         __builtin_amdgcn_wave_barrier();
-        if (s + WAVES < nsteps) load_w<KIND, T>(w, a, n0, (s + WAVES) * kStep, lane);
+    };
+    auto products = [&](auto jc, const QuarterX<KIND, MT>& x) {
+        constexpr int j = decltype(jc)::value;
+        uint4 wf[T];
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+            wf[t] = *reinterpret_cast<const uint4*>(st + (16 * t + c16) * kStageRow + 64 * g + 16 * j);
         if constexpr (kMx) {
-            uint32_t xsc[MT];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const int64_t nb = a.K / 32, b = k0 / 32 + 4 * g;
-                const uint8_t* p = a.xs + xrow[m] * nb + b;
-                xsc[m] = whole ? ld4_a1(p) : scales_until(p, b, nb, 127u);
-            }
-            // Logical block b of product j is block 4 b + j of the step.  A
-            // lane's X halves: logical k 16 g.. and 64 + 16 g.., i.e. half
-            // g % 2 of logical blocks g / 2 and 2 + g / 2.
-            auto product = [&](auto jc) {
-                constexpr int j = decltype(jc)::value;
-                uint4 wf[T];
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int t = 0; t < T; ++t)
-                    wf[t] = *reinterpret_cast<const uint4*>(st + (16 * t + c16) * kStageRow + 64 * g + 16 * j);
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    const int64_t k = k0 + 32 * (4 * (g >> 1) + j) + 16 * (g & 1);
-                    const uint8_t* p = a.x + xrow[m] * a.K + k;
-                    uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-                    if (whole || k < a.K) lo = *reinterpret_cast<const uint4*>(p);
-                    if (whole || k + 256 < a.K) hi = *reinterpret_cast<const uint4*>(p + 256);
-#pragma unroll
-                    for (int t = 0; t < T; ++t) acc[m][t] = mfma_mx<j>(lo, hi, wf[t], xsc[m], sc[t][0], acc[m][t]);
-                }
-            };
-            product(std::integral_constant<int, 0>{});
-            product(std::integral_constant<int, 1>{});
-            product(std::integral_constant<int, 2>{});
-            product(std::integral_constant<int, 3>{});
+                    acc[m][t] = mfma_mx<j>(x.v[m][0], x.v[m][1], wf[t], xsc[m], sc[t][0], acc[m][t]);
         } else {
-            // product i takes k = 128 g + 8 i .. + 7 of the step in lane group g
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint4 wf[T];
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int t = 0; t < T; ++t)
-                    wf[t] = *reinterpret_cast<const uint4*>(st + (16 * t + c16) * kStageRow + 64 * g + 16 * j);
+                for (int t = 0; t < T; ++t) {
+                    // the lane's 16-block 2 j + i / 2, or 32-block j
+                    const uint32_t byte = kNv ? sc[t][kNv ? j >> 1 : 0] >> (8 * (2 * (j & 1) + (i >> 1))) : sc[t][0] >> (8 * j);
+                    const bf16x8 wv = kNv ? widen_nv(pick(wf[t], i), e4m3_f32(byte))
+                                          : widen_mx(pick(wf[t], i), e8m0_f32(byte));
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int64_t k = k0 + 128 * g + 32 * j + 8 * i;
-                    bf16x8 wb[T];
-#pragma unroll
-                    for (int t = 0; t < T; ++t) {
-                        if (kNv) {
-                            const int b = 2 * j + (i >> 1);  // the lane's 16-block
-                            wb[t] = widen_nv(pick(wf[t], i), e4m3_any_value((sc[t][b >> 2 & (kNv ? 1 : 0)] >> (8 * (b & 3))) & 0xFFu));
-                        } else {
-                            wb[t] = widen_mx(pick(wf[t], i), e8m0_value((sc[t][0] >> (8 * j)) & 0xFFu));
-                        }
-                    }
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        uint4 xv = make_uint4(0, 0, 0, 0);
-                        if (whole || k < a.K) xv = *reinterpret_cast<const uint4*>(a.x + 2 * (xrow[m] * a.K + k));
-                        const bf16x8 xb = __builtin_bit_cast(bf16x8, xv);
-#pragma unroll
-                        for (int t = 0; t < T; ++t)
-                            acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb, wb[t], acc[m][t], 0, 0, 0);
-                    }
+                    for (int m = 0; m < MT; ++m)
+                        acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            __builtin_bit_cast(bf16x8, x.v[m][kMx ? 0 : i]), wv, acc[m][t], 0, 0, 0);
                 }
-            }
         }
+    };
+    constexpr std::integral_constant<int, 0> q0{};
+    constexpr std::integral_constant<int, 1> q1{};
+    constexpr std::integral_constant<int, 2> q2{};
+    constexpr std::integral_constant<int, 3> q3{};
+
+    if (wave < full) {
+        load_w(wave);
+        x0.template load<false>(xat(wave), xoff, 0, 0, g);
+    }
+    for (int s = wave; s < full; s += WAVES) {
+        const int sn = s + WAVES < full ? s + WAVES : s;  // the last step loads itself again
+        stage_w();
+        load_w(sn);
+        x1.template load<false>(xat(s), xoff, 1, 0, g);
+        products(q0, x0);
+        x0.template load<false>(xat(s), xoff, 2, 0, g);
+        products(q1, x1);
+        x1.template load<false>(xat(s), xoff, 3, 0, g);
+        products(q2, x0);
+        x0.template load<false>(xat(sn), xoff, 0, 0, g);
+        products(q3, x1);
         __builtin_amdgcn_wave_barrier();
+    }
+    const int left = K - full * kStep;
+    if (left > 0 && wave == full % WAVES) {
+        w.template load<true>(wb + (int64_t)full * (kStep / 2), wsb + full * (kStep / (kNv ? 16 : 32)), coff, soff, left, lane);
+        if (kMx) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                xsn[m] = scales_until(xsb + full * (kStep / 32) + xsoff[m], 4 * g, left / 32, 127u);
+        }
+        stage_w();
+        x0.template load<true>(xat(full), xoff, 0, left, g);
+        products(q0, x0);
+        x0.template load<true>(xat(full), xoff, 1, left, g);
+        products(q1, x0);
+        x0.template load<true>(xat(full), xoff, 2, left, g);
+        products(q2, x0);
+        x0.template load<true>(xat(full), xoff, 3, left, g);
+        products(q3, x0);
     }
 
     // register r of lane l in tile (m, t): token 16 m + 4 (l / 16) + r, column
@@ -277,16 +335,27 @@ __global__ __launch_bounds__(64 * WAVES) void k_w4_decode(W4Args a, int64_t tile
     }
 }
 
+// The call restricted to at most `most` token rows from `row` on.
+template <int KIND, bool BF16_OUT>
+W4Args rows_from(const W4Args& args, int64_t row, int64_t most) {
+    W4Args a = args;
+    a.M = args.M - row < most ? args.M - row : most;
+    a.x += row * a.K * (KIND == kW4Mx ? 1 : 2);
+    if (KIND == kW4Mx) a.xs += row * (a.K / 32);
+    a.y = reinterpret_cast<uint8_t*>(a.y) + row * a.N * (BF16_OUT ? 2 : 4);
+    return a;
+}
+
 // ---------------------------------------------------------------------------
-// MXFP8 x MXFP4 with many tokens: tiles of BM tokens x BN columns, k in steps
-// of 128, three stages in LDS.  Codes go from memory to LDS without passing
-// through registers (16 bytes per lane).  Rows are stored unpadded (the
-// transfer writes lane after lane) and their 16-byte pieces permuted by the
-// row, so that the fragment reads of 8 rows cover all banks: X row r holds
-// piece p at p ^ (r & 7) of 8, W row r at p ^ ((r >> 1) & 3) of 4; the
-// transferring lane picks its global address accordingly.  The scale bytes of
-// a row's step are one dword, loaded a step ahead into a register of the
-// thread that owns the row.
+// Many tokens: tiles of BM tokens x BN columns, k in steps of KS, three stages
+// in LDS.  Codes go from memory to LDS without passing through registers (16
+// bytes per lane).  Rows are stored unpadded (the transfer writes lane after
+// lane) and their 16-byte pieces permuted by the row, so that the fragment
+// reads of neighbouring rows cover all banks: piece p of row r lies at
+// p ^ (r mod the row's pieces, at most 16), in a 64-byte W row at
+// p ^ ((r >> 1) & 3); the transferring lane picks its global address
+// accordingly.  The scale bytes of a row's step are loaded a step ahead into a
+// register of the thread that owns the row.
 //
 // A step has two halves around its one barrier, which says that every
 // wavefront has left step s - 1 and that the data of step s + 1 are in LDS.
@@ -295,12 +364,13 @@ __global__ __launch_bounds__(64 * WAVES) void k_w4_decode(W4Args a, int64_t tile
 // fragments are read while the second half's products run, and X fragments
 // come `kAhead` subtiles ahead of their products throughout.
 //
+// Small tiles take long steps: what a step costs beside its products (the
+// barrier, the first fragments' latency, the transfer's instructions) is then
+// spread over more of k, and more bytes are on their way.
+//
 // W is the first operand of the product, so that a lane's four accumulators
 // are four neighbouring columns of one token.
 // ---------------------------------------------------------------------------
-
-constexpr int kTileK = 128;
-constexpr int64_t kMaxTileK = (int64_t)1 << 23;  // a tile's offsets fit 32 bits
 
 typedef __attribute__((address_space(3))) uint8_t lds_byte;
 
@@ -309,11 +379,11 @@ __device__ __forceinline__ uint32_t lds_address(const uint8_t* p) {
 }
 
 // 16 bytes per lane from base + offset to LDS at `dst` + 16 * lane (dst and
-// base uniform).  The instruction has no register result; it is complete
-// after wait_transfers().  Written out because the compiler, which cannot tell
-// the stages apart, would wait for every transfer before any LDS read.  m0
-// holds nothing of the compiler's here: no other instruction of these kernels
-// reads it.
+// base uniform).  The instruction has no register result, and its address
+// registers are read when it issues; it is complete after wait_transfers().
+// Written out because the compiler, which cannot tell the stages apart, would
+// wait for every transfer before any LDS read.  m0 holds nothing of the
+// compiler's here: no other instruction of these kernels reads it.
 __device__ __forceinline__ void to_lds16(const uint8_t* base, uint32_t offset, uint32_t dst) {
     asm volatile(
         "s_mov_b32 m0, %0\n\t"
@@ -326,8 +396,8 @@ __device__ __forceinline__ void to_lds16(const uint8_t* base, uint32_t offset, u
 
 __device__ __forceinline__ void wait_transfers() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
-// The product of W subtile j and X subtile i, whose scales are bytes j % 4 and
-// i % 4 of ws and xs.
+// The block-scaled product of W subtile j and X subtile i, whose scales are
+// bytes SW and SX of ws and xs.
 template <int SW, int SX>
 __device__ __forceinline__ f32x4 mfma_tile(const uint4& w, const uint4& lo, const uint4& hi, uint32_t ws, uint32_t xs,
                                            f32x4 acc) {
@@ -339,7 +409,7 @@ __device__ __forceinline__ f32x4 mfma_tile(const uint4& w, const uint4& lo, cons
 template <int SX>
 __device__ __forceinline__ f32x4 mfma_tile(int sw, const uint4& w, const uint4& lo, const uint4& hi, uint32_t ws,
                                            uint32_t xs, f32x4 acc) {
-    switch (sw & 3) {
+    switch (sw) {
         case 0: return mfma_tile<0, SX>(w, lo, hi, ws, xs, acc);
         case 1: return mfma_tile<1, SX>(w, lo, hi, ws, xs, acc);
         case 2: return mfma_tile<2, SX>(w, lo, hi, ws, xs, acc);
@@ -349,7 +419,7 @@ __device__ __forceinline__ f32x4 mfma_tile(int sw, const uint4& w, const uint4& 
 
 __device__ __forceinline__ f32x4 mfma_tile(int sw, int sx, const uint4& w, const uint4& lo, const uint4& hi,
                                            uint32_t ws, uint32_t xs, f32x4 acc) {
-    switch (sx & 3) {
+    switch (sx) {
         case 0: return mfma_tile<0>(sw, w, lo, hi, ws, xs, acc);
         case 1: return mfma_tile<1>(sw, w, lo, hi, ws, xs, acc);
         case 2: return mfma_tile<2>(sw, w, lo, hi, ws, xs, acc);
@@ -357,21 +427,11 @@ __device__ __forceinline__ f32x4 mfma_tile(int sw, int sx, const uint4& w, const
     }
 }
 
-// Scale byte of block g of a step, row r of an operand tile, in LDS: the bytes
-// of SUB rows 16 apart (SUB subtiles of one wavefront) are neighbours, so that
-// a lane reads them at once and the instruction selects one.
-template <int SUB>
-__device__ __forceinline__ int scale_at(int r, int g) {
-    return SUB * (((r / (16 * SUB)) * 16 + (r & 15)) * 4 + g) + (r >> 4) % SUB;
-}
-
-template <int SUB>
-__device__ __forceinline__ uint32_t read_scales(const uint8_t* base, int r, int g) {
-    const uint8_t* p = base + scale_at<SUB>(r, g);
-    if (SUB == 4) return *reinterpret_cast<const uint32_t*>(p);
-    if (SUB == 2) return *reinterpret_cast<const uint16_t*>(p);
-    return *p;
-}
+// Where the scale bytes of a step lie, KS == 128 and MXFP8 with wavefront tiles
+// of whole groups of 4 subtiles: block g of row r.  The bytes of 4 rows 16
+// apart are neighbours, so that a lane reads 4 subtiles' scales at once and
+// the instruction selects one.  (Otherwise a row's bytes stay together.)
+__device__ __forceinline__ int scale_at(int r, int g) { return 4 * (((r >> 6) * 16 + (r & 15)) * 4 + g) + ((r >> 4) & 3); }
 
 // Workgroup -> tile: workgroups are dealt to the 8 XCDs in turn, so each XCD
 // takes a contiguous range of tiles, in columns of `kGroupM` token tiles, and
@@ -392,94 +452,113 @@ __device__ __forceinline__ TilePos tile_of(int64_t bid, int64_t tiles_m, int64_t
     return {first + in % gm, in / gm};
 }
 
-template <int BM, int BN, int WM, int WN, bool BF16_OUT>
-__global__ __launch_bounds__(64 * WM * WN) void k_mx_tiled(W4Args a, int64_t tiles_m, int64_t tiles_n) {
-    constexpr int kThreads = 64 * WM * WN;
-    constexpr int kXPieces = BM * 8 / kThreads, kWPieces = BN * 4 / kThreads;  // 16-byte pieces per thread and step
-    constexpr int TM = BM / WM / 16, TN = BN / WN / 16;
-    constexpr int kSubM = TM < 4 ? TM : 4, kSubN = TN < 4 ? TN : 4;
-    constexpr int kAhead = TM >= 4 ? 2 : 1, kRing = 2 * kAhead;
-    constexpr int kXBytes = BM * kTileK, kWBytes = BN * kTileK / 2, kSBytes = (BM + BN) * 4;
-    constexpr int kStageBytes = kXBytes + kWBytes + kSBytes;
-    constexpr int kScaleRows = (BM + BN + kThreads - 1) / kThreads;
-    static_assert(kXPieces >= 1 && kWPieces >= 1, "every thread transfers both operands");
-    static_assert(TM % kRing == 0 && TN % kSubN == 0, "fragment ring and scale groups");
-    __shared__ __attribute__((aligned(128))) uint8_t lds[3 * kStageBytes];
+template <int KIND, int KS, int BM, int BN, int WM, int WN, bool BF16_OUT>
+__global__ __launch_bounds__(64 * WM * WN) void k_w4_tiled(W4Args a, int64_t tiles_m, int64_t tiles_n) {
+    constexpr bool kMx = KIND == kW4Mx, kNv = KIND == kW4Bf16Nvfp4;
+    constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+    constexpr int TM = BM / WM / 16, TN = BN / WN / 16;                          // 16 x 16 subtiles per wavefront
+    constexpr int kXRow = kMx ? KS : 2 * KS, kWRow = KS / 2;                     // bytes of a row's step
+    constexpr int kXPer = kXRow / 16, kWPer = kWRow / 16;                        // 16-byte pieces of it
+    constexpr int kXMask = kXPer < 16 ? kXPer - 1 : 15, kWMask = kWPer < 16 ? kWPer - 1 : 15;
+    constexpr int kXInst = BM * kXRow / 1024 / kWaves, kWInst = BN * kWRow / 1024 / kWaves;  // transfers per wavefront
+    constexpr int kBlock = kNv ? 16 : 32, kSb = KS / kBlock;                     // scale bytes of a row's step
+    constexpr int kSRows = (kMx ? BM : 0) + BN;                                  // rows that have scales
+    constexpr int kXBytes = BM * kXRow, kWBytes = BN * kWRow, kStageBytes = kXBytes + kWBytes + kSRows * kSb;
+    constexpr int NJ = KS >= 128 ? KS / 128 : 1;                                 // W pieces per lane and subtile
+    constexpr int NP = kMx ? 2 * NJ : KS / 32;                                   // X pieces per lane and subtile
+    constexpr bool kGroup = kMx && KS == 128 && TM % 4 == 0 && TN % 4 == 0;      // scale_at
+    constexpr int kLaneSb = kMx ? NJ : (kSb >= 4 ? kSb / 4 : 1);                 // scale bytes per lane and subtile
+    constexpr int kAhead = NP <= 4 && TM >= 4 ? 2 : 1, kRing = 2 * kAhead;
+    static_assert(kMx ? KS % 128 == 0 && KS <= 512 : KS == 64 || KS == 128 || KS == 256, "k per step");
+    static_assert(BM * kXRow % (1024 * kWaves) == 0 && BN * kWRow % (1024 * kWaves) == 0, "every wavefront transfers alike");
+    static_assert(kSRows <= kThreads && TM % kRing == 0, "one row's scales per thread; fragment ring");
+    __shared__ __attribute__((aligned(256))) uint8_t lds[3 * kStageBytes];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c16 = lane & 15, g = lane >> 4;
     const TilePos pos = tile_of(blockIdx.x, tiles_m, tiles_n);
     const int64_t m0 = pos.m * BM, n0 = pos.n * BN;
-    const int nsteps = (int)((a.K + kTileK - 1) / kTileK), full = (int)(a.K / kTileK);
-    const int64_t nb = a.K / 32;
+    const int K = (int)a.K, full = K / KS, nsteps = (K + KS - 1) / KS;
+    const int nb = K / kBlock;
 
-    // Piece i of this thread: rows in order of waves, then i.  Rows past the
-    // operand's end read its last row and feed outputs that are never stored.
-    // Offsets from the tile's first row fit 32 bits (K <= kMaxTileK).
-    const uint8_t* xbase = a.x + m0 * a.K;
-    const uint8_t* wbase = a.wc + n0 * (a.K / 2);
-    uint32_t xoff[kXPieces], woff[kWPieces];
-    constexpr int kXWave = kXPieces * 8, kWWave = kWPieces * 16;  // rows per wavefront
-    const uint32_t K32 = (uint32_t)a.K;
+    // Sources of this lane's transfers, as offsets from the tile's first row
+    // (32 bits: K <= kMaxW4K).  Rows past the operand's end read its last row
+    // and feed outputs that are never stored.
+    const uint8_t* xbase = a.x + m0 * K * (kMx ? 1 : 2);
+    const uint8_t* wbase = a.wc + n0 * (K / 2);
     const int mlast = (int)(a.M - 1 - m0 < BM ? a.M - 1 - m0 : BM), nlast = (int)(a.N - 1 - n0 < BN ? a.N - 1 - n0 : BN);
-    const int xpiece = (lane & 7) ^ (lane >> 3), wpiece = (lane & 3) ^ ((lane >> 3) & 3);
+    uint32_t xoff[kXInst], woff[kWInst];
+    int xpiece[kXInst], wpiece[kWInst];
 #pragma unroll
-    for (int i = 0; i < kXPieces; ++i)
-        xoff[i] = (uint32_t)min(wave * kXWave + 8 * i + (lane >> 3), mlast) * K32 + 16 * xpiece;
-#pragma unroll
-    for (int i = 0; i < kWPieces; ++i)
-        woff[i] = (uint32_t)min(wave * kWWave + 16 * i + (lane >> 2), nlast) * (K32 / 2) + 16 * wpiece;
-    const uint8_t* ssrc[kScaleRows];
-#pragma unroll
-    for (int i = 0; i < kScaleRows; ++i) {
-        const int r = tid + kThreads * i;
-        ssrc[i] = r < BM ? a.xs + (m0 + min(r, mlast)) * nb : a.ws + (n0 + min(r - BM, nlast)) * nb;
+    for (int i = 0; i < kXInst; ++i) {
+        const int row = (wave * kXInst + i) * 64 / kXPer + lane / kXPer;
+        xpiece[i] = (lane % kXPer) ^ (row & kXMask);
+        xoff[i] = (uint32_t)min(row, mlast) * (uint32_t)(K * (kMx ? 1 : 2)) + 16 * xpiece[i];
     }
+    auto wperm = [](int r) { return kWPer == 2 ? 0 : kWPer == 4 ? (r >> 1) & 3 : r & kWMask; };
+#pragma unroll
+    for (int i = 0; i < kWInst; ++i) {
+        const int row = (wave * kWInst + i) * 64 / kWPer + lane / kWPer;
+        wpiece[i] = (lane % kWPer) ^ wperm(row);
+        woff[i] = (uint32_t)min(row, nlast) * (uint32_t)(K / 2) + 16 * wpiece[i];
+    }
+    // the row whose scales this thread loads: X rows first
+    const int srow = kMx && tid < BM ? min(tid, mlast) : min(tid - (kMx ? BM : 0), nlast);
+    const uint8_t* ssrc = kMx && tid < BM ? a.xs + (m0 + srow) * nb : a.ws + (n0 + srow) * nb;
+    constexpr int kSDwords = (kSb + 3) / 4;
+    uint32_t sreg[kSDwords];
 
-    auto load_codes = [&](int s, uint8_t* st) {
-        uint8_t* xd = st + wave * kXWave * kTileK;
-        uint8_t* wd = st + kXBytes + wave * kWWave * (kTileK / 2);
-        const uint8_t* xb = xbase + (int64_t)s * kTileK;
-        const uint8_t* wb = wbase + (int64_t)s * (kTileK / 2);
+    auto load = [&](int s, uint8_t* st) {
+        if (kSRows == kThreads || tid < kSRows) {
+            const uint8_t* p = ssrc + s * kSb;
+#pragma unroll
+            for (int i = 0; i < kSDwords; ++i) {
+                if (kSb >= 4) {
+                    sreg[i] = s < full ? ld4_a1(p + 4 * i) : scales_until(p + 4 * i, s * kSb + 4 * i, nb, kNv ? 0x38u : 127u);
+                } else {  // two blocks; K % 32 == 0, so an absent one is the second
+                    sreg[i] = p[0] | (uint32_t)(s < full || s * kSb + 1 < nb ? p[1] : 127) << 8;
+                }
+            }
+        }
+        uint8_t* xd = st + wave * kXInst * 1024;
+        uint8_t* wd = st + kXBytes + wave * kWInst * 1024;
+        const uint8_t* xb = xbase + (int64_t)s * kXRow;
+        const uint8_t* wb = wbase + (int64_t)s * kWRow;
         if (s < full) {
 #pragma unroll
-            for (int i = 0; i < kXPieces; ++i) to_lds16(xb, xoff[i], lds_address(xd + i * 8 * kTileK));
+            for (int i = 0; i < kXInst; ++i) to_lds16(xb, xoff[i], lds_address(xd + i * 1024));
 #pragma unroll
-            for (int i = 0; i < kWPieces; ++i) to_lds16(wb, woff[i], lds_address(wd + i * 16 * (kTileK / 2)));
+            for (int i = 0; i < kWInst; ++i) to_lds16(wb, woff[i], lds_address(wd + i * 1024));
         } else {
             // the last, partial step: pieces past K are zeros
-            const int left = (int)(a.K - (int64_t)s * kTileK);
+            const int left = K - s * KS;
 #pragma unroll
-            for (int i = 0; i < kXPieces; ++i) {
+            for (int i = 0; i < kXInst; ++i) {
                 uint4 v = make_uint4(0, 0, 0, 0);
-                if (16 * xpiece < left) v = *reinterpret_cast<const uint4*>(xb + xoff[i]);
-                *reinterpret_cast<uint4*>(xd + i * 8 * kTileK + 16 * lane) = v;
+                if ((kMx ? 16 : 8) * xpiece[i] < left) v = *reinterpret_cast<const uint4*>(xb + xoff[i]);
+                *reinterpret_cast<uint4*>(xd + i * 1024 + 16 * lane) = v;
             }
 #pragma unroll
-            for (int i = 0; i < kWPieces; ++i) {
+            for (int i = 0; i < kWInst; ++i) {
                 uint4 v = make_uint4(0, 0, 0, 0);
-                if (32 * wpiece < left) v = *reinterpret_cast<const uint4*>(wb + woff[i]);
-                *reinterpret_cast<uint4*>(wd + i * 16 * (kTileK / 2) + 16 * lane) = v;
+                if (32 * wpiece[i] < left) v = *reinterpret_cast<const uint4*>(wb + woff[i]);
+                *reinterpret_cast<uint4*>(wd + i * 1024 + 16 * lane) = v;
             }
         }
     };
-    uint32_t sreg[kScaleRows];
-    auto load_scales = [&](int s) {
-#pragma unroll
-        for (int i = 0; i < kScaleRows; ++i)
-            if (kScaleRows * kThreads == BM + BN || tid + kThreads * i < BM + BN)
-                sreg[i] = scales_until(ssrc[i] + 4 * s, 4 * s, nb, 127u);
-    };
     auto store_scales = [&](uint8_t* st) {
+        uint8_t* p = st + kXBytes + kWBytes;
+        if (kSRows == kThreads || tid < kSRows) {
+            if (kGroup) {  // BM % 64 == 0
 #pragma unroll
-        for (int i = 0; i < kScaleRows; ++i)
-            if (kScaleRows * kThreads == BM + BN || tid + kThreads * i < BM + BN) {
-                const int r = tid + kThreads * i;
-                uint8_t* p = st + kXBytes + kWBytes;
+                for (int b = 0; b < 4; ++b) p[scale_at(tid, b)] = (uint8_t)(sreg[0] >> (8 * b));
+            } else if (kSb >= 4) {
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
-                    p[r < BM ? scale_at<kSubM>(r, b) : 4 * BM + scale_at<kSubN>(r - BM, b)] = (uint8_t)(sreg[i] >> (8 * b));
+                for (int i = 0; i < kSDwords; ++i) reinterpret_cast<uint32_t*>(p + tid * kSb)[i] = sreg[i];
+            } else {
+                *reinterpret_cast<uint16_t*>(p + tid * kSb) = (uint16_t)sreg[0];
             }
+        }
     };
 
     f32x4 acc[TN][TM];
@@ -488,37 +567,91 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_tiled(W4Args a, int64_t til
 #pragma unroll
         for (int i = 0; i < TM; ++i) acc[j][i] = (f32x4){};
     const int mrow = (wave / WN) * (BM / WM), nrow = (wave % WN) * (BN / WN);
-    // fragment addresses within a stage; the permutation depends on c16 alone
-    const int xlo = (mrow + c16) * kTileK + 16 * (g ^ (c16 & 7)), xhi = xlo ^ 64;
-    const int wat = kXBytes + (nrow + c16) * (kTileK / 2) + 16 * (g ^ ((c16 >> 1) & 3));
+    // Fragment addresses within a stage; the permutations depend on c16 alone.
+    // MXFP8, product j of NJ: logical block b is block NJ b + j of the step; the
+    // lane's W piece is that of logical block g, its X halves are half g % 2 of
+    // logical blocks g / 2 and 2 + g / 2.  BF16: the lane takes k = KS/4 g ..
+    // of the step, 8 per product.  Every index below is an XOR of disjoint bits.
+    const int xat = (mrow + c16) * kXRow + 16 * ((kMx ? 2 * NJ * (g >> 1) + (g & 1) : NP * g) ^ (c16 & kXMask));
+    const int wat = kXBytes + (nrow + c16) * kWRow + (kWPer == 2 ? 8 * g : 16 * ((NJ * g) ^ wperm(c16)));
+    auto xpart = [](int q) { return kMx ? 32 * (q >> 1) ^ (q & 1) * 64 * NJ : 16 * q; };  // MXFP8: q = 2 j + half
 
-    struct Frags {  // of one step: W and all scales
-        uint4 w[TN];
-        uint32_t ws[TN / kSubN], xs[TM / kSubM];
+    struct Frags {  // of one step: W as stored, and all scales
+        uint4 w[TN][NJ];
+        uint32_t ws[kGroup ? TN / 4 : TN], xs[kGroup ? TM / 4 : kMx ? TM : 1];
     };
-    uint4 xl[kRing], xh[kRing];
+    uint4 xf[kRing][NP];
     auto read_x = [&](const uint8_t* st, int i) {
-        xl[i % kRing] = *reinterpret_cast<const uint4*>(st + xlo + i * 16 * kTileK);
-        xh[i % kRing] = *reinterpret_cast<const uint4*>(st + xhi + i * 16 * kTileK);
+#pragma unroll
+        for (int q = 0; q < NP; ++q)
+            xf[i % kRing][q] = *reinterpret_cast<const uint4*>(st + (xat ^ xpart(q)) + i * 16 * kXRow);
+    };
+    auto lane_scales = [&](const uint8_t* row) -> uint32_t {  // the lane's bytes of a row's step
+        if (kSb == 2) return row[g >> 1];
+        const uint8_t* p = row + kLaneSb * g;
+        return kLaneSb == 4 ? *reinterpret_cast<const uint32_t*>(p) : kLaneSb == 2 ? *reinterpret_cast<const uint16_t*>(p) : *p;
     };
     auto read_w = [&](const uint8_t* st, Frags& f) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            const uint8_t* p = st + j * 16 * kWRow;
+            if (kWPer == 2) {
+                const uint2 v = *reinterpret_cast<const uint2*>(p + wat);
+                f.w[j][0] = make_uint4(v.x, v.y, 0, 0);
+            } else {
+#pragma unroll
+                for (int q = 0; q < NJ; ++q) f.w[j][q] = *reinterpret_cast<const uint4*>(p + (wat ^ (16 * q)));
+            }
+        }
         const uint8_t* sc = st + kXBytes + kWBytes;
+        if (kGroup) {
 #pragma unroll
-        for (int j = 0; j < TN; ++j) f.w[j] = *reinterpret_cast<const uint4*>(st + wat + j * 16 * (kTileK / 2));
+            for (int j = 0; j < TN; j += 4)
+                f.ws[kGroup ? j / 4 : 0] = *reinterpret_cast<const uint32_t*>(sc + 4 * BM + scale_at(nrow + 16 * j + c16, g));
 #pragma unroll
-        for (int j = 0; j < TN; j += kSubN) f.ws[j / kSubN] = read_scales<kSubN>(sc + 4 * BM, nrow + 16 * j + c16, g);
+            for (int i = 0; i < TM; i += 4)
+                f.xs[kGroup ? i / 4 : 0] = *reinterpret_cast<const uint32_t*>(sc + scale_at(mrow + 16 * i + c16, g));
+        } else {
 #pragma unroll
-        for (int i = 0; i < TM; i += kSubM) f.xs[i / kSubM] = read_scales<kSubM>(sc, mrow + 16 * i + c16, g);
+            for (int j = 0; j < TN; ++j)
+                f.ws[kGroup ? 0 : j] = lane_scales(sc + ((kMx ? BM : 0) + nrow + 16 * j + c16) * kSb);
+            if (kMx) {
+#pragma unroll
+                for (int i = 0; i < TM; ++i) f.xs[kGroup ? 0 : i] = lane_scales(sc + (mrow + 16 * i + c16) * kSb);
+            }
+        }
+    };
+    // BF16 activations: a step's W in BF16, product q of NP
+    bf16x8 wv[kMx ? 1 : TN][NP];
+    auto widen = [&](const Frags& f) {
+        if constexpr (!kMx) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int q = 0; q < NP; ++q) {
+                    const uint32_t c = pick(f.w[j][q >> 2], q & 3);  // 8 codes, k = 8 q of the lane's
+                    wv[j][q] = kNv ? widen_nv(c, e4m3_f32(f.ws[j] >> (8 * (q >> 1)))) : widen_mx(c, e8m0_f32(f.ws[j] >> (8 * (q >> 2))));
+                }
+        }
     };
     auto products = [&](int i, const Frags& f) {
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
-            acc[j][i] = mfma_tile(j % kSubN, i % kSubM, f.w[j], xl[i % kRing], xh[i % kRing], f.ws[j / kSubN],
-                                  f.xs[i / kSubM], acc[j][i]);
+        for (int q = 0; q < (kMx ? NJ : NP); ++q)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                if constexpr (kMx)
+                    acc[j][i] = mfma_tile(kGroup ? j % 4 : q, kGroup ? i % 4 : q, f.w[j][q], xf[i % kRing][kMx ? 2 * q : 0],
+                                          xf[i % kRing][kMx ? 2 * q + 1 : 0], f.ws[kGroup ? j / 4 : j],
+                                          f.xs[kGroup ? i / 4 : i], acc[j][i]);
+                else
+                    acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        wv[j][q], __builtin_bit_cast(bf16x8, xf[i % kRing][q]), acc[j][i], 0, 0, 0);
+            }
     };
     // step s with its fragments f, in stage `cur`; reads the next step's
     // fragments into n
-    auto step = [&](int s, const uint8_t* cur, uint8_t* next, uint8_t* after, const Frags& f, Frags& n) {
+    auto step = [&](int s, const uint8_t* cur, uint8_t* next, uint8_t* last, const Frags& f, Frags& n) {
+        widen(f);
 #pragma unroll
         for (int i = 0; i < TM / 2; ++i) {
             read_x(cur, i + kAhead);
@@ -527,10 +660,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_tiled(W4Args a, int64_t til
         if (s + 1 < nsteps) store_scales(next);
         wait_transfers();
         __syncthreads();
-        if (s + 2 < nsteps) {
-            load_scales(s + 2);
-            load_codes(s + 2, after);
-        }
+        if (s + 2 < nsteps) load(s + 2, last);
         read_w(next, n);  // past the last step: a stage's leftovers, not used
 #pragma unroll
         for (int i = TM / 2; i < TM; ++i) {
@@ -541,13 +671,9 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_tiled(W4Args a, int64_t til
     Frags f0, f1;
     uint8_t *s0 = lds, *s1 = lds + kStageBytes, *s2 = lds + 2 * kStageBytes;
     if (nsteps > 0) {
-        load_scales(0);
-        load_codes(0, s0);
+        load(0, s0);
         store_scales(s0);
-        if (nsteps > 1) {
-            load_scales(1);
-            load_codes(1, s1);
-        }
+        if (nsteps > 1) load(1, s1);
         wait_transfers();
         __syncthreads();
         read_w(s0, f0);
@@ -565,6 +691,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_tiled(W4Args a, int64_t til
 
     // register r of lane l in tile (j, i): column 16 j + 4 (l / 16) + r, token
     // 16 i + l % 16
+    const float s2w = kNv ? a.ws2[0] : 1.0f;
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
         const int64_t row = m0 + mrow + 16 * i + c16;
@@ -572,8 +699,9 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_tiled(W4Args a, int64_t til
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
             const int64_t col = n0 + nrow + 16 * j + 4 * g;
-            const f32x4 v = acc[j][i];
-            if (col + 3 < a.N && a.N % 4 == 0) {
+            f32x4 v = acc[j][i];
+            if (kNv) v = v * s2w;
+            if (col + 3 < a.N && a.N % 4 == 0 && ((uintptr_t)a.y & (BF16_OUT ? 7 : 15)) == 0) {
                 if (BF16_OUT)
                     *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.y) + row * a.N + col) =
                         make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
@@ -593,52 +721,133 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_tiled(W4Args a, int64_t til
     }
 }
 
-template <int BM, int BN, int WM, int WN, bool BF16_OUT>
-hipError_t run_tiled(const W4Args& a, hipStream_t stream) {
-    const int64_t tiles_m = (a.M + BM - 1) / BM, tiles_n = (a.N + BN - 1) / BN;
-    return launch(&k_mx_tiled<BM, BN, WM, WN, BF16_OUT>, dim3((unsigned)(tiles_m * tiles_n)), dim3(64 * WM * WN), stream, a,
-                  tiles_m, tiles_n);
-}
-
-template <int KIND, bool BF16_OUT, int MT>
-hipError_t run_decode(const W4Args& args, hipStream_t stream) {
-    constexpr int kWaves = 8, kT = 1;
-    const int64_t tiles_n = (args.N + 16 * kT - 1) / (16 * kT);
+template <int KIND, int KS, int BM, int BN, int WM, int WN, bool BF16_OUT>
+hipError_t run_tiled(const W4Args& args, hipStream_t stream) {
+    const int64_t tiles_n = (args.N + BN - 1) / BN;
     // runs of token tiles whose grid stays within 2^31 threads
-    const int64_t most = (((int64_t)1 << 31) / (64 * kWaves)) / tiles_n;
+    const int64_t most = (((int64_t)1 << 31) / (64 * WM * WN)) / tiles_n;
     if (most < 1) return hipErrorInvalidValue;
-    for (int64_t row = 0; row < args.M; row += most * 16 * MT) {
-        W4Args a = args;
-        a.M = args.M - row < most * 16 * MT ? args.M - row : most * 16 * MT;
-        a.x += row * a.K * (KIND == kW4Mx ? 1 : 2);
-        if (KIND == kW4Mx) a.xs += row * (a.K / 32);
-        a.y = reinterpret_cast<uint8_t*>(a.y) + row * a.N * (BF16_OUT ? 2 : 4);
-        const int64_t tiles_m = (a.M + 16 * MT - 1) / (16 * MT);
-        const hipError_t e = launch(&k_w4_decode<KIND, BF16_OUT, kWaves, kT, MT>, dim3((unsigned)(tiles_m * tiles_n)),
-                                    dim3(64 * kWaves), stream, a, tiles_n);
+    for (int64_t row = 0; row < args.M; row += most * BM) {
+        const W4Args a = rows_from<KIND, BF16_OUT>(args, row, most * BM);
+        const int64_t tiles_m = (a.M + BM - 1) / BM;
+        const hipError_t e = launch(&k_w4_tiled<KIND, KS, BM, BN, WM, WN, BF16_OUT>, dim3((unsigned)(tiles_m * tiles_n)),
+                                    dim3(64 * WM * WN), stream, a, tiles_m, tiles_n);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
 }
 
+template <int KIND, bool BF16_OUT, int WAVES, int T, int MT>
+hipError_t run_decode(const W4Args& args, hipStream_t stream) {
+    const int64_t tiles_n = (args.N + 16 * T - 1) / (16 * T);
+    // runs of token tiles whose grid stays within 2^31 threads
+    const int64_t most = (((int64_t)1 << 31) / (64 * WAVES)) / tiles_n;
+    if (most < 1) return hipErrorInvalidValue;
+    for (int64_t row = 0; row < args.M; row += most * 16 * MT) {
+        const W4Args a = rows_from<KIND, BF16_OUT>(args, row, most * 16 * MT);
+        const int64_t tiles_m = (a.M + 16 * MT - 1) / (16 * MT);
+        const hipError_t e = launch(&k_w4_decode<KIND, BF16_OUT, WAVES, T, MT>, dim3((unsigned)(tiles_m * tiles_n)),
+                                    dim3(64 * WAVES), stream, a, tiles_n);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+// Which kernel.  Decode (wavefronts share a column tile and split k): `t`
+// 16-column tiles per workgroup, as few as let every workgroup be resident at
+// once -- X is then read once per 16 t columns, and fewer, wider workgroups
+// leave CUs idle.  Measured (us; MXFP8 x MXFP4 at t = 1, 2, 4): 8 x 4096 x 4096
+// 4.5, 5.4, -; 8 x 6144 x 4096 7.1, 6.0, 7.4; 8 x 14336 x 4096 11.6, 10.0, 10.0;
+// 8 x 28672 x 8192 39, 35.2, 32.1.  With up to 4 tokens X costs little and t
+// stays at 2 at most (1 x 14336 x 4096 8.4 against 9.7 with 4).  Four
+// wavefronts; eight where such a small batch meets a long K (1 x 8192 x 28672
+// 23.9 against 27.3; at 4096 they are 10 % slower).
+int decode_columns(int64_t tiles_m, int64_t M, int64_t N, int64_t cus) {
+    int t = 1;
+    while (t < (M <= 4 ? 2 : 4) && tiles_m * ((N + 16 * t - 1) / (16 * t)) > cus) t *= 2;
+    return t;
+}
+
+constexpr int64_t kDecodeOneTile = 16, kDecodeTwoTiles = 64, kDecodeLongK = 8192;
+
 template <int KIND, bool BF16_OUT>
-hipError_t pick_decode(const W4Args& a, hipStream_t stream) {
-    if (a.M <= 16) return run_decode<KIND, BF16_OUT, 1>(a, stream);
-    if (KIND == kW4Mx && a.M > 64 && a.K <= kMaxTileK) return run_tiled<256, 256, 2, 4, BF16_OUT>(a, stream);
-    return run_decode<KIND, BF16_OUT, 2>(a, stream);
+hipError_t decode_16(const W4Args& a, int64_t cus, hipStream_t stream) {
+    const int t = decode_columns(1, a.M, a.N, cus);
+    if (a.M <= 4 && a.K > kDecodeLongK)
+        return t == 1 ? run_decode<KIND, BF16_OUT, 8, 1, 1>(a, stream) : run_decode<KIND, BF16_OUT, 8, 2, 1>(a, stream);
+    if (t == 1) return run_decode<KIND, BF16_OUT, 4, 1, 1>(a, stream);
+    if (t == 2) return run_decode<KIND, BF16_OUT, 4, 2, 1>(a, stream);
+    return run_decode<KIND, BF16_OUT, 4, 4, 1>(a, stream);
+}
+
+// 17 to 64 tokens: two token tiles per wavefront, while at most 32 columns per
+// workgroup fill the device: 32 x 4096 x 14336 20.7 us against 27.5 with tiles
+// of 32 x 64 and a step at a time, but 32 x 14336 x 4096 13.5 against 11.3.
+bool decode_32_fits(int64_t M, int64_t N, int64_t cus) {
+    return M <= kDecodeTwoTiles && ((M + 31) / 32) * ((N + 31) / 32) <= cus;
+}
+
+template <int KIND, bool BF16_OUT>
+hipError_t decode_32(const W4Args& a, int64_t cus, hipStream_t stream) {
+    return decode_columns((a.M + 31) / 32, a.M, a.N, cus) == 1 ? run_decode<KIND, BF16_OUT, 4, 1, 2>(a, stream)
+                                                               : run_decode<KIND, BF16_OUT, 4, 2, 2>(a, stream);
+}
+
+inline int64_t tiles(const W4Args& a, int bm, int bn) { return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); }
+
+// Tiles: the smallest whose workgroups are all resident at once (a second
+// round of few workgroups costs as much as a full one), else the largest,
+// which moves the fewest bytes per product.  Measured (us): 100 x 4096 x 4096
+// with tiles of 32 x 64, 64 x 64, 64 x 64 in shorter steps (two workgroups per
+// CU), 128 x 128: 10.4, 11.9, 15.2, 27; 100 x 14336 x 4096: 28, 22.4, 17.3, 27.9;
+// 512 x 14336 x 4096, the last two, 256 x 128 and 256 x 256: 59, 44.4, 42.1, 59.6;
+// 8192 x 14336 x 4096, the last three: 579, 600, 444.
+template <bool BF16_OUT>
+hipError_t pick_mx(const W4Args& a, int64_t cus, hipStream_t stream) {
+    if (a.M <= kDecodeOneTile) return decode_16<kW4Mx, BF16_OUT>(a, cus, stream);
+    if (decode_32_fits(a.M, a.N, cus)) return decode_32<kW4Mx, BF16_OUT>(a, cus, stream);
+    if (tiles(a, 32, 64) <= cus) return run_tiled<kW4Mx, 512, 32, 64, 1, 4, BF16_OUT>(a, stream);
+    if (tiles(a, 64, 64) <= cus) return run_tiled<kW4Mx, 512, 64, 64, 2, 4, BF16_OUT>(a, stream);
+    if (tiles(a, 64, 64) <= 2 * cus) return run_tiled<kW4Mx, 256, 64, 64, 2, 2, BF16_OUT>(a, stream);
+    if (tiles(a, 128, 128) <= cus) return run_tiled<kW4Mx, 128, 128, 128, 2, 2, BF16_OUT>(a, stream);
+    if (tiles(a, 256, 128) <= cus) return run_tiled<kW4Mx, 128, 256, 128, 4, 2, BF16_OUT>(a, stream);
+    return run_tiled<kW4Mx, 128, 256, 256, 2, 4, BF16_OUT>(a, stream);
+}
+
+// BF16 activations, by the same rule (NVFP4, us): 61 x 4096 x 4096 with tiles of
+// 32 x 32 and 32 x 64: 16.5, 16.8; 61 x 6144 x 4096: 19.1, 17.2; 128 x 14336 x 4096
+// with 32 x 64 and 64 x 128: 41, 31.5; 512 x 28672 x 8192 with 64 x 128 and
+// 256 x 256: 315, 239, but 512 x 14336 x 4096: 87, 108 -- the middle tile keeps
+// two workgroups per CU and stays ahead for two rounds of them.  The tiles'
+// transfers of 16 bytes want K % 32 == 0.
+template <int KIND, bool BF16_OUT>
+hipError_t pick_bf16(const W4Args& a, int64_t cus, hipStream_t stream) {
+    if (a.M <= kDecodeOneTile) return decode_16<KIND, BF16_OUT>(a, cus, stream);
+    if (decode_32_fits(a.M, a.N, cus)) return decode_32<KIND, BF16_OUT>(a, cus, stream);
+    if (KIND == kW4Bf16Nvfp4 && a.K % 32 != 0) return run_decode<KIND, BF16_OUT, 4, 4, 2>(a, stream);
+    if (tiles(a, 32, 32) <= cus) return run_tiled<KIND, 256, 32, 32, 1, 2, BF16_OUT>(a, stream);
+    if (tiles(a, 32, 64) <= 2 * cus) return run_tiled<KIND, 256, 32, 64, 1, 4, BF16_OUT>(a, stream);
+    if (tiles(a, 64, 128) <= 4 * cus) return run_tiled<KIND, 128, 64, 128, 1, 4, BF16_OUT>(a, stream);
+    return run_tiled<KIND, 64, 256, 256, 2, 4, BF16_OUT>(a, stream);
+}
+
+template <bool BF16_OUT>
+hipError_t pick(const W4Args& a, W4Kind kind, int64_t cus, hipStream_t stream) {
+    switch (kind) {
+        case kW4Mx: return pick_mx<BF16_OUT>(a, cus, stream);
+        case kW4Bf16Nvfp4: return pick_bf16<kW4Bf16Nvfp4, BF16_OUT>(a, cus, stream);
+        case kW4Bf16Mxfp4: return pick_bf16<kW4Bf16Mxfp4, BF16_OUT>(a, cus, stream);
+    }
+    return hipErrorInvalidValue;
 }
 
 }  // namespace
 
 hipError_t launch_w4_linear(const W4Args& a, W4Kind kind, bool bf16_out, hipStream_t stream) {
-    switch (kind) {
-        case kW4Mx: return bf16_out ? pick_decode<kW4Mx, true>(a, stream) : pick_decode<kW4Mx, false>(a, stream);
-        case kW4Bf16Nvfp4:
-            return bf16_out ? pick_decode<kW4Bf16Nvfp4, true>(a, stream) : pick_decode<kW4Bf16Nvfp4, false>(a, stream);
-        case kW4Bf16Mxfp4:
-            return bf16_out ? pick_decode<kW4Bf16Mxfp4, true>(a, stream) : pick_decode<kW4Bf16Mxfp4, false>(a, stream);
-    }
-    return hipErrorInvalidValue;
+    int64_t cus = 0;
+    const hipError_t e = nvfp4_linear_cus(cus);
+    if (e != hipSuccess) return e;
+    return bf16_out ? pick<true>(a, kind, cus, stream) : pick<false>(a, kind, cus, stream);
 }
 
 }  // namespace focus

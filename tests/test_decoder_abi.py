@@ -96,42 +96,41 @@ def test_quantize_mxfp8_validation(lib):
 
 def test_mxfp4_linear_validation(lib):
     f = lib.focus_mxfp4_linear
-    #        xc    xs    M  wc    ws    N  K   y    dt ws  bytes stream
-    assert f(FAKE, FAKE, 4, FAKE, FAKE, 8, 48, FAKE, 0, None, 0, None) == ERR_SHAPE
-    assert f(FAKE, FAKE, -1, FAKE, FAKE, 8, 64, FAKE, 0, None, 0, None) == ERR_SHAPE
-    assert f(FAKE, FAKE, (1 << 31) + 1, FAKE, FAKE, 8, 64, FAKE, 0, None, 0, None) == ERR_RANGE
-    assert f(FAKE, FAKE, 4, FAKE, FAKE, (1 << 26) + 1, 64, FAKE, 0, None, 0, None) == ERR_RANGE
-    assert f(FAKE, FAKE, 4, FAKE, FAKE, 8, 64, FAKE, 2, None, 0, None) == ERR_RANGE
-    assert f(FAKE, FAKE, 4, FAKE, FAKE, 8, 64, FAKE, 0, FAKE, -4, None) == ERR_RANGE
+    #        xc    xs    M  wc    ws    N  K   y    dt stream
+    assert f(FAKE, FAKE, 4, FAKE, FAKE, 8, 48, FAKE, 0, None) == ERR_SHAPE
+    assert f(FAKE, FAKE, -1, FAKE, FAKE, 8, 64, FAKE, 0, None) == ERR_SHAPE
+    assert f(FAKE, FAKE, (1 << 31) + 1, FAKE, FAKE, 8, 64, FAKE, 0, None) == ERR_RANGE
+    assert f(FAKE, FAKE, 4, FAKE, FAKE, (1 << 26) + 1, 64, FAKE, 0, None) == ERR_RANGE
+    assert f(FAKE, FAKE, 4, FAKE, FAKE, 8, 64, FAKE, 2, None) == ERR_RANGE
+    assert f(FAKE, FAKE, 4, FAKE, FAKE, 8, (1 << 22) + 32, FAKE, 0, None) == ERR_RANGE
     for k in range(4):
         p = [FAKE] * 4
         p[k] = None
-        assert f(p[0], p[1], 4, p[2], p[3], 8, 64, FAKE, 0, None, 0, None) == ERR_NULL
+        assert f(p[0], p[1], 4, p[2], p[3], 8, 64, FAKE, 0, None) == ERR_NULL
         if k in (0, 2):  # codes
             p[k] = FAKE + 8
-            assert f(p[0], p[1], 4, p[2], p[3], 8, 64, FAKE, 0, None, 0, None) == ERR_ALIGN
-    assert f(FAKE, FAKE, 4, FAKE, FAKE, 8, 64, None, 0, None, 0, None) == ERR_NULL
-    assert f(FAKE, FAKE, 4, FAKE, FAKE, 8, 64, FAKE + 2, 0, None, 0, None) == ERR_ALIGN
-    assert f(FAKE, FAKE, 4, FAKE, FAKE, 8, 64, FAKE + 1, 1, None, 0, None) == ERR_ALIGN
-    assert f(FAKE, FAKE, 4, FAKE, FAKE, 8, 64, FAKE, 0, FAKE + 4, 64, None) == ERR_ALIGN
-    assert f(None, None, 0, None, None, 8, 64, None, 0, None, 0, None) == OK
-    assert f(None, None, 4, None, None, 0, 64, None, 0, None, 0, None) == OK
+            assert f(p[0], p[1], 4, p[2], p[3], 8, 64, FAKE, 0, None) == ERR_ALIGN
+    assert f(FAKE, FAKE, 4, FAKE, FAKE, 8, 64, None, 0, None) == ERR_NULL
+    assert f(FAKE, FAKE, 4, FAKE, FAKE, 8, 64, FAKE + 2, 0, None) == ERR_ALIGN
+    assert f(FAKE, FAKE, 4, FAKE, FAKE, 8, 64, FAKE + 1, 1, None) == ERR_ALIGN
+    assert f(None, None, 0, None, None, 8, 64, None, 0, None) == OK
+    assert f(None, None, 4, None, None, 0, 64, None, 0, None) == OK
 
 
 def test_w4a16_linear_validation(lib):
     f = lib.focus_w4a16_linear
-    #        x    M  fmt wc    ws    s2    N  K   y    dt ws  bytes stream
-    assert f(FAKE, 4, 2, FAKE, FAKE, FAKE, 8, 64, FAKE, 0, None, 0, None) == ERR_RANGE
-    assert f(FAKE, 4, 0, FAKE, FAKE, FAKE, 8, 40, FAKE, 0, None, 0, None) == ERR_SHAPE
-    assert f(FAKE, 4, 1, FAKE, FAKE, None, 8, 48, FAKE, 0, None, 0, None) == ERR_SHAPE
-    assert f(FAKE, 4, 0, FAKE, FAKE, None, 8, 48, FAKE, 0, None, 0, None) == ERR_NULL   # NVFP4 needs s2
-    assert f(None, 4, 1, FAKE, FAKE, None, 8, 64, FAKE, 0, None, 0, None) == ERR_NULL
-    assert f(FAKE, 4, 1, FAKE, None, None, 8, 64, FAKE, 0, None, 0, None) == ERR_NULL
-    assert f(FAKE, 4, 0, FAKE, FAKE, FAKE + 2, 8, 64, FAKE, 0, None, 0, None) == ERR_ALIGN
-    assert f(FAKE + 8, 4, 0, FAKE, FAKE, FAKE, 8, 64, FAKE, 0, None, 0, None) == ERR_ALIGN
-    assert f(FAKE, 4, 0, FAKE + 8, FAKE, FAKE, 8, 64, FAKE, 0, None, 0, None) == ERR_ALIGN
-    assert f(FAKE, 4, 0, FAKE, FAKE, FAKE, 8, 64, FAKE, 3, None, 0, None) == ERR_RANGE
-    assert f(None, 0, 0, None, None, None, 8, 64, None, 1, None, 0, None) == OK
+    #        x    M  fmt wc    ws    s2    N  K   y    dt stream
+    assert f(FAKE, 4, 2, FAKE, FAKE, FAKE, 8, 64, FAKE, 0, None) == ERR_RANGE
+    assert f(FAKE, 4, 0, FAKE, FAKE, FAKE, 8, 40, FAKE, 0, None) == ERR_SHAPE
+    assert f(FAKE, 4, 1, FAKE, FAKE, None, 8, 48, FAKE, 0, None) == ERR_SHAPE
+    assert f(FAKE, 4, 0, FAKE, FAKE, None, 8, 48, FAKE, 0, None) == ERR_NULL   # NVFP4 needs s2
+    assert f(None, 4, 1, FAKE, FAKE, None, 8, 64, FAKE, 0, None) == ERR_NULL
+    assert f(FAKE, 4, 1, FAKE, None, None, 8, 64, FAKE, 0, None) == ERR_NULL
+    assert f(FAKE, 4, 0, FAKE, FAKE, FAKE + 2, 8, 64, FAKE, 0, None) == ERR_ALIGN
+    assert f(FAKE + 8, 4, 0, FAKE, FAKE, FAKE, 8, 64, FAKE, 0, None) == ERR_ALIGN
+    assert f(FAKE, 4, 0, FAKE + 8, FAKE, FAKE, 8, 64, FAKE, 0, None) == ERR_ALIGN
+    assert f(FAKE, 4, 0, FAKE, FAKE, FAKE, 8, 64, FAKE, 3, None) == ERR_RANGE
+    assert f(None, 0, 0, None, None, None, 8, 64, None, 1, None) == OK
 
 
 def test_bindings_refuse_cpu_tensors():
