@@ -570,29 +570,55 @@ def nvfp4_linear_noalloc(x: Quantized, w: Quantized, out: torch.Tensor) -> torch
 # between the linear layers: norm, gated activation, MXFP8
 # ---------------------------------------------------------------------------
 
+# The current stream's handle without building a torch.cuda.Stream object.
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    lambda index: torch.cuda.current_stream(index).cuda_stream
+
+
 def _launch(fn, dev, *args):
     """Call ``fn`` with ``dev`` current and its current stream as the last
     argument."""
-    if torch.cuda.current_device() != dev.index:
+    index = dev.index
+    if torch.cuda.current_device() != index:
         with torch.cuda.device(dev):
-            _lib.check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+            st = fn(*args, _raw_stream(index))
     else:
-        _lib.check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+        st = fn(*args, _raw_stream(index))
+    if st:
+        _lib.check(st)
+
+
+def _fits(t, dtype, index) -> bool:
+    """Whether ``_check_dev`` accepts ``t`` for the HIP device ``index``: one
+    expression in front of the check that names the reason."""
+    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.is_contiguous()
+
+
+def _on_gpu(name, t, dtype):
+    """Device index of a call's first operand, checked."""
+    index = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if index < 0 or not _fits(t, dtype, index):
+        _check_dev(name, t, dtype)
+    return index
 
 
 def _rows_2d(name, t, unit):
-    _check_dev(name, t, torch.bfloat16)
+    """(rows, cols, device index) of a 2-D BF16 operand."""
+    index = _on_gpu(name, t, torch.bfloat16)
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D [tokens, hidden]")
-    if t.shape[1] % unit:
+    rows, cols = t.shape
+    if cols % unit:
         raise ValueError(f"hidden must be a multiple of {unit}")
-    return t.shape
+    return rows, cols, index
 
 
-def _bf16_out(out, rows, cols, dev, label="out"):
+def _bf16_out(out, like, label="out"):
+    """A BF16 output of ``like``'s shape (contiguous)."""
     if out is None:
-        return torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
-    _check_buf(label, out, torch.bfloat16, dev, rows * cols)
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
+    if not (_fits(out, torch.bfloat16, like.get_device()) and out.numel() == like.numel()):
+        _check_buf(label, out, torch.bfloat16, like.device, like.numel())
     return out
 
 
@@ -621,20 +647,21 @@ def _token_nvfp4_outs(out, rows, cols, dev, dequant):
 
 
 def _norm_inputs(x, weight, residual, residual_out, unit):
-    """Checks a norm's inputs; returns (tokens, hidden, device, residual_out)."""
-    t, h = _rows_2d("x", x, unit)
-    dev = x.device
-    _check_dev("weight", weight, torch.bfloat16, dev)
+    """Checks a norm's inputs; returns (tokens, hidden, residual_out)."""
+    t, h, index = _rows_2d("x", x, unit)
+    if not _fits(weight, torch.bfloat16, index):
+        _check_dev("weight", weight, torch.bfloat16, x.device)
     if weight.numel() != h:
         raise ValueError(f"weight holds {weight.numel()} elements, expected {h}")
     if residual is None:
         if residual_out is not None:
             raise ValueError("residual_out needs a residual")
-        return t, h, dev, None
-    _check_dev("residual", residual, torch.bfloat16, dev)
+        return t, h, None
+    if not _fits(residual, torch.bfloat16, index):
+        _check_dev("residual", residual, torch.bfloat16, x.device)
     if residual.shape != x.shape:
         raise ValueError(f"residual must be [{t}, {h}]")
-    return t, h, dev, _bf16_out(residual_out, t, h, dev, "residual_out")
+    return t, h, _bf16_out(residual_out, x, "residual_out")
 
 
 def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual: Optional[torch.Tensor] = None,
@@ -644,8 +671,9 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual: 
     [hidden] BF16.  Returns (y [tokens, hidden] BF16, h or None);
     ``residual_out``, which receives h, may be ``x`` or ``residual`` itself and
     is allocated when None."""
-    t, h, dev, res = _norm_inputs(x, weight, residual, residual_out, 8)
-    y = _bf16_out(out, t, h, dev)
+    t, h, res = _norm_inputs(x, weight, residual, residual_out, 8)
+    dev = x.device
+    y = _bf16_out(out, x)
     _launch(_lib.lib().focus_rmsnorm, dev, _p(x), _p(residual), _p(weight), eps, t, h, _p(res), _p(y))
     return y, res
 
@@ -655,7 +683,8 @@ def rmsnorm_nvfp4(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
                   out: Optional[Quantized] = None, residual_out: Optional[torch.Tensor] = None):
     """``rmsnorm`` with the result in per-token NVFP4 (hidden % 16 == 0), the
     input of ``nvfp4_linear``.  Returns (Quantized, h or None)."""
-    t, h, dev, res = _norm_inputs(x, weight, residual, residual_out, 16)
+    t, h, res = _norm_inputs(x, weight, residual, residual_out, 16)
+    dev = x.device
     q = _token_nvfp4_outs(out, t, h, dev, dequant)
     _launch(_lib.lib().focus_rmsnorm_nvfp4, dev, _p(x), _p(residual), _p(weight), eps, t, h, _p(res), _p(q.codes),
             _p(q.scales), _p(q.s2), _p(q.deq))
@@ -668,7 +697,8 @@ def rmsnorm_mxfp8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
     """``rmsnorm`` with the result in MXFP8 (hidden % 32 == 0), the input of
     ``mxfp4_linear``.  Returns (Quantized with codes [tokens, hidden], scales
     [tokens, hidden/32] and s2 None, h or None)."""
-    t, h, dev, res = _norm_inputs(x, weight, residual, residual_out, 32)
+    t, h, res = _norm_inputs(x, weight, residual, residual_out, 32)
+    dev = x.device
     q = _mxfp8_outs(out, t, h, dev, dequant)
     _launch(_lib.lib().focus_rmsnorm_mxfp8, dev, _p(x), _p(residual), _p(weight), eps, t, h, _p(res), _p(q.codes),
             _p(q.scales), _p(q.deq))
@@ -676,20 +706,23 @@ def rmsnorm_mxfp8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
 
 
 def _gated_input(name, t):
-    """A gate or up operand: 2-D with contiguous elements in a row and rows a
-    fixed distance apart (for example half the columns of a wider tensor)."""
+    """Row stride of a gate or up operand: 2-D with contiguous elements in a
+    row and rows a fixed distance apart (for example half the columns of a
+    wider tensor)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be on a HIP device")
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D [tokens, hidden]")
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    stride, one = t.stride()
+    if cols > 1 and one != 1:
         raise ValueError(f"the elements of {name}'s rows must be contiguous")
-    stride = t.stride(0) if rows > 1 else cols
+    if rows <= 1:
+        return cols
     if stride < cols or stride % 8:
         raise ValueError(f"{name}'s rows must be at least {cols} elements apart, by a multiple of 8")
     return stride
@@ -712,7 +745,7 @@ def silu_mul(gate: torch.Tensor, up: torch.Tensor, out: Optional[torch.Tensor] =
     BF16 tensors (hidden % 8 == 0; rows may lie a multiple of 8 elements
     apart, as the halves of one product's rows do) -> BF16 [tokens, hidden]."""
     t, h, dev, gs, us = _gated_inputs(gate, up, 8)
-    y = _bf16_out(out, t, h, dev)
+    y = _bf16_out(out, gate)
     _launch(_lib.lib().focus_silu_mul, dev, _p(gate), gs, _p(up), us, t, h, _p(y))
     return y
 
@@ -740,7 +773,7 @@ def silu_mul_mxfp8(gate: torch.Tensor, up: torch.Tensor, dequant: bool = False,
 def quantize_mxfp8(x: torch.Tensor, dequant: bool = False, out: Optional[Quantized] = None) -> Quantized:
     """MXFP8 of activations X [tokens, hidden] BF16 (hidden % 32 == 0): E4M3
     codes [tokens, hidden], E8M0 scale bytes [tokens, hidden/32]."""
-    t, h = _rows_2d("x", x, 32)
+    t, h, _ = _rows_2d("x", x, 32)
     q = _mxfp8_outs(out, t, h, x.device, dequant)
     _launch(_lib.lib().focus_quantize_mxfp8, x.device, _p(x), t, h, _p(q.codes), _p(q.scales), _p(q.deq))
     return q
@@ -751,7 +784,7 @@ def quantize_mxfp8(x: torch.Tensor, dequant: bool = False, out: Optional[Quantiz
 # ---------------------------------------------------------------------------
 
 def _w4_out(out, M, N, out_dtype, dev):
-    if out_dtype not in (torch.bfloat16, torch.float32):
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise TypeError("out_dtype must be bfloat16 or float32")
     if out is None:
         return torch.empty((M, N), dtype=out_dtype, device=dev)
@@ -766,10 +799,11 @@ def mxfp4_linear(x: Quantized, w: Quantized, out_dtype: torch.dtype = torch.bflo
     """Y = X' W'^T for MXFP8 activations ``x`` (codes [M, K], scales [M, K/32])
     and MXFP4 weights ``w`` (codes [N, K/2], scales [N, K/32]) on the matrix
     cores; Y [M, N] in ``out_dtype`` (bfloat16 or float32)."""
-    _check_dev("x.codes", x.codes, torch.uint8)
+    index = _on_gpu("x.codes", x.codes, torch.uint8)
     dev = x.codes.device
     for name, t in (("x.scales", x.scales), ("w.codes", w.codes), ("w.scales", w.scales)):
-        _check_dev(name, t, torch.uint8, dev)
+        if not _fits(t, torch.uint8, index):
+            _check_dev(name, t, torch.uint8, dev)
     if x.codes.dim() != 2 or w.codes.dim() != 2:
         raise ValueError("x.codes must be [M, K] and w.codes [N, K/2]")
     M, K = x.codes.shape
@@ -788,10 +822,11 @@ def w4a16_linear(x: torch.Tensor, w: Quantized, out_dtype: torch.dtype = torch.b
     (codes [N, K/2], scales [N, K/16], one s2; K % 16 == 0) or, where ``w.s2``
     is None, MXFP4 (scales [N, K/32]; K % 32 == 0).  Y [M, N] in ``out_dtype``
     (bfloat16 or float32)."""
-    _check_dev("x", x, torch.bfloat16)
+    index = _on_gpu("x", x, torch.bfloat16)
     dev = x.device
-    _check_dev("w.codes", w.codes, torch.uint8, dev)
-    _check_dev("w.scales", w.scales, torch.uint8, dev)
+    if not (_fits(w.codes, torch.uint8, index) and _fits(w.scales, torch.uint8, index)):
+        _check_dev("w.codes", w.codes, torch.uint8, dev)
+        _check_dev("w.scales", w.scales, torch.uint8, dev)
     if x.dim() != 2 or w.codes.dim() != 2:
         raise ValueError("x must be [M, K] and w.codes [N, K/2]")
     M, K = x.shape
@@ -800,7 +835,8 @@ def w4a16_linear(x: torch.Tensor, w: Quantized, out_dtype: torch.dtype = torch.b
     if K % block or w.codes.shape[1] * 2 != K or w.scales.shape != (N, K // block):
         raise ValueError(f"operand shapes do not match: x [M, K], w [N, K] with K % {block} == 0")
     if w.s2 is not None:
-        _check_dev("w.s2", w.s2, torch.float32, dev)
+        if not _fits(w.s2, torch.float32, index):
+            _check_dev("w.s2", w.s2, torch.float32, dev)
         if w.s2.numel() != 1:
             raise ValueError("w.s2 must hold one float")
     y = _w4_out(out, M, N, out_dtype, dev)

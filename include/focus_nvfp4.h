@@ -400,15 +400,17 @@ int64_t focus_nvfp4_linear_scratch_bytes(void);
  *               scale bytes 0x38, signed-zero codes).  hidden % 16 == 0.
  *   _mxfp8      per 32 elements S = 2^(floor(log2 max|y_b|) - 8) (the OCP
  *               Microscaling rule; exponent at least -127; a zero block:
- *               S = 1), stored as the E8M0 byte, exponent + 127, scales
+ *               S = 1; a block with an infinity or NaN: the byte 255, E8M0's
+ *               NaN), stored as the E8M0 byte, exponent + 127, scales
  *               [tokens, hidden/32]; codes [tokens, hidden] E4M3 of
  *               clamp(y / S, -448, 448).  hidden % 32 == 0.
  *   y_deq       [tokens, hidden] BF16 or NULL: the values of the stored
  *               codes, BF16((c*S)*s2) or BF16(c*S).
  * All row pointers are 16-byte aligned, s2_out 4-byte, codes 8-byte;
  * FOCUS_ERR_SHAPE for a hidden size that does not fit the format,
- * FOCUS_ERR_RANGE for tokens or hidden above 2^31.  Rows are independent: a
- * row of infinities or NaN changes no other row.  One kernel launch (for the
+ * FOCUS_ERR_RANGE for tokens or hidden above 2^31.  Rows are independent: an
+ * infinity or NaN changes no other row, and shows in its own (as NaN or
+ * infinity in a BF16 result, in s2, or as scale byte 255).  One kernel launch (for the
  * gated activation and the MXFP8 quantizer, one per 2^34 elements).
  *
  *   x, residual, residual_out  [tokens, hidden] BF16.  residual_out (NULL:
@@ -453,8 +455,9 @@ int focus_quantize_mxfp8(const uint16_t* x_bf16, int64_t tokens, int64_t hidden,
  *     Y[t, o] = sum_k (cx[t,k] * Sx[t, k/32]) * (cw[o,k] * Sw[o, k/32])
  * with MXFP8 activations (cx E4M3, Sx E8M0) and MXFP4 weights (cw E2M1, Sw
  * E8M0).
- *   x_codes  [M, K] E4M3 bytes (no NaN), x_scales [M, K/32], e.g. from
- *            focus_rmsnorm_mxfp8
+ *   x_codes  [M, K] E4M3 bytes, x_scales [M, K/32], e.g. from
+ *            focus_rmsnorm_mxfp8 (a scale byte 255 or a NaN code makes its
+ *            token's outputs NaN, and no others)
  *   w_codes  [N, K/2], w_scales [N, K/32], e.g. from focus_quantize_mx;
  *            scale bytes 0..254
  *   y        [M, N] row-major, FP32 (y_dtype 0) or BF16 (y_dtype 1)

@@ -85,10 +85,12 @@ def mxfp8(y):
     bm = np.abs(b).max(-1)
     _, ex = np.frexp(bm)
     e = np.where(bm == 0, 0, np.maximum(ex.astype(np.int64) - 9, -127))
+    e = np.where(np.isfinite(bm), e, 128)  # scale byte 255, NaN
     x = np.clip(np.ldexp(b.astype(np.float64), -e[..., None]), -448.0, 448.0)
     # x is a binary32 value or, below 2^-126, far under half the smallest code
     codes = torch.from_numpy(x.astype(np.float32)).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
     deq = bf16_round(np.ldexp(E4M3[codes], e[..., None]).astype(np.float32))
+    deq[e == 128] = np.nan
     return codes.reshape(t, h), (e + 127).astype(np.uint8), deq.reshape(t, h)
 
 

@@ -180,8 +180,28 @@ def test_norm_extreme_rows(focus):
     codes, scales, _ = ref.mxfp8(y)
     assert np.array_equal(got.codes[fin].cpu().numpy(), codes)
     assert np.array_equal(got.scales[fin].cpu().numpy(), scales)
+    # the bad rows show what they are: an infinity leaves NaN in its place (its
+    # row's root is infinite), a NaN everywhere
+    assert (got.scales[4] == 255).all() and torch.isnan(got.deq[4]).all()
+    assert got.scales[2, 0] == 255 and torch.isnan(got.deq[2, :32]).all() and (got.deq[2, 32:] == 0).all()
     out, _ = focus.rmsnorm(bad.to(DEV), w.to(DEV), EPS)
-    assert torch.isnan(out[4]).all()
+    assert torch.isnan(out[4]).all() and torch.isnan(out[2, 5])
+    q4, _ = focus.rmsnorm_nvfp4(bad.to(DEV), w.to(DEV), EPS)
+    assert torch.isnan(q4.s2[[2, 4]]).all() and torch.isfinite(q4.s2[keep + fin]).all()
+
+
+def test_silu_and_mxfp8_show_bad_values(focus):
+    g, u = _input(5, 256, 7), _input(5, 256, 8)
+    g[1, 40], u[2, 70], g[3, 3] = float("nan"), float("inf"), float("inf")
+    q = focus.silu_mul_mxfp8(g.to(DEV), u.to(DEV), dequant=True)
+    want = torch.zeros(5, 8, dtype=torch.bool)
+    want[1, 1] = want[2, 2] = want[3, 0] = True
+    assert torch.equal(q.scales.cpu() == 255, want)
+    assert torch.equal(torch.isnan(q.deq.float().view(5, 8, 32)).all(-1).cpu(), want)
+    s2 = focus.silu_mul_nvfp4(g.to(DEV), u.to(DEV)).s2
+    assert torch.equal(torch.isfinite(s2).cpu(), torch.tensor([True, False, False, False, True]))
+    x = focus.quantize_mxfp8(u.to(DEV))
+    assert (x.scales == 255).sum() == 1 and x.scales[2, 2] == 255
 
 
 # --------------------------------------------------------------------------

@@ -138,6 +138,11 @@ def test_bad_rows_stay_their_own(focus, fmt, M, N):
         x = c.x.clone()
         x[bad, 40] = float("nan")
     y = c.call(x, c.w, out_dtype=torch.float32, out=buf[:M])
+    if fmt == "mx":  # a NaN scale does the same
+        scales = c.x.scales.clone()
+        scales[bad, 1] = 255
+        z = c.call(focus.Quantized(c.x.codes, scales, None, None), c.w, out_dtype=torch.float32)
+        assert torch.isnan(z[bad]).all() and torch.isfinite(z).sum() == (M - 1) * N
     torch.cuda.synchronize()
     keep = [i for i in range(M) if i != bad]
     assert torch.equal(y[keep], clean[keep])
