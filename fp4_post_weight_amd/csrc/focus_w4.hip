@@ -436,24 +436,27 @@ __device__ __forceinline__ int scale_at(int r, int g) { return 4 * (((r >> 6) * 
 // Workgroup -> tile: workgroups are dealt to the 8 XCDs in turn, so each XCD
 // takes a contiguous range of tiles, in columns of `kGroupM` token tiles, and
 // its L2 holds few rows of both operands at a time.
-constexpr int64_t kXcds = 8, kGroupM = 4;
+constexpr uint32_t kXcds = 8, kGroupM = 4;
 
 struct TilePos {
     int64_t m, n;
 };
 
-__device__ __forceinline__ TilePos tile_of(int64_t bid, int64_t tiles_m, int64_t tiles_n) {
-    const int64_t total = tiles_m * tiles_n;
-    const int64_t q = total / kXcds, r = total % kXcds, xcd = bid % kXcds;
-    const int64_t tile = xcd * q + (xcd < r ? xcd : r) + bid / kXcds;
-    const int64_t group = tile / (kGroupM * tiles_n), in = tile % (kGroupM * tiles_n);
-    const int64_t first = group * kGroupM;
-    const int64_t gm = tiles_m - first < kGroupM ? tiles_m - first : kGroupM;
-    return {first + in % gm, in / gm};
+__device__ __forceinline__ TilePos tile_of(uint32_t bid, uint32_t tiles_m, uint32_t tiles_n) {
+    const uint32_t total = tiles_m * tiles_n;
+    const uint32_t q = total / kXcds, r = total % kXcds, xcd = bid % kXcds;
+    const uint32_t tile = xcd * q + (xcd < r ? xcd : r) + bid / kXcds;
+    const uint32_t full = tiles_m / kGroupM * tiles_n;  // columns of kGroupM tiles
+    if (tile / kGroupM < full) {
+        const uint32_t c = tile / kGroupM;
+        return {(int64_t)(c / tiles_n) * kGroupM + tile % kGroupM, c % tiles_n};
+    }
+    const uint32_t in = tile - full * kGroupM, gm = tiles_m % kGroupM;
+    return {(int64_t)(tiles_m - gm) + in % gm, in / gm};
 }
 
 template <int KIND, int KS, int BM, int BN, int WM, int WN, bool BF16_OUT>
-__global__ __launch_bounds__(64 * WM * WN) void k_w4_tiled(W4Args a, int64_t tiles_m, int64_t tiles_n) {
+__global__ __launch_bounds__(64 * WM * WN) void k_w4_tiled(W4Args a, uint32_t tiles_m, uint32_t tiles_n) {
     constexpr bool kMx = KIND == kW4Mx, kNv = KIND == kW4Bf16Nvfp4;
     constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
     constexpr int TM = BM / WM / 16, TN = BN / WN / 16;                          // 16 x 16 subtiles per wavefront
@@ -721,6 +724,334 @@ __global__ __launch_bounds__(64 * WM * WN) void k_w4_tiled(W4Args a, int64_t til
     }
 }
 
+// Stores a wavefront's accumulators: register r of lane (c16, g) in acc[j][i] is
+// column n0 + 16 j + 4 g + r of token m0 + 16 i (m0 includes c16), or with PAIR,
+// whose W rows are ordered by w_row, column n0 + 32 (j / 2) + 8 g + 4 (j % 2) + r.
+// wide: rows of y start at multiples of 16 bytes; whole: all of it is in range.
+template <int TM, int TN, bool BF16_OUT>
+__device__ __forceinline__ void store_tile(f32x4 (&acc)[TN][TM], const W4Args& a, int64_t m0, int64_t n0, int g, float s2,
+                                           bool wide, bool whole) {
+    constexpr int C = BF16_OUT ? 2 : 1;  // subtiles per store
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        const int64_t row = m0 + 16 * i;
+        if (!whole && row >= a.M) continue;
+#pragma unroll
+        for (int j = 0; j < TN; j += C) {
+            const int64_t col = n0 + 16 * j + 4 * C * g;
+            f32x4 v[C];
+#pragma unroll
+            for (int b = 0; b < C; ++b) v[b] = acc[j + b][i] * s2;
+            if (whole || (wide && col < a.N)) {
+                if constexpr (BF16_OUT) {
+                    const u32x4 p = {bf16_pair(v[0][0], v[0][1]), bf16_pair(v[0][2], v[0][3]),
+                                     bf16_pair(v[C - 1][0], v[C - 1][1]), bf16_pair(v[C - 1][2], v[C - 1][3])};
+                    __builtin_nontemporal_store(p, reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(a.y) + row * a.N + col));
+                }
+                else
+                    __builtin_nontemporal_store(v[0], reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.y) + row * a.N + col));
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4 * C; ++r) {
+                    if (col + r >= a.N) break;
+                    if constexpr (BF16_OUT)
+                        reinterpret_cast<uint16_t*>(a.y)[row * a.N + col + r] =
+                            (uint16_t)(bf16_pair(v[r / 4][r % 4], 0.0f) & 0xFFFFu);
+                    else
+                        reinterpret_cast<float*>(a.y)[row * a.N + col + r] = v[0][r];
+                }
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Many tokens and columns, K % KS == 0: tiles of 256 x 256, one workgroup of
+// eight wavefronts per CU, which takes tile after tile without a pause.
+//
+// Wavefronts w and w + 4 share a SIMD.  A wavefront alternates between reading
+// all fragments of a step (and starting transfers) and multiplying them, with a
+// barrier after each; wavefronts 4..7 run one barrier behind, so that on every
+// SIMD one wavefront multiplies while the other reads.  The steps of all tiles
+// of a workgroup are one sequence: a tile's results are stored, and its first
+// transfers started, in reading phases under the other half's products.
+//
+//   phase      2s - 1      2s          2s + 1      2s + 2
+//   w 0..3     read s      multiply s  read s + 1  multiply s + 1
+//   w 4..7     multiply .  read s      multiply s  read s + 1
+//
+// Transfers of step s + 2 start in the reading phase of step s, into the stage
+// of s - 1, which the other half has read a phase before; they have landed when
+// the reading phase of step s + 1 ends, which is before either half reads them.
+// Scales come 16 bytes per row, that is 4 or 8 steps at a time (a row's bytes
+// of one step would cost a cache line each time), by way of a register.  BF16
+// activations: of the W fragments only the first 16 columns are widened in the
+// reading phase, the rest between the products that do not need them yet.
+//
+// Measured against the same tile with one barrier per step and fragments read
+// under a wavefront's own products (k_w4_tiled), us: MXFP8 8192 x 14336 x 4096 366
+// against 473, 2.63 PFLOP/s; BF16 4096 x 14336 x 4096 405 against 471 (NVFP4, 1.19
+// PFLOP/s), 361 against 446 (MXFP4, 1.33).  MXFP8: 331 if nothing is stored; the
+// products alone would take 243 (the clock falls under them: 4.9 PFLOP/s on zeros,
+// 4.0 on random codes).
+// ---------------------------------------------------------------------------
+
+// A barrier alone (the waits stand before it); nothing moves across it.
+__device__ __forceinline__ void phase_barrier() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// The W row of a 64-column segment that lies at position t of the segment.  For
+// BF16 results a lane's accumulators of two subtiles are then 8 neighbouring
+// columns, and 4 lanes write 64 bytes in a row; 32-bit results do that as it is.
+template <bool BF16_OUT>
+__device__ __forceinline__ int w_row(int t) {
+    return BF16_OUT ? (t & ~31) | (t & 12) << 1 | (t >> 2 & 4) | (t & 3) : t;
+}
+
+template <int KIND, bool BF16_OUT>
+__global__ __launch_bounds__(512) void k_w4_big(W4Args a, uint32_t tiles_m, uint32_t tiles_n) {
+    constexpr bool kMx = KIND == kW4Mx, kNv = KIND == kW4Bf16Nvfp4;
+    constexpr int BM = 256, BN = 256, TM = 8, TN = 4;  // subtiles of 16 x 16 per wavefront
+    constexpr int KS = kMx ? 128 : 64, kXRow = 128, kWRow = KS / 2;
+    constexpr int kXInst = BM * kXRow / 8192, kWInst = BN * kWRow / 8192;  // transfers per wavefront and step
+    constexpr int kWPer = kWRow / 16;
+    constexpr int kXBytes = BM * kXRow, kStage = kXBytes + BN * kWRow;
+    constexpr int kSb = kNv ? KS / 16 : KS / 32, kChunk = 16 / kSb;  // a row's scale bytes of a step; steps in 16 bytes
+    constexpr int kSRows = (kMx ? BM : 0) + BN, kSBytes = kSRows * 16;
+    constexpr int kStores = BF16_OUT ? TM * TN / 2 : TM * TN;
+    typedef u32x4 u32x4_a1 __attribute__((aligned(1)));
+    __shared__ __attribute__((aligned(256))) uint8_t lds[3 * kStage + 2 * kSBytes];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int half = wave >> 2;
+    const int c16 = lane & 15, g = lane >> 4;
+    const uint32_t total = tiles_m * tiles_n;
+    const int K = (int)a.K, n = K / KS, nb = K / (kNv ? 16 : 32);
+
+    // What is transferred next: step ls of tile lt.  Offsets are from the tile's
+    // first row (32 bits: K <= kMaxW4K).  Rows past the operand's end read its
+    // last row and feed outputs that are never stored.
+    uint32_t lt = blockIdx.x;
+    int ls = 0;
+    const uint8_t *xbase, *wbase, *sbase;
+    uint32_t xoff[kXInst], woff[kWInst], soff;
+    auto source = [&]() {
+        const TilePos pos = tile_of(lt, tiles_m, tiles_n);
+        const int64_t m0 = pos.m * BM, n0 = pos.n * BN;
+        const int mlast = (int)(a.M - 1 - m0 < BM ? a.M - 1 - m0 : BM), nlast = (int)(a.N - 1 - n0 < BN ? a.N - 1 - n0 : BN);
+        xbase = a.x + m0 * K * (kMx ? 1 : 2);
+        wbase = a.wc + n0 * (K / 2);
+#pragma unroll
+        for (int i = 0; i < kXInst; ++i) {
+            const int row = (wave * kXInst + i) * 8 + lane / 8;
+            xoff[i] = (uint32_t)min(row, mlast) * (uint32_t)(K * (kMx ? 1 : 2)) + 16 * ((lane & 7) ^ (row & 7));
+        }
+#pragma unroll
+        for (int i = 0; i < kWInst; ++i) {
+            const int t = (wave * kWInst + i) * (64 / kWPer) + lane / kWPer;
+            woff[i] = (uint32_t)min(w_row<BF16_OUT>(t), nlast) * (uint32_t)(K / 2) +
+                      16 * ((lane % kWPer) ^ (kMx ? (t >> 1) & 3 : 0));
+        }
+        const bool sx = kMx && wave < 4;
+        sbase = sx ? a.xs + m0 * nb : a.ws + n0 * nb;
+        soff = (uint32_t)(sx ? min(tid, mlast) : min(w_row<BF16_OUT>(tid & 255), nlast)) * (uint32_t)nb;
+    };
+    // 16 scale bytes of the thread's row, of step ls and those behind it (the
+    // row's last 16 where fewer are left)
+    u32x4 sreg = {};
+    auto load_scales = [&]() { sreg = *reinterpret_cast<const u32x4_a1*>(sbase + min(ls * kSb, nb - 16) + soff); };
+    auto transfer = [&](uint32_t stage) {
+        const uint8_t* xb = xbase + (int64_t)ls * kXRow;
+        const uint8_t* wb = wbase + (int64_t)ls * kWRow;
+#pragma unroll
+        for (int i = 0; i < kXInst; ++i) to_lds16(xb, xoff[i], stage + (wave * kXInst + i) * 1024);
+#pragma unroll
+        for (int i = 0; i < kWInst; ++i) to_lds16(wb, woff[i], stage + kXBytes + (wave * kWInst + i) * 1024);
+        if (++ls == n) {
+            ls = 0;
+            lt += gridDim.x;
+            if (lt < total) source();
+        }
+    };
+    // Chunks of scales alternate between two areas.
+    uint8_t* const scales = lds + 3 * kStage;
+    int filled = 0;
+    auto store_scales = [&]() {
+        if (kSRows == 512 || tid < kSRows) *reinterpret_cast<u32x4*>(scales + filled * kSBytes + tid * 16) = sreg;
+        filled ^= 1;
+    };
+
+    // Fragments of a step.  MXFP8: the lane's W piece is logical block g, its X
+    // halves are pieces g and 4 + g.  BF16: k = 16 g .. of the step.
+    const int mrow = half * 128, nrow = (wave & 3) * 64;
+    const int xat = (mrow + c16) * kXRow + 16 * ((kMx ? g : 2 * g) ^ (c16 & 7)), xother = kMx ? 64 : 16;
+    const int wat = kXBytes + (nrow + c16) * kWRow + (kMx ? 16 * (g ^ ((c16 >> 1) & 3)) : 8 * g);
+    const int sg = kSb == 2 ? g >> 1 : g;
+    const int sxat = (mrow + c16) * 16 + sg, swat = ((kMx ? BM : 0) + nrow + c16) * 16 + sg;
+    uint4 w[kMx ? TN : 1], x[TM][2];
+    uint32_t ws[TN], xs[kMx ? TM : 1];
+    bf16x8 wv[kMx ? 1 : TN][2];
+    auto read_x = [&](const uint8_t* st, const uint8_t* sc) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            x[i][0] = *reinterpret_cast<const uint4*>(st + xat + i * 16 * kXRow);
+            x[i][1] = *reinterpret_cast<const uint4*>(st + (xat ^ xother) + i * 16 * kXRow);
+            if constexpr (kMx) xs[i] = sc[sxat + i * 256];
+        }
+    };
+    uint2 wc[kMx ? 1 : TN];
+    auto read_w = [&](const uint8_t* st, const uint8_t* sc) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            if constexpr (kMx)
+                w[j] = *reinterpret_cast<const uint4*>(st + wat + j * 16 * kWRow);
+            else
+                wc[j] = *reinterpret_cast<const uint2*>(st + wat + j * 16 * kWRow);
+            ws[j] = sc[swat + j * 256];
+        }
+    };
+    auto widen = [&](int from, int to) {
+        if constexpr (!kMx) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                if (j < from || j >= to) continue;
+                const float s = kNv ? e4m3_f32(ws[j]) : e8m0_f32(ws[j]);
+                wv[j][0] = kNv ? widen_nv(wc[j].x, s) : widen_mx(wc[j].x, s);
+                wv[j][1] = kNv ? widen_nv(wc[j].y, s) : widen_mx(wc[j].y, s);
+            }
+        }
+    };
+    f32x4 acc[TN][TM];
+    auto clear = [&]() {
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int i = 0; i < TM; ++i) acc[j][i] = (f32x4){};
+    };
+    auto products = [&]() {
+        if constexpr (kMx) {
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    acc[j][i] = mfma_tile<0, 0>(w[j], x[i][0], x[i][1], ws[j], xs[i], acc[j][i]);
+        } else {
+            // columns 16 .. 63 are widened under the first columns' products
+            widen(1, TN);
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[j][q], __builtin_bit_cast(bf16x8, x[i][q]),
+                                                                            acc[j][i], 0, 0, 0);
+        }
+    };
+    // Stores tile t; whether exactly kStores instructions did it.
+    const float s2w = kNv ? a.ws2[0] : 1.0f;
+    const bool wide = (BF16_OUT ? a.N % 8 == 0 : a.N % 4 == 0) && ((uintptr_t)a.y & 15) == 0;
+    auto store = [&](uint32_t t) {
+        const TilePos pos = tile_of(t, tiles_m, tiles_n);
+        const int64_t m0 = pos.m * BM + mrow, n0 = pos.n * BN + nrow;
+        const bool whole = wide && m0 + 128 <= a.M && n0 + 64 <= a.N;
+        store_tile<TM, TN, BF16_OUT>(acc, a, m0 + c16, n0, g, s2w, wide, whole);
+        return whole;
+    };
+
+    uint8_t *s0 = lds, *s1 = lds + kStage, *s2 = lds + 2 * kStage;
+    source();
+    load_scales();
+    transfer(lds_address(s0));
+    store_scales();
+    bool chunk = false;  // a chunk of scales is in registers
+    if (lt < total) {
+        if (ls % kChunk == 0) {
+            load_scales();
+            chunk = true;
+        }
+        transfer(lds_address(s1));
+    }
+    wait_transfers();
+    clear();
+    __syncthreads();
+    if (half) phase_barrier();
+    int used = 1;  // the area of the present chunk
+    uint32_t before = blockIdx.x;
+    for (uint32_t t = blockIdx.x; t < total; t += gridDim.x) {
+        for (int s = 0; s < n; ++s) {
+            bool counted = false;
+            if (s == 0 && t != before) {
+                counted = store(before);
+                clear();
+            }
+            if (s % kChunk == 0) used ^= 1;
+            if (chunk) store_scales();
+            chunk = false;
+            const bool more = lt < total;
+            if (more && ls % kChunk == 0) {
+                load_scales();
+                chunk = true;
+            }
+            const uint8_t* const sc = scales + used * kSBytes + s * kSb - min((s - s % kChunk) * kSb, nb - 16);
+            __builtin_amdgcn_sched_barrier(0);
+            if (!kMx) read_w(s0, sc);  // widened while the rest comes
+            __builtin_amdgcn_sched_barrier(0);
+            if (more) transfer(lds_address(s2));
+            __builtin_amdgcn_sched_barrier(0);
+            if (kMx) read_w(s0, sc);
+            read_x(s0, sc);
+            widen(0, 1);
+            __builtin_amdgcn_sched_barrier(0);
+            // step s + 1 has landed; what came after it may be under way
+            if (!more)
+                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+            else if (counted)
+                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kXInst + kWInst + kStores) : "memory");
+            else
+                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kXInst + kWInst) : "memory");
+            phase_barrier();
+            __builtin_amdgcn_s_setprio(1);
+            products();
+            __builtin_amdgcn_s_setprio(0);
+            phase_barrier();
+            uint8_t* const free = s0;
+            s0 = s1;
+            s1 = s2;
+            s2 = free;
+        }
+        before = t;
+    }
+    if (!half) phase_barrier();
+    store(before);
+}
+
+// Whole steps, and 16 scale bytes per row.
+template <int KIND>
+bool big_fits(int64_t K) {
+    return K % (KIND == kW4Mx ? 128 : 64) == 0 && K >= (KIND == kW4Bf16Nvfp4 ? 256 : 512);
+}
+
+template <int KIND, bool BF16_OUT>
+hipError_t run_big(const W4Args& args, int64_t cus, hipStream_t stream) {
+    const int64_t tiles_n = (args.N + 255) / 256;
+    const int64_t most = ((int64_t)1 << 30) / tiles_n;  // token tiles of a launch: 32-bit tile numbers
+    for (int64_t row = 0; row < args.M; row += most * 256) {
+        const W4Args a = rows_from<KIND, BF16_OUT>(args, row, most * 256);
+        const int64_t tiles_m = (a.M + 255) / 256;
+        const int64_t grid = tiles_m * tiles_n < cus ? tiles_m * tiles_n : cus;
+        const hipError_t e = launch(&k_w4_big<KIND, BF16_OUT>, dim3((unsigned)grid), dim3(512), stream, a,
+                                    (uint32_t)tiles_m, (uint32_t)tiles_n);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 template <int KIND, int KS, int BM, int BN, int WM, int WN, bool BF16_OUT>
 hipError_t run_tiled(const W4Args& args, hipStream_t stream) {
     const int64_t tiles_n = (args.N + BN - 1) / BN;
@@ -731,7 +1062,7 @@ hipError_t run_tiled(const W4Args& args, hipStream_t stream) {
         const W4Args a = rows_from<KIND, BF16_OUT>(args, row, most * BM);
         const int64_t tiles_m = (a.M + BM - 1) / BM;
         const hipError_t e = launch(&k_w4_tiled<KIND, KS, BM, BN, WM, WN, BF16_OUT>, dim3((unsigned)(tiles_m * tiles_n)),
-                                    dim3(64 * WM * WN), stream, a, tiles_m, tiles_n);
+                                    dim3(64 * WM * WN), stream, a, (uint32_t)tiles_m, (uint32_t)tiles_n);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
@@ -800,8 +1131,9 @@ inline int64_t tiles(const W4Args& a, int bm, int bn) { return ((a.M + bm - 1) /
 // which moves the fewest bytes per product.  Measured (us): 100 x 4096 x 4096
 // with tiles of 32 x 64, 64 x 64, 64 x 64 in shorter steps (two workgroups per
 // CU), 128 x 128: 10.4, 11.9, 15.2, 27; 100 x 14336 x 4096: 28, 22.4, 17.3, 27.9;
-// 512 x 14336 x 4096, the last two, 256 x 128 and 256 x 256: 59, 44.4, 42.1, 59.6;
-// 8192 x 14336 x 4096, the last three: 579, 600, 444.
+// 512 x 14336 x 4096, the last two, 256 x 128 and 256 x 256: 60, 45.2, 42.7, 47.1;
+// 1024 x 14336 x 4096: 106, 82, 80, 53; 8192 x 14336 x 4096, the last three: 579, 600,
+// 366.  Lengths that the last kernel does not take go to its one-barrier form.
 template <bool BF16_OUT>
 hipError_t pick_mx(const W4Args& a, int64_t cus, hipStream_t stream) {
     if (a.M <= kDecodeOneTile) return decode_16<kW4Mx, BF16_OUT>(a, cus, stream);
@@ -811,13 +1143,14 @@ hipError_t pick_mx(const W4Args& a, int64_t cus, hipStream_t stream) {
     if (tiles(a, 64, 64) <= 2 * cus) return run_tiled<kW4Mx, 256, 64, 64, 2, 2, BF16_OUT>(a, stream);
     if (tiles(a, 128, 128) <= cus) return run_tiled<kW4Mx, 128, 128, 128, 2, 2, BF16_OUT>(a, stream);
     if (tiles(a, 256, 128) <= cus) return run_tiled<kW4Mx, 128, 256, 128, 4, 2, BF16_OUT>(a, stream);
+    if (big_fits<kW4Mx>(a.K)) return run_big<kW4Mx, BF16_OUT>(a, cus, stream);
     return run_tiled<kW4Mx, 128, 256, 256, 2, 4, BF16_OUT>(a, stream);
 }
 
 // BF16 activations, by the same rule (NVFP4, us): 61 x 4096 x 4096 with tiles of
 // 32 x 32 and 32 x 64: 16.5, 16.8; 61 x 6144 x 4096: 19.1, 17.2; 128 x 14336 x 4096
-// with 32 x 64 and 64 x 128: 41, 31.5; 512 x 28672 x 8192 with 64 x 128 and
-// 256 x 256: 315, 239, but 512 x 14336 x 4096: 87, 108 -- the middle tile keeps
+// with 32 x 64 and 64 x 128: 41, 31.5; 1024 x 14336 x 4096 with 64 x 128 and
+// 256 x 256: 154, 106, but 512 x 14336 x 4096: 87, 90 -- the middle tile keeps
 // two workgroups per CU and stays ahead for two rounds of them.  The tiles'
 // transfers of 16 bytes want K % 32 == 0.
 template <int KIND, bool BF16_OUT>
@@ -828,6 +1161,7 @@ hipError_t pick_bf16(const W4Args& a, int64_t cus, hipStream_t stream) {
     if (tiles(a, 32, 32) <= cus) return run_tiled<KIND, 256, 32, 32, 1, 2, BF16_OUT>(a, stream);
     if (tiles(a, 32, 64) <= 2 * cus) return run_tiled<KIND, 256, 32, 64, 1, 4, BF16_OUT>(a, stream);
     if (tiles(a, 64, 128) <= 4 * cus) return run_tiled<KIND, 128, 64, 128, 1, 4, BF16_OUT>(a, stream);
+    if (big_fits<KIND>(a.K)) return run_big<KIND, BF16_OUT>(a, cus, stream);
     return run_tiled<KIND, 64, 256, 256, 2, 4, BF16_OUT>(a, stream);
 }
 

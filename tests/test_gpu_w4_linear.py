@@ -240,3 +240,60 @@ def test_another_stream_and_graph(focus, fmt):
         torch.cuda.synchronize()
         for a, b in zip(eager, caught):
             assert torch.equal(a, b)
+
+
+# More 256 x 256 tiles than compute units: workgroups take several in turn.
+# Column edges inside a store, a last chunk of scale bytes that overlaps the one
+# before, one chunk only, and lengths that are whole steps for BF16
+# activations alone (832) or for none (736).
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,N,K", [(2100, 9100, 640), (2100, 9103, 832), (4400, 5000, 512), (4360, 4376, 1664), (3000, 6000, 736)])
+def test_many_tiles(focus, fmt, M, N, K):
+    c = Case(focus, fmt, M, N, K, seed=K, exact=True)
+    buf = torch.full((M + 1, N), 7.0, device=DEV)
+    y = c.call(c.x, c.w, out_dtype=torch.float32, out=buf[:M])
+    assert np.array_equal(y.cpu().double().numpy(), c.want)
+    assert (buf[M] == 7.0).all()
+    h = c.call(c.x, c.w, out_dtype=torch.bfloat16)
+    assert torch.equal(h.cpu(), torch.from_numpy(c.want).to(torch.bfloat16))
+    # a result that starts 4 bytes off a multiple of 16
+    off = torch.full((M * N + 8,), 7.0, device=DEV)
+    z = c.call(c.x, c.w, out_dtype=torch.float32, out=off[1:1 + M * N].view(M, N))
+    assert torch.equal(z, y)
+    assert off[0] == 7.0 and (off[1 + M * N:] == 7.0).all()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        caught = c.call(c.x, c.w, out_dtype=torch.bfloat16)
+    for _ in range(3):
+        caught.fill_(float("nan"))
+        c.call(c.x, c.w, out_dtype=torch.float32)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(caught, h)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_many_tiles_spread(focus, fmt):
+    """Scales and values over their range, and a bad row."""
+    M, N, K = 2100, 8500, 640
+    c = Case(focus, fmt, M, N, K, seed=77)
+    rows = np.r_[0:M:67, M - 20:M]  # the bounds of these
+    c.xv, c.want = c.xv[rows], c.want[rows]
+    if fmt == "mx":
+        c.xc, c.xs = c.xc[rows], c.xs[rows]
+    for dtype in (torch.float32, torch.bfloat16):
+        c.check(c.call(c.x, c.w, out_dtype=dtype)[torch.from_numpy(rows).to(DEV)], dtype)
+    y = c.call(c.x, c.w, out_dtype=torch.float32)
+    bad = 1801
+    if fmt == "mx":
+        scales = c.x.scales.clone()
+        scales[bad, K // 32 - 1] = 255
+        x = focus.Quantized(c.x.codes, scales, None, None)
+    else:
+        x = c.x.clone()
+        x[bad, K - 1] = float("nan")
+    z = c.call(x, c.w, out_dtype=torch.float32)
+    assert torch.isnan(z[bad]).all()
+    z[bad] = y[bad]
+    assert torch.equal(z, y)
