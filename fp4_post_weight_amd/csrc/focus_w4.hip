@@ -31,6 +31,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "focus_gemm.h"
 #include "focus_launch.h"
 #include "focus_numerics.h"
@@ -347,26 +349,30 @@ W4Args rows_from(const W4Args& args, int64_t row, int64_t most) {
 }
 
 // ---------------------------------------------------------------------------
-// Many tokens: tiles of BM tokens x BN columns, k in steps of KS, three stages
-// in LDS.  Codes go from memory to LDS without passing through registers (16
-// bytes per lane).  Rows are stored unpadded (the transfer writes lane after
+// Many tokens: tiles of BM tokens x BN columns, k in steps of KS, a ring of
+// stages in LDS.  Codes go from memory to LDS without passing through registers
+// (16 bytes per lane).  Rows are stored unpadded (the transfer writes lane after
 // lane) and their 16-byte pieces permuted by the row, so that the fragment
 // reads of neighbouring rows cover all banks: piece p of row r lies at
 // p ^ (r mod the row's pieces, at most 16), in a 64-byte W row at
 // p ^ ((r >> 1) & 3); the transferring lane picks its global address
-// accordingly.  The scale bytes of a row's step are loaded a step ahead into a
-// register of the thread that owns the row.
+// accordingly.
+//
+// STAGES > 0: K is a multiple of KS, the scale bytes are transferred likewise, 4
+// per lane, and a wavefront waits by count, so that STAGES - 2 steps are under
+// way.  STAGES = 0: any K; three stages, the scale bytes of a row's step loaded a
+// step ahead into a register of the thread that owns the row, and a last step
+// begun only is filled up with zeros.
 //
 // A step has two halves around its one barrier, which says that every
 // wavefront has left step s - 1 and that the data of step s + 1 are in LDS.
-// After it the transfer of step s + 2 starts, into the stage of s - 1, and has
-// a whole step to land; the W fragments of step s + 1 and its first X
-// fragments are read while the second half's products run, and X fragments
-// come `kAhead` subtiles ahead of their products throughout.
+// After it the next transfer starts, into the stage of s - 1; the W fragments of
+// step s + 1 and its first X fragments are read while the second half's products
+// run, and X fragments come `kAhead` subtiles ahead of their products throughout.
 //
-// Small tiles take long steps: what a step costs beside its products (the
-// barrier, the first fragments' latency, the transfer's instructions) is then
-// spread over more of k, and more bytes are on their way.
+// Small tiles give each SIMD too little to hide those reads behind.  They take
+// long steps, and WK wavefronts share an output tile: each multiplies 1 / WK of
+// every step, and at the end the first adds the others' sums in order.
 //
 // W is the first operand of the product, so that a lane's four accumulators
 // are four neighbouring columns of one token.
@@ -380,7 +386,7 @@ __device__ __forceinline__ uint32_t lds_address(const uint8_t* p) {
 
 // 16 bytes per lane from base + offset to LDS at `dst` + 16 * lane (dst and
 // base uniform).  The instruction has no register result, and its address
-// registers are read when it issues; it is complete after wait_transfers().
+// registers are read when it issues; it is complete after wait_transfers<0>().
 // Written out because the compiler, which cannot tell the stages apart, would
 // wait for every transfer before any LDS read.  m0 holds nothing of the
 // compiler's here: no other instruction of these kernels reads it.
@@ -394,7 +400,23 @@ __device__ __forceinline__ void to_lds16(const uint8_t* base, uint32_t offset, u
         : "memory");
 }
 
-__device__ __forceinline__ void wait_transfers() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// 4 bytes per lane, likewise; to `dst` + 4 * lane.
+__device__ __forceinline__ void to_lds4(const uint8_t* base, uint32_t offset, uint32_t dst) {
+    asm volatile(
+        "s_mov_b32 m0, %0\n\t"
+        "s_nop 0\n\t"
+        "global_load_lds_dword %1, %2"
+        :
+        : "s"(dst), "v"(offset), "s"(base)
+        : "memory");
+}
+
+// All but this wavefront's last N have landed (they do so in order).
+template <int N>
+__device__ __forceinline__ void wait_transfers() {
+    static_assert(N <= 63, "the counter's range");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
 
 // The block-scaled product of W subtile j and X subtile i, whose scales are
 // bytes SW and SX of ws and xs.
@@ -455,10 +477,70 @@ __device__ __forceinline__ TilePos tile_of(uint32_t bid, uint32_t tiles_m, uint3
     return {(int64_t)(tiles_m - gm) + in % gm, in / gm};
 }
 
-template <int KIND, int KS, int BM, int BN, int WM, int WN, bool BF16_OUT>
-__global__ __launch_bounds__(64 * WM * WN) void k_w4_tiled(W4Args a, uint32_t tiles_m, uint32_t tiles_n) {
+// The W row of a wavefront's columns that lies at position t of them.  For BF16
+// results (PAIR) a lane's accumulators of two subtiles are then 8 neighbouring
+// columns, and 4 lanes write 64 bytes in a row; 32-bit results do that as it is.
+template <bool PAIR>
+__device__ __forceinline__ int w_row(int t) {
+    return PAIR ? (t & ~31) | (t & 12) << 1 | (t >> 2 & 4) | (t & 3) : t;
+}
+
+// Stores a wavefront's accumulators: register r of lane (c16, g) in acc[j][i] is
+// column n0 + 16 j + 4 g + r of token m0 + 16 i (m0 includes c16), or with PAIR
+// column n0 + 32 (j / 2) + 8 g + 4 (j % 2) + r.  wide: a lane's columns are
+// aligned in y and all present or all absent; whole: all of it is in range.
+template <int TM, int TN, bool BF16_OUT, bool PAIR>
+__device__ __forceinline__ void store_tile(f32x4 (&acc)[TN][TM], const W4Args& a, int64_t m0, int64_t n0, int g, float s2,
+                                           bool wide, bool whole) {
+    constexpr int C = PAIR ? 2 : 1;  // subtiles per store
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        const int64_t row = m0 + 16 * i;
+        if (!whole && row >= a.M) continue;
+#pragma unroll
+        for (int j = 0; j < TN; j += C) {
+            const int64_t col = n0 + 16 * j + 4 * C * g;
+            f32x4 v[C];
+#pragma unroll
+            for (int b = 0; b < C; ++b) v[b] = acc[j + b][i] * s2;
+            if (whole || (wide && col < a.N)) {
+                uint16_t* const h = reinterpret_cast<uint16_t*>(a.y) + row * a.N + col;
+                if constexpr (PAIR) {
+                    const u32x4 p = {bf16_pair(v[0][0], v[0][1]), bf16_pair(v[0][2], v[0][3]),
+                                     bf16_pair(v[C - 1][0], v[C - 1][1]), bf16_pair(v[C - 1][2], v[C - 1][3])};
+                    __builtin_nontemporal_store(p, reinterpret_cast<u32x4*>(h));
+                } else if constexpr (BF16_OUT) {
+                    *reinterpret_cast<uint2*>(h) = make_uint2(bf16_pair(v[0][0], v[0][1]), bf16_pair(v[0][2], v[0][3]));
+                } else {
+                    __builtin_nontemporal_store(v[0], reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.y) + row * a.N + col));
+                }
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4 * C; ++r) {
+                    if (col + r >= a.N) break;
+                    if constexpr (BF16_OUT)
+                        reinterpret_cast<uint16_t*>(a.y)[row * a.N + col + r] =
+                            (uint16_t)(bf16_pair(v[r / 4][r % 4], 0.0f) & 0xFFFFu);
+                    else
+                        reinterpret_cast<float*>(a.y)[row * a.N + col + r] = v[0][r];
+                }
+            }
+        }
+    }
+}
+
+// store_tile's `wide`
+template <bool BF16_OUT, bool PAIR>
+__device__ __forceinline__ bool wide_rows(const W4Args& a) {
+    return a.N % (PAIR ? 8 : 4) == 0 && ((uintptr_t)a.y & (BF16_OUT && !PAIR ? 7 : 15)) == 0;
+}
+
+template <int KIND, int KS, int BM, int BN, int WM, int WN, int WK, int STAGES, bool BF16_OUT>
+__global__ __launch_bounds__(64 * WM * WN * WK) void k_w4_tiled(W4Args a, uint32_t tiles_m, uint32_t tiles_n) {
     constexpr bool kMx = KIND == kW4Mx, kNv = KIND == kW4Bf16Nvfp4;
-    constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+    constexpr int kWaves = WM * WN * WK, kThreads = 64 * kWaves;
+    constexpr bool kDirect = STAGES > 0;                                          // whole steps; scales transferred too
+    constexpr int kStages = kDirect ? STAGES : 3;
     constexpr int TM = BM / WM / 16, TN = BN / WN / 16;                          // 16 x 16 subtiles per wavefront
     constexpr int kXRow = kMx ? KS : 2 * KS, kWRow = KS / 2;                     // bytes of a row's step
     constexpr int kXPer = kXRow / 16, kWPer = kWRow / 16;                        // 16-byte pieces of it
@@ -466,16 +548,23 @@ __global__ __launch_bounds__(64 * WM * WN) void k_w4_tiled(W4Args a, uint32_t ti
     constexpr int kXInst = BM * kXRow / 1024 / kWaves, kWInst = BN * kWRow / 1024 / kWaves;  // transfers per wavefront
     constexpr int kBlock = kNv ? 16 : 32, kSb = KS / kBlock;                     // scale bytes of a row's step
     constexpr int kSRows = (kMx ? BM : 0) + BN;                                  // rows that have scales
-    constexpr int kXBytes = BM * kXRow, kWBytes = BN * kWRow, kStageBytes = kXBytes + kWBytes + kSRows * kSb;
-    constexpr int NJ = KS >= 128 ? KS / 128 : 1;                                 // W pieces per lane and subtile
-    constexpr int NP = kMx ? 2 * NJ : KS / 32;                                   // X pieces per lane and subtile
-    constexpr bool kGroup = kMx && KS == 128 && TM % 4 == 0 && TN % 4 == 0;      // scale_at
-    constexpr int kLaneSb = kMx ? NJ : (kSb >= 4 ? kSb / 4 : 1);                 // scale bytes per lane and subtile
+    constexpr int kXBytes = BM * kXRow, kWBytes = BN * kWRow, kSInst = kDirect ? (kSRows * kSb + 256 * kWaves - 1) / (256 * kWaves) : 0;
+    constexpr int kStageBytes = kXBytes + kWBytes + (kDirect ? kSInst * kWaves * 256 : kSRows * kSb);
+    constexpr int KW = KS / WK;                                                  // k of a step per wavefront
+    constexpr int NJ = KW >= 128 ? KW / 128 : 1;                                 // W pieces per lane and subtile
+    constexpr int NP = kMx ? 2 * NJ : KW / 32;                                   // X pieces per lane and subtile
+    constexpr bool kGroup = !kDirect && kMx && KS == 128 && TM % 4 == 0 && TN % 4 == 0;      // scale_at
+    constexpr int kLaneSb = kMx ? NJ : (kSb / WK >= 4 ? kSb / WK / 4 : 1);                 // scale bytes per lane and subtile
+    constexpr bool kPair = BF16_OUT && TN % 2 == 0;
     constexpr int kAhead = NP <= 4 && TM >= 4 ? 2 : 1, kRing = 2 * kAhead;
-    static_assert(kMx ? KS % 128 == 0 && KS <= 512 : KS == 64 || KS == 128 || KS == 256, "k per step");
+    static_assert(kMx ? KW % 128 == 0 && KW <= 512 : KW == 64 || KW == 128 || KW == 256, "k per step");
     static_assert(BM * kXRow % (1024 * kWaves) == 0 && BN * kWRow % (1024 * kWaves) == 0, "every wavefront transfers alike");
-    static_assert(kSRows <= kThreads && TM % kRing == 0, "one row's scales per thread; fragment ring");
-    __shared__ __attribute__((aligned(256))) uint8_t lds[3 * kStageBytes];
+    static_assert((kDirect || kSRows <= kThreads) && TM % kRing == 0, "one row's scales per thread; fragment ring");
+    static_assert(!kDirect || ((!kMx || BM * kSb % 256 == 0) && kStages >= 3), "a transfer of scales is of one operand");
+    static_assert(WK == 1 || (kDirect && KW >= 128), "a wavefront's part of a step");
+    static_assert((WK - 1) * BM * BN * 4 <= kStages * kStageBytes, "room for partial sums");
+    constexpr int kInst = kXInst + kWInst + kSInst;
+    __shared__ __attribute__((aligned(256))) uint8_t lds[kStages * kStageBytes];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c16 = lane & 15, g = lane >> 4;
@@ -503,16 +592,26 @@ __global__ __launch_bounds__(64 * WM * WN) void k_w4_tiled(W4Args a, uint32_t ti
     for (int i = 0; i < kWInst; ++i) {
         const int row = (wave * kWInst + i) * 64 / kWPer + lane / kWPer;
         wpiece[i] = (lane % kWPer) ^ wperm(row);
-        woff[i] = (uint32_t)min(row, nlast) * (uint32_t)(K / 2) + 16 * wpiece[i];
+        woff[i] = (uint32_t)min(w_row<kPair>(row), nlast) * (uint32_t)(K / 2) + 16 * wpiece[i];
     }
-    // the row whose scales this thread loads: X rows first
-    const int srow = kMx && tid < BM ? min(tid, mlast) : min(tid - (kMx ? BM : 0), nlast);
+    // Scales, X rows first.  Transferred 4 bytes per lane (K % KS == 0, so that a
+    // row's bytes start at multiples of 4), lanes behind the last row as the last;
+    uint32_t soff[kSInst > 0 ? kSInst : 1];
+    if (kDirect) {
+#pragma unroll
+        for (int i = 0; i < kSInst; ++i) {
+            const int at = ((wave * kSInst + i) * 64 + lane) * 4, row = at / kSb;
+            soff[i] = (uint32_t)(kMx && row < BM ? min(row, mlast) : min(w_row<kPair>(min(row - (kMx ? BM : 0), BN - 1)), nlast)) * (uint32_t)nb + at % kSb;
+        }
+    }
+    // or loaded by the thread that owns the row
+    const int srow = kMx && tid < BM ? min(tid, mlast) : min(w_row<kPair>(tid - (kMx ? BM : 0)), nlast);
     const uint8_t* ssrc = kMx && tid < BM ? a.xs + (m0 + srow) * nb : a.ws + (n0 + srow) * nb;
     constexpr int kSDwords = (kSb + 3) / 4;
     uint32_t sreg[kSDwords];
 
     auto load = [&](int s, uint8_t* st) {
-        if (kSRows == kThreads || tid < kSRows) {
+        if (!kDirect && (kSRows == kThreads || tid < kSRows)) {
             const uint8_t* p = ssrc + s * kSb;
 #pragma unroll
             for (int i = 0; i < kSDwords; ++i) {
@@ -527,7 +626,15 @@ __global__ __launch_bounds__(64 * WM * WN) void k_w4_tiled(W4Args a, uint32_t ti
         uint8_t* wd = st + kXBytes + wave * kWInst * 1024;
         const uint8_t* xb = xbase + (int64_t)s * kXRow;
         const uint8_t* wb = wbase + (int64_t)s * kWRow;
-        if (s < full) {
+        if (kDirect) {
+#pragma unroll
+            for (int i = 0; i < kSInst; ++i) {
+                const int at = (wave * kSInst + i) * 256;
+                const uint8_t* sb = kMx && at < BM * kSb ? a.xs + m0 * nb : a.ws + n0 * nb;
+                to_lds4(sb + (int64_t)s * kSb, soff[i], lds_address(st + kXBytes + kWBytes + at));
+            }
+        }
+        if (kDirect || s < full) {
 #pragma unroll
             for (int i = 0; i < kXInst; ++i) to_lds16(xb, xoff[i], lds_address(xd + i * 1024));
 #pragma unroll
@@ -551,6 +658,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_w4_tiled(W4Args a, uint32_t ti
     };
     auto store_scales = [&](uint8_t* st) {
         uint8_t* p = st + kXBytes + kWBytes;
+        if (kDirect) return;
         if (kSRows == kThreads || tid < kSRows) {
             if (kGroup) {  // BM % 64 == 0
 #pragma unroll
@@ -569,14 +677,15 @@ __global__ __launch_bounds__(64 * WM * WN) void k_w4_tiled(W4Args a, uint32_t ti
     for (int j = 0; j < TN; ++j)
 #pragma unroll
         for (int i = 0; i < TM; ++i) acc[j][i] = (f32x4){};
-    const int mrow = (wave / WN) * (BM / WM), nrow = (wave % WN) * (BN / WN);
+    const int kz = WK == 1 ? 0 : wave / (WM * WN), tile_wave = WK == 1 ? wave : wave % (WM * WN);
+    const int mrow = (tile_wave / WN) * (BM / WM), nrow = (tile_wave % WN) * (BN / WN);
     // Fragment addresses within a stage; the permutations depend on c16 alone.
     // MXFP8, product j of NJ: logical block b is block NJ b + j of the step; the
     // lane's W piece is that of logical block g, its X halves are half g % 2 of
     // logical blocks g / 2 and 2 + g / 2.  BF16: the lane takes k = KS/4 g ..
     // of the step, 8 per product.  Every index below is an XOR of disjoint bits.
-    const int xat = (mrow + c16) * kXRow + 16 * ((kMx ? 2 * NJ * (g >> 1) + (g & 1) : NP * g) ^ (c16 & kXMask));
-    const int wat = kXBytes + (nrow + c16) * kWRow + (kWPer == 2 ? 8 * g : 16 * ((NJ * g) ^ wperm(c16)));
+    const int xat = (mrow + c16) * kXRow + 16 * ((kz * (kXPer / WK) + (kMx ? 2 * NJ * (g >> 1) + (g & 1) : NP * g)) ^ (c16 & kXMask));
+    const int wat = kXBytes + (nrow + c16) * kWRow + (kWPer == 2 ? 8 * g : 16 * ((kz * (kWPer / WK) + NJ * g) ^ wperm(c16)));
     auto xpart = [](int q) { return kMx ? 32 * (q >> 1) ^ (q & 1) * 64 * NJ : 16 * q; };  // MXFP8: q = 2 j + half
 
     struct Frags {  // of one step: W as stored, and all scales
@@ -591,7 +700,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_w4_tiled(W4Args a, uint32_t ti
     };
     auto lane_scales = [&](const uint8_t* row) -> uint32_t {  // the lane's bytes of a row's step
         if (kSb == 2) return row[g >> 1];
-        const uint8_t* p = row + kLaneSb * g;
+        const uint8_t* p = row + kz * (kSb / WK) + kLaneSb * g;
         return kLaneSb == 4 ? *reinterpret_cast<const uint32_t*>(p) : kLaneSb == 2 ? *reinterpret_cast<const uint16_t*>(p) : *p;
     };
     auto read_w = [&](const uint8_t* st, Frags& f) {
@@ -652,7 +761,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_w4_tiled(W4Args a, uint32_t ti
             }
     };
     // step s with its fragments f, in stage `cur`; reads the next step's
-    // fragments into n
+    // fragments into n.  The transfer that starts goes into the stage of s - 1.
     auto step = [&](int s, const uint8_t* cur, uint8_t* next, uint8_t* last, const Frags& f, Frags& n) {
         widen(f);
 #pragma unroll
@@ -661,9 +770,12 @@ __global__ __launch_bounds__(64 * WM * WN) void k_w4_tiled(W4Args a, uint32_t ti
             products(i, f);
         }
         if (s + 1 < nsteps) store_scales(next);
-        wait_transfers();
+        if (kStages > 3 && s + kStages - 2 < nsteps)
+            wait_transfers<(kStages - 3) * kInst>();  // s + 1 has landed, s + 2 .. s + kStages - 2 are under way
+        else
+            wait_transfers<0>();
         __syncthreads();
-        if (s + 2 < nsteps) load(s + 2, last);
+        if (s + kStages - 1 < nsteps) load(s + kStages - 1, last);
         read_w(next, n);  // past the last step: a stage's leftovers, not used
 #pragma unroll
         for (int i = TM / 2; i < TM; ++i) {
@@ -672,97 +784,54 @@ __global__ __launch_bounds__(64 * WM * WN) void k_w4_tiled(W4Args a, uint32_t ti
         }
     };
     Frags f0, f1;
-    uint8_t *s0 = lds, *s1 = lds + kStageBytes, *s2 = lds + 2 * kStageBytes;
     if (nsteps > 0) {
-        load(0, s0);
-        store_scales(s0);
-        if (nsteps > 1) load(1, s1);
-        wait_transfers();
+        load(0, lds);
+        store_scales(lds);
+#pragma unroll
+        for (int i = 1; i < kStages - 1; ++i)
+            if (i < nsteps) load(i, lds + i * kStageBytes);
+        if (kStages > 3 && kStages - 2 < nsteps)
+            wait_transfers<(kStages - 2) * kInst>();
+        else
+            wait_transfers<0>();
         __syncthreads();
-        read_w(s0, f0);
+        read_w(lds, f0);
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) read_x(s0, i);
+        for (int i = 0; i < kAhead; ++i) read_x(lds, i);
     }
+    auto after = [&](int o) { return o == (kStages - 1) * kStageBytes ? 0 : o + kStageBytes; };
+    int cur = 0, last = (kStages - 1) * kStageBytes;  // stages of steps s and s - 1
     for (int s = 0; s < nsteps; s += 2) {
-        step(s, s0, s1, s2, f0, f1);
-        if (s + 1 < nsteps) step(s + 1, s1, s2, s0, f1, f0);
-        uint8_t* t = s0;  // two steps on
-        s0 = s2;
-        s2 = s1;
-        s1 = t;
+        const int next = after(cur);
+        step(s, lds + cur, lds + next, lds + last, f0, f1);
+        if (s + 1 < nsteps) step(s + 1, lds + next, lds + after(next), lds + cur, f1, f0);
+        last = next;
+        cur = after(next);
     }
 
-    // register r of lane l in tile (j, i): column 16 j + 4 (l / 16) + r, token
-    // 16 i + l % 16
-    const float s2w = kNv ? a.ws2[0] : 1.0f;
+    if (WK > 1) {  // partial sums of the wavefronts that share a tile, added in order
+        constexpr int kTile = WM * WN * TN * TM * 64;
+        f32x4* const part = reinterpret_cast<f32x4*>(lds) + (tile_wave * TN * TM * 64 + lane);
+        __syncthreads();
+        if (kz > 0) {
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-        const int64_t row = m0 + mrow + 16 * i + c16;
-        if (row >= a.M) continue;
+            for (int j = 0; j < TN; ++j)
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            const int64_t col = n0 + nrow + 16 * j + 4 * g;
-            f32x4 v = acc[j][i];
-            if (kNv) v = v * s2w;
-            if (col + 3 < a.N && a.N % 4 == 0 && ((uintptr_t)a.y & (BF16_OUT ? 7 : 15)) == 0) {
-                if (BF16_OUT)
-                    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.y) + row * a.N + col) =
-                        make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
-                else
-                    *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.y) + row * a.N + col) = v;
-            } else {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    if (col + r >= a.N) break;
-                    if (BF16_OUT)
-                        reinterpret_cast<uint16_t*>(a.y)[row * a.N + col + r] = (uint16_t)(bf16_pair(v[r], 0.0f) & 0xFFFFu);
-                    else
-                        reinterpret_cast<float*>(a.y)[row * a.N + col + r] = v[r];
-                }
-            }
+                for (int i = 0; i < TM; ++i) part[(kz - 1) * kTile + (j * TM + i) * 64] = acc[j][i];
         }
+        __syncthreads();
+        if (kz > 0) return;
+#pragma unroll
+        for (int z = 0; z < WK - 1; ++z)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int i = 0; i < TM; ++i) acc[j][i] = acc[j][i] + part[z * kTile + (j * TM + i) * 64];
     }
-}
-
-// Stores a wavefront's accumulators: register r of lane (c16, g) in acc[j][i] is
-// column n0 + 16 j + 4 g + r of token m0 + 16 i (m0 includes c16), or with PAIR,
-// whose W rows are ordered by w_row, column n0 + 32 (j / 2) + 8 g + 4 (j % 2) + r.
-// wide: rows of y start at multiples of 16 bytes; whole: all of it is in range.
-template <int TM, int TN, bool BF16_OUT>
-__device__ __forceinline__ void store_tile(f32x4 (&acc)[TN][TM], const W4Args& a, int64_t m0, int64_t n0, int g, float s2,
-                                           bool wide, bool whole) {
-    constexpr int C = BF16_OUT ? 2 : 1;  // subtiles per store
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-        const int64_t row = m0 + 16 * i;
-        if (!whole && row >= a.M) continue;
-#pragma unroll
-        for (int j = 0; j < TN; j += C) {
-            const int64_t col = n0 + 16 * j + 4 * C * g;
-            f32x4 v[C];
-#pragma unroll
-            for (int b = 0; b < C; ++b) v[b] = acc[j + b][i] * s2;
-            if (whole || (wide && col < a.N)) {
-                if constexpr (BF16_OUT) {
-                    const u32x4 p = {bf16_pair(v[0][0], v[0][1]), bf16_pair(v[0][2], v[0][3]),
-                                     bf16_pair(v[C - 1][0], v[C - 1][1]), bf16_pair(v[C - 1][2], v[C - 1][3])};
-                    __builtin_nontemporal_store(p, reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(a.y) + row * a.N + col));
-                }
-                else
-                    __builtin_nontemporal_store(v[0], reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.y) + row * a.N + col));
-            } else {
-#pragma unroll
-                for (int r = 0; r < 4 * C; ++r) {
-                    if (col + r >= a.N) break;
-                    if constexpr (BF16_OUT)
-                        reinterpret_cast<uint16_t*>(a.y)[row * a.N + col + r] =
-                            (uint16_t)(bf16_pair(v[r / 4][r % 4], 0.0f) & 0xFFFFu);
-                    else
-                        reinterpret_cast<float*>(a.y)[row * a.N + col + r] = v[0][r];
-                }
-            }
-        }
-    }
+    const int64_t mw = m0 + mrow, nw = n0 + nrow;
+    const bool wide = wide_rows<BF16_OUT, kPair>(a);
+    store_tile<TM, TN, BF16_OUT, kPair>(acc, a, mw + c16, nw, g, kNv ? a.ws2[0] : 1.0f, wide,
+                                        wide && mw + 16 * TM <= a.M && nw + 16 * TN <= a.N);
 }
 
 // ---------------------------------------------------------------------------
@@ -803,14 +872,6 @@ __device__ __forceinline__ void phase_barrier() {
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
-}
-
-// The W row of a 64-column segment that lies at position t of the segment.  For
-// BF16 results a lane's accumulators of two subtiles are then 8 neighbouring
-// columns, and 4 lanes write 64 bytes in a row; 32-bit results do that as it is.
-template <bool BF16_OUT>
-__device__ __forceinline__ int w_row(int t) {
-    return BF16_OUT ? (t & ~31) | (t & 12) << 1 | (t >> 2 & 4) | (t & 3) : t;
 }
 
 template <int KIND, bool BF16_OUT>
@@ -955,12 +1016,12 @@ __global__ __launch_bounds__(512) void k_w4_big(W4Args a, uint32_t tiles_m, uint
     };
     // Stores tile t; whether exactly kStores instructions did it.
     const float s2w = kNv ? a.ws2[0] : 1.0f;
-    const bool wide = (BF16_OUT ? a.N % 8 == 0 : a.N % 4 == 0) && ((uintptr_t)a.y & 15) == 0;
+    const bool wide = wide_rows<BF16_OUT, BF16_OUT>(a);
     auto store = [&](uint32_t t) {
         const TilePos pos = tile_of(t, tiles_m, tiles_n);
         const int64_t m0 = pos.m * BM + mrow, n0 = pos.n * BN + nrow;
         const bool whole = wide && m0 + 128 <= a.M && n0 + 64 <= a.N;
-        store_tile<TM, TN, BF16_OUT>(acc, a, m0 + c16, n0, g, s2w, wide, whole);
+        store_tile<TM, TN, BF16_OUT, BF16_OUT>(acc, a, m0 + c16, n0, g, s2w, wide, whole);
         return whole;
     };
 
@@ -977,7 +1038,7 @@ __global__ __launch_bounds__(512) void k_w4_big(W4Args a, uint32_t tiles_m, uint
         }
         transfer(lds_address(s1));
     }
-    wait_transfers();
+    wait_transfers<0>();
     clear();
     __syncthreads();
     if (half) phase_barrier();
@@ -1052,17 +1113,17 @@ hipError_t run_big(const W4Args& args, int64_t cus, hipStream_t stream) {
     return hipSuccess;
 }
 
-template <int KIND, int KS, int BM, int BN, int WM, int WN, bool BF16_OUT>
+template <int KIND, int KS, int BM, int BN, int WM, int WN, int WK, int STAGES, bool BF16_OUT>
 hipError_t run_tiled(const W4Args& args, hipStream_t stream) {
     const int64_t tiles_n = (args.N + BN - 1) / BN;
     // runs of token tiles whose grid stays within 2^31 threads
-    const int64_t most = (((int64_t)1 << 31) / (64 * WM * WN)) / tiles_n;
+    const int64_t most = (((int64_t)1 << 31) / (64 * WM * WN * WK)) / tiles_n;
     if (most < 1) return hipErrorInvalidValue;
     for (int64_t row = 0; row < args.M; row += most * BM) {
         const W4Args a = rows_from<KIND, BF16_OUT>(args, row, most * BM);
         const int64_t tiles_m = (a.M + BM - 1) / BM;
-        const hipError_t e = launch(&k_w4_tiled<KIND, KS, BM, BN, WM, WN, BF16_OUT>, dim3((unsigned)(tiles_m * tiles_n)),
-                                    dim3(64 * WM * WN), stream, a, (uint32_t)tiles_m, (uint32_t)tiles_n);
+        const hipError_t e = launch(&k_w4_tiled<KIND, KS, BM, BN, WM, WN, WK, STAGES, BF16_OUT>, dim3((unsigned)(tiles_m * tiles_n)),
+                                    dim3(64 * WM * WN * WK), stream, a, (uint32_t)tiles_m, (uint32_t)tiles_n);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
@@ -1084,12 +1145,14 @@ hipError_t run_decode(const W4Args& args, hipStream_t stream) {
     return hipSuccess;
 }
 
-// Which kernel.  Decode (wavefronts share a column tile and split k): `t`
-// 16-column tiles per workgroup, as few as let every workgroup be resident at
-// once -- X is then read once per 16 t columns, and fewer, wider workgroups
-// leave CUs idle.  Measured (us; MXFP8 x MXFP4 at t = 1, 2, 4): 8 x 4096 x 4096
-// 4.5, 5.4, -; 8 x 6144 x 4096 7.1, 6.0, 7.4; 8 x 14336 x 4096 11.6, 10.0, 10.0;
-// 8 x 28672 x 8192 39, 35.2, 32.1.  With up to 4 tokens X costs little and t
+// Which kernel, by length, tokens and how many workgroups a tile gives.  The
+// times are microseconds, medians of several buffers in turn.
+//
+// Decode (wavefronts share a column tile and split k): `t` 16-column tiles per
+// workgroup, as few as let every workgroup be resident at once -- X is then read
+// once per 16 t columns, and fewer, wider workgroups leave CUs idle (MXFP8 x
+// MXFP4 at t = 1, 2, 4: 8 x 4096 x 4096 4.5, 5.4, -; 8 x 6144 x 4096 7.1, 6.0, 7.4;
+// 8 x 28672 x 8192 39, 35.2, 32.1).  With up to 4 tokens X costs little and t
 // stays at 2 at most (1 x 14336 x 4096 8.4 against 9.7 with 4).  Four
 // wavefronts; eight where such a small batch meets a long K (1 x 8192 x 28672
 // 23.9 against 27.3; at 4096 they are 10 % slower).
@@ -1099,7 +1162,7 @@ int decode_columns(int64_t tiles_m, int64_t M, int64_t N, int64_t cus) {
     return t;
 }
 
-constexpr int64_t kDecodeOneTile = 16, kDecodeTwoTiles = 64, kDecodeLongK = 8192;
+constexpr int64_t kDecodeLongK = 8192;
 
 template <int KIND, bool BF16_OUT>
 hipError_t decode_16(const W4Args& a, int64_t cus, hipStream_t stream) {
@@ -1111,66 +1174,113 @@ hipError_t decode_16(const W4Args& a, int64_t cus, hipStream_t stream) {
     return run_decode<KIND, BF16_OUT, 4, 4, 1>(a, stream);
 }
 
-// 17 to 64 tokens: two token tiles per wavefront, while at most 32 columns per
-// workgroup fill the device: 32 x 4096 x 14336 20.7 us against 27.5 with tiles
-// of 32 x 64 and a step at a time, but 32 x 14336 x 4096 13.5 against 11.3.
-bool decode_32_fits(int64_t M, int64_t N, int64_t cus) {
-    return M <= kDecodeTwoTiles && ((M + 31) / 32) * ((N + 31) / 32) <= cus;
-}
-
-template <int KIND, bool BF16_OUT>
-hipError_t decode_32(const W4Args& a, int64_t cus, hipStream_t stream) {
-    return decode_columns((a.M + 31) / 32, a.M, a.N, cus) == 1 ? run_decode<KIND, BF16_OUT, 4, 1, 2>(a, stream)
-                                                               : run_decode<KIND, BF16_OUT, 4, 2, 2>(a, stream);
-}
-
 inline int64_t tiles(const W4Args& a, int bm, int bn) { return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); }
 
-// Tiles: the smallest whose workgroups are all resident at once (a second
-// round of few workgroups costs as much as a full one), else the largest,
-// which moves the fewest bytes per product.  Measured (us): 100 x 4096 x 4096
-// with tiles of 32 x 64, 64 x 64, 64 x 64 in shorter steps (two workgroups per
-// CU), 128 x 128: 10.4, 11.9, 15.2, 27; 100 x 14336 x 4096: 28, 22.4, 17.3, 27.9;
-// 512 x 14336 x 4096, the last two, 256 x 128 and 256 x 256: 60, 45.2, 42.7, 47.1;
-// 1024 x 14336 x 4096: 106, 82, 80, 53; 8192 x 14336 x 4096, the last three: 579, 600,
-// 366.  Lengths that the last kernel does not take go to its one-barrier form.
-template <bool BF16_OUT>
-hipError_t pick_mx(const W4Args& a, int64_t cus, hipStream_t stream) {
-    if (a.M <= kDecodeOneTile) return decode_16<kW4Mx, BF16_OUT>(a, cus, stream);
-    if (decode_32_fits(a.M, a.N, cus)) return decode_32<kW4Mx, BF16_OUT>(a, cus, stream);
-    if (tiles(a, 32, 64) <= cus) return run_tiled<kW4Mx, 512, 32, 64, 1, 4, BF16_OUT>(a, stream);
-    if (tiles(a, 64, 64) <= cus) return run_tiled<kW4Mx, 512, 64, 64, 2, 4, BF16_OUT>(a, stream);
-    if (tiles(a, 64, 64) <= 2 * cus) return run_tiled<kW4Mx, 256, 64, 64, 2, 2, BF16_OUT>(a, stream);
-    if (tiles(a, 128, 128) <= cus) return run_tiled<kW4Mx, 128, 128, 128, 2, 2, BF16_OUT>(a, stream);
-    if (tiles(a, 256, 128) <= cus) return run_tiled<kW4Mx, 128, 256, 128, 4, 2, BF16_OUT>(a, stream);
-    if (big_fits<kW4Mx>(a.K)) return run_big<kW4Mx, BF16_OUT>(a, cus, stream);
-    return run_tiled<kW4Mx, 128, 256, 256, 2, 4, BF16_OUT>(a, stream);
+// Up to 4 tokens always, up to 8 where tiles of 32 x 32 would all be resident:
+// 8 x 4096 x 4096 5.1 against 5.5 (MXFP8), 6.3 against 8.5 (BF16 x NVFP4); but
+// 8 x 14336 x 4096 10.6 against 8.4, and 13.3 against 12.1; 16 x 4096 x 4096 6.1
+// against 5.5, 16 x 4096 x 14336 21.6 against 21.4 (NVFP4).
+bool decode_fits(const W4Args& a, int64_t cus) { return a.M <= 4 || (a.M <= 8 && tiles(a, 32, 32) <= cus); }
+
+// Whole steps of at least one of the tiles below, scales that 4-byte transfers
+// can take.
+bool direct_fits(const W4Args& a) {
+    return a.K % 256 == 0 && ((uintptr_t)a.ws & 3) == 0 && ((uintptr_t)a.xs & 3) == 0;
 }
 
-// BF16 activations, by the same rule (NVFP4, us): 61 x 4096 x 4096 with tiles of
-// 32 x 32 and 32 x 64: 16.5, 16.8; 61 x 6144 x 4096: 19.1, 17.2; 128 x 14336 x 4096
-// with 32 x 64 and 64 x 128: 41, 31.5; 1024 x 14336 x 4096 with 64 x 128 and
-// 256 x 256: 154, 106, but 512 x 14336 x 4096: 87, 90 -- the middle tile keeps
-// two workgroups per CU and stays ahead for two rounds of them.  The tiles'
-// transfers of 16 bytes want K % 32 == 0.
+// Tiles: the smallest whose workgroups are all resident at once (a second round
+// of few workgroups costs as much as a full one), else the largest, which moves
+// the fewest bytes per product.  Small tiles have several wavefronts per output
+// that split the step (61 x 6144 x 4096 of NVFP4: 11.8 with four, 13.0 with two,
+// 15.7 with one) and up to six stages (100 x 4096 x 4096 of MXFP8 8.5 with four,
+// 9.3 with three).
+// MXFP8, tiles of 32 x 32, 32 x 64, 64 x 64, 64 x 128: 32 x 4096 x 4096 5.8, 6.7,
+// 8.6, -; 100 x 4096 x 4096 -, 7.7, 10.3, -; 100 x 14336 x 4096 -, -, 15.1, 13.6;
+// 64 x 128, 128 x 128, 256 x 128, 256 x 256: 300 x 4096 x 4096 13.2, 23, 31, 46;
+// 512 x 6144 x 4096 24.5, 22.8, 36, 47; 512 x 14336 x 4096 49, 44, 37, 47;
+// 1024 x 14336 x 4096 85, 81, 77, 53.
+template <bool BF16_OUT>
+hipError_t direct_mx(const W4Args& a, int64_t cus, hipStream_t stream) {
+    if (a.K % 512 == 0) {
+        if (tiles(a, 32, 32) <= cus) return run_tiled<kW4Mx, 512, 32, 32, 1, 2, 4, 4, BF16_OUT>(a, stream);
+        if (tiles(a, 32, 64) <= cus) return run_tiled<kW4Mx, 512, 32, 64, 1, 2, 4, 4, BF16_OUT>(a, stream);
+    }
+    if (tiles(a, 64, 64) <= cus) return run_tiled<kW4Mx, 256, 64, 64, 2, 2, 2, 4, BF16_OUT>(a, stream);
+    if (tiles(a, 64, 128) <= cus) return run_tiled<kW4Mx, 256, 64, 128, 2, 2, 2, 4, BF16_OUT>(a, stream);
+    if (tiles(a, 128, 128) <= cus) return run_tiled<kW4Mx, 128, 128, 128, 2, 4, 1, 6, BF16_OUT>(a, stream);
+    if (tiles(a, 256, 128) <= cus) return run_tiled<kW4Mx, 128, 256, 128, 4, 2, 1, 3, BF16_OUT>(a, stream);
+    if (big_fits<kW4Mx>(a.K)) return run_big<kW4Mx, BF16_OUT>(a, cus, stream);
+    return run_tiled<kW4Mx, 128, 256, 256, 2, 4, 1, 0, BF16_OUT>(a, stream);
+}
+
+// BF16 activations likewise, but with two workgroups per CU where their stages
+// leave room (32 x 64 in steps of 256, 64 x 64 for NVFP4, whose widening costs
+// more, and 128 x 128).  NVFP4, tiles of 32 x 32, 32 x 64 in steps of 512, 32 x 64,
+// 64 x 64, 64 x 128: 61 x 4096 x 4096 10.0, 11.4, 12.7, 16.3, -; 61 x 6144 x 4096
+// 17.1, 11.8, 13.0, 16.5, -; 61 x 14336 x 4096 31, 21.3, 18.8, 17.7, 26;
+// 32 x 28672 x 8192 70, 50, 45, 67, -; 64 x 128, 128 x 128, 256 x 256:
+// 512 x 4096 x 4096 24.9, 40, 89; 256 x 14336 x 4096 45.9, 42.0, 90;
+// 512 x 14336 x 4096 89, 82, 90; 1024 x 14336 x 4096 154, -, 106.
 template <int KIND, bool BF16_OUT>
-hipError_t pick_bf16(const W4Args& a, int64_t cus, hipStream_t stream) {
-    if (a.M <= kDecodeOneTile) return decode_16<KIND, BF16_OUT>(a, cus, stream);
-    if (decode_32_fits(a.M, a.N, cus)) return decode_32<KIND, BF16_OUT>(a, cus, stream);
-    if (KIND == kW4Bf16Nvfp4 && a.K % 32 != 0) return run_decode<KIND, BF16_OUT, 4, 4, 2>(a, stream);
-    if (tiles(a, 32, 32) <= cus) return run_tiled<KIND, 256, 32, 32, 1, 2, BF16_OUT>(a, stream);
-    if (tiles(a, 32, 64) <= 2 * cus) return run_tiled<KIND, 256, 32, 64, 1, 4, BF16_OUT>(a, stream);
-    if (tiles(a, 64, 128) <= 4 * cus) return run_tiled<KIND, 128, 64, 128, 1, 4, BF16_OUT>(a, stream);
+hipError_t direct_bf16(const W4Args& a, int64_t cus, hipStream_t stream) {
+    if (a.K % 512 == 0) {
+        if (tiles(a, 32, 32) <= cus) return run_tiled<KIND, 512, 32, 32, 1, 2, 4, 3, BF16_OUT>(a, stream);
+        if (tiles(a, 32, 64) <= cus) return run_tiled<KIND, 512, 32, 64, 1, 4, 4, 3, BF16_OUT>(a, stream);
+    }
+    if constexpr (KIND == kW4Bf16Nvfp4) {
+        if (a.M > 32 && tiles(a, 64, 64) <= cus) return run_tiled<KIND, 256, 64, 64, 1, 4, 2, 3, BF16_OUT>(a, stream);
+    }
+    if (tiles(a, 32, 64) <= 2 * cus) return run_tiled<KIND, 256, 32, 64, 1, 4, 2, 3, BF16_OUT>(a, stream);
+    if (tiles(a, 64, 128) <= cus) return run_tiled<KIND, 256, 64, 128, 1, 4, 2, 3, BF16_OUT>(a, stream);
+    if (tiles(a, 128, 128) <= 2 * cus) return run_tiled<KIND, 128, 128, 128, 2, 4, 1, 3, BF16_OUT>(a, stream);
     if (big_fits<KIND>(a.K)) return run_big<KIND, BF16_OUT>(a, cus, stream);
-    return run_tiled<KIND, 64, 256, 256, 2, 4, BF16_OUT>(a, stream);
+    return run_tiled<KIND, 64, 256, 256, 2, 4, 1, 0, BF16_OUT>(a, stream);
+}
+
+// Other lengths: decode up to 64 tokens, with two token tiles per wavefront from
+// 17, while at most 32 columns per workgroup fill the device (32 x 4096 x 14336
+// 20.7 against 27.5 with tiles of 32 x 64, but 32 x 14336 x 4096 13.5 against 11.3);
+// then few tiles by the same rule, which bear a partial step (100 x 14336 x 4096
+// of MXFP8: 64 x 64 17.3, 128 x 128 27.9; 128 x 14336 x 4096 of NVFP4: 32 x 64 41,
+// 64 x 128 31.5).
+template <int KIND, bool BF16_OUT>
+hipError_t pick_any(const W4Args& a, int64_t cus, hipStream_t stream) {
+    if (a.M <= 16) return decode_16<KIND, BF16_OUT>(a, cus, stream);
+    const int64_t pairs = (a.M + 31) / 32;
+    if (a.M <= 64 && pairs * ((a.N + 31) / 32) <= cus)
+        return decode_columns(pairs, a.M, a.N, cus) == 1 ? run_decode<KIND, BF16_OUT, 4, 1, 2>(a, stream)
+                                                         : run_decode<KIND, BF16_OUT, 4, 2, 2>(a, stream);
+    if constexpr (KIND == kW4Mx) {
+        if (tiles(a, 64, 64) <= 2 * cus) return run_tiled<KIND, 256, 64, 64, 2, 2, 1, 0, BF16_OUT>(a, stream);
+        if (tiles(a, 128, 128) <= cus) return run_tiled<KIND, 128, 128, 128, 2, 2, 1, 0, BF16_OUT>(a, stream);
+        if (big_fits<KIND>(a.K)) return run_big<KIND, BF16_OUT>(a, cus, stream);
+        return run_tiled<KIND, 128, 256, 256, 2, 4, 1, 0, BF16_OUT>(a, stream);
+    } else {
+        // the tiles' transfers of 16 bytes want K % 32 == 0
+        if (KIND == kW4Bf16Nvfp4 && a.K % 32 != 0) return run_decode<KIND, BF16_OUT, 4, 4, 2>(a, stream);
+        if (tiles(a, 32, 64) <= 2 * cus) return run_tiled<KIND, 256, 32, 64, 1, 4, 1, 0, BF16_OUT>(a, stream);
+        if (tiles(a, 64, 128) <= 4 * cus) return run_tiled<KIND, 128, 64, 128, 1, 4, 1, 0, BF16_OUT>(a, stream);
+        if (big_fits<KIND>(a.K)) return run_big<KIND, BF16_OUT>(a, cus, stream);
+        return run_tiled<KIND, 64, 256, 256, 2, 4, 1, 0, BF16_OUT>(a, stream);
+    }
+}
+
+template <int KIND, bool BF16_OUT>
+hipError_t pick_kind(const W4Args& a, int64_t cus, hipStream_t stream) {
+    if (!direct_fits(a)) return pick_any<KIND, BF16_OUT>(a, cus, stream);
+    if (decode_fits(a, cus)) return decode_16<KIND, BF16_OUT>(a, cus, stream);
+    if constexpr (KIND == kW4Mx)
+        return direct_mx<BF16_OUT>(a, cus, stream);
+    else
+        return direct_bf16<KIND, BF16_OUT>(a, cus, stream);
 }
 
 template <bool BF16_OUT>
 hipError_t pick(const W4Args& a, W4Kind kind, int64_t cus, hipStream_t stream) {
     switch (kind) {
-        case kW4Mx: return pick_mx<BF16_OUT>(a, cus, stream);
-        case kW4Bf16Nvfp4: return pick_bf16<kW4Bf16Nvfp4, BF16_OUT>(a, cus, stream);
-        case kW4Bf16Mxfp4: return pick_bf16<kW4Bf16Mxfp4, BF16_OUT>(a, cus, stream);
+        case kW4Mx: return pick_kind<kW4Mx, BF16_OUT>(a, cus, stream);
+        case kW4Bf16Nvfp4: return pick_kind<kW4Bf16Nvfp4, BF16_OUT>(a, cus, stream);
+        case kW4Bf16Mxfp4: return pick_kind<kW4Bf16Mxfp4, BF16_OUT>(a, cus, stream);
     }
     return hipErrorInvalidValue;
 }

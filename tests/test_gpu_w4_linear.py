@@ -297,3 +297,79 @@ def test_many_tiles_spread(focus, fmt):
     assert torch.isnan(z[bad]).all()
     z[bad] = y[bad]
     assert torch.equal(z, y)
+
+
+# Lengths of whole steps.  On a device of 256 compute units each line takes
+# another tile of some format, in one step, in fewer steps than LDS stages and in
+# more; token and column edges inside the tiles.
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,N,K", [(9, 40, 512), (33, 129, 2560), (61, 4000, 1536), (20, 9000, 1536), (61, 6000, 1024),
+                                   (100, 4100, 768), (70, 300, 256), (61, 14000, 768), (20, 14000, 1280),
+                                   (8, 9000, 4608), (100, 14003, 512), (250, 14000, 1024), (500, 14000, 768),
+                                   (130, 4001, 4352)])
+def test_whole_steps(focus, fmt, M, N, K):
+    c = Case(focus, fmt, M, N, K, seed=M + K, exact=True)
+    buf = torch.full((M + 1, N), 7.0, device=DEV)
+    y = c.call(c.x, c.w, out_dtype=torch.float32, out=buf[:M])
+    assert np.array_equal(y.cpu().double().numpy(), c.want)
+    assert (buf[M] == 7.0).all()
+    h = c.call(c.x, c.w, out_dtype=torch.bfloat16)
+    assert torch.equal(h.cpu(), torch.from_numpy(c.want).to(torch.bfloat16))
+    bad = M - 2
+    if fmt == "mx":
+        codes = c.x.codes.clone()
+        codes[bad, K - 1] = 0x7F
+        x = focus.Quantized(codes, c.x.scales, None, None)
+    else:
+        x = c.x.clone()
+        x[bad, K - 1] = float("nan")
+    z = c.call(x, c.w, out_dtype=torch.float32)
+    assert torch.isnan(z[bad]).all()
+    z[bad] = y[bad]
+    assert torch.equal(z, y)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,N,K", [(12, 300, 1024), (61, 700, 1024), (200, 4000, 512), (2100, 8400, 512)])
+def test_scales_at_odd_addresses(focus, fmt, M, N, K):
+    c = Case(focus, fmt, M, N, K, seed=M, exact=True)
+
+    def odd(t):
+        buf = torch.empty(t.numel() + 1, dtype=torch.uint8, device=DEV)
+        buf[1:] = t.reshape(-1)
+        return buf[1:].view(t.shape)
+
+    w = focus.Quantized(c.w.codes, odd(c.w.scales), None, c.w.s2)
+    x = focus.Quantized(c.x.codes, odd(c.x.scales), None, None) if fmt == "mx" else c.x
+    y = c.call(x, w, out_dtype=torch.float32)
+    assert np.array_equal(y.cpu().double().numpy(), c.want)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,N,K", [(61, 6144, 512), (100, 5000, 768), (250, 14000, 256)])
+def test_whole_steps_spread(focus, fmt, M, N, K):
+    """Scales and values over their range, on some of the columns."""
+    c = Case(focus, fmt, M, N, K, seed=5)
+    cols = np.r_[0:N:29, N - 16:N]
+    c.wv, c.wc, c.ws, c.want = c.wv[cols], c.wc[cols], c.ws[cols], c.want[:, cols]
+    for dtype in (torch.float32, torch.bfloat16):
+        c.check(c.call(c.x, c.w, out_dtype=dtype)[:, torch.from_numpy(cols).to(DEV)], dtype)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_two_streams_at_once(focus, fmt):
+    """No call keeps anything another could use: the same calls on two streams,
+    in turn and unsynchronized."""
+    cases = [Case(focus, fmt, M, N, K, seed=M) for M, N, K in ((1, 2000, 2048), (61, 6144, 1024), (300, 5000, 768), (2100, 8500, 512))]
+    want = [c.call(c.x, c.w, out_dtype=torch.float32) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(3):
+        for s, out in zip(streams, got):
+            with torch.cuda.stream(s):
+                out += [c.call(c.x, c.w, out_dtype=torch.float32) for c in cases]
+    torch.cuda.synchronize()
+    for out in got:
+        for i, y in enumerate(out):
+            assert torch.equal(y, want[i % len(cases)])
