@@ -23,7 +23,11 @@
 // wavefront covers contiguous memory, and a 16- or 32-element block is 2 or 4
 // neighbouring lanes, whose maximum is exchanged by DPP.  All of it is bound
 // by HBM for large batches and by the launch and two dependent memory
-// latencies for a single token.
+// latencies for a single token.  Measured: norm to MXFP8 of [8192, 4096] 41 us
+// (5.7 TB/s), norm to BF16 of [1003, 8192] 10.8 (6.1 TB/s, the last-level cache),
+// gated activation to MXFP8 of [333, 28672] 10.6 (4.5 TB/s), to NVFP4 with values
+// of [8192, 14336] 153-172 (4.5-5.0 TB/s, the exact exponential and the codes keep
+// the vector units as busy), one row 2.5-2.9.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>

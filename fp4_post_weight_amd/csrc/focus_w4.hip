@@ -26,7 +26,9 @@
 // wavefront to reach the matrix layout, whose 16 neighbouring lanes hold 16
 // different rows.  Within a step the sum is order-free: lane group g takes
 // the blocks 4g..4g+3, so that its four scale bytes are one dword, selected
-// by the instruction.
+// by the instruction.  Measured: 1 x 4096 x 14336 of NVFP4 9.6 us (3.5 TB/s; a large
+// copy reaches 4.9), 1 x 4096 x 4096 of MXFP8 x MXFP4 3.4-4.0 (a launch and two
+// memory latencies).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
