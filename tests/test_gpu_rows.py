@@ -430,3 +430,63 @@ def test_another_stream_and_graph(focus):
         torch.cuda.synchronize()
         for a, b in zip(eager, caught):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("t,h", [(560_000, 4096), (70, 36_700_160)])
+def test_offsets_past_32_bits(focus, t, h):
+    """More than 2^31 elements: the last rows equal those of the same call on
+    these rows alone."""
+    def rows(p, n):
+        return p[t - n:].clone()
+
+    g = torch.Generator(device=DEV).manual_seed(h)
+    x = torch.randn(t, h, device=DEV, dtype=torch.bfloat16, generator=g)
+    r = torch.randn(t, h, device=DEV, dtype=torch.bfloat16, generator=g)
+    w = torch.randn(h, device=DEV, dtype=torch.bfloat16, generator=g)
+    n = 3
+
+    def same(big, small):
+        for a, b in zip(big, small):
+            if a is not None:
+                assert torch.equal(a[t - n:], b)
+
+    y, res = focus.rmsnorm(x, w, EPS, residual=r)
+    y1, res1 = focus.rmsnorm(rows(x, n), w, EPS, residual=rows(r, n))
+    same((y, res), (y1, res1))
+    del y, res
+    for call in (focus.rmsnorm_nvfp4, focus.rmsnorm_mxfp8):
+        q, _ = call(x, w, EPS, residual=r)
+        same(q, call(rows(x, n), w, EPS, residual=rows(r, n))[0])
+        del q
+    same((focus.silu_mul(x, r),), (focus.silu_mul(rows(x, n), rows(r, n)),))
+    for call in (focus.silu_mul_nvfp4, focus.silu_mul_mxfp8):
+        same(call(x, r, dequant=True), call(rows(x, n), rows(r, n), dequant=True))
+    same(focus.quantize_mxfp8(x, dequant=True), focus.quantize_mxfp8(rows(x, n), dequant=True))
+
+
+def test_two_streams_at_once(focus):
+    """No call keeps anything another could use."""
+    ins = [(torch.randn(t, h, device=DEV).to(torch.bfloat16), torch.randn(t, h, device=DEV).to(torch.bfloat16),
+            torch.randn(h, device=DEV).to(torch.bfloat16)) for t, h in ((1, 4096), (300, 8192), (4096, 2048))]
+
+    def run():
+        out = []
+        for x, r, w in ins:
+            y, res = focus.rmsnorm(x, w, EPS, residual=r)
+            q, _ = focus.rmsnorm_nvfp4(x, w, EPS, dequant=True)
+            p = focus.silu_mul_mxfp8(x, r, dequant=True)
+            out += [y, res, q.codes, q.scales, q.s2, q.deq, p.codes, p.scales, p.deq]
+        return out
+
+    want = run()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(3):
+        for s, out in zip(streams, got):
+            with torch.cuda.stream(s):
+                out += run()
+    torch.cuda.synchronize()
+    for out in got:
+        for i, y in enumerate(out):
+            assert torch.equal(y, want[i % len(want)])

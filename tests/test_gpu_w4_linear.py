@@ -373,3 +373,45 @@ def test_two_streams_at_once(focus, fmt):
     for out in got:
         for i, y in enumerate(out):
             assert torch.equal(y, want[i % len(cases)])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,N", [(3, 50), (12, 9000), (100, 4000), (2100, 9100)])
+def test_no_k(focus, fmt, M, N):
+    e = torch.empty
+    u8 = dict(dtype=torch.uint8, device=DEV)
+    w = focus.Quantized(e((N, 0), **u8), e((N, 0), **u8), None, torch.ones(1, device=DEV) if fmt == "nvfp4" else None)
+    if fmt == "mx":
+        y = focus.mxfp4_linear(focus.Quantized(e((M, 0), **u8), e((M, 0), **u8), None, None), w)
+    else:
+        y = focus.w4a16_linear(e((M, 0), dtype=torch.bfloat16, device=DEV), w)
+    assert y.shape == (M, N) and (y == 0).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M", [2, 40, 520])
+def test_offsets_past_32_bits(focus, fmt, M):
+    """4.6 GB of codes and, at 520 tokens, 4.7 GB of results: the last columns
+    equal those of the same layer cut to them (exact sums, any tile)."""
+    N, K, cut = 2_250_000, 4096, 300
+    g = torch.Generator(device=DEV).manual_seed(M)
+    codes = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device=DEV, generator=g)
+    block = 16 if fmt == "nvfp4" else 32
+    scales = torch.randint(0x37 if block == 16 else 126, 0x39 if block == 16 else 128, (N, K // block), dtype=torch.uint8,
+                           device=DEV, generator=g)
+    if block == 16:
+        scales = (scales & 0x38) | 0x30  # 0.5 and 1
+    s2 = torch.ones(1, device=DEV) if fmt == "nvfp4" else None
+    if fmt == "mx":
+        pool = torch.tensor([0x30, 0x38, 0x40, 0xB0, 0xB8, 0xC0], dtype=torch.uint8, device=DEV)
+        x = focus.Quantized(pool[torch.randint(0, 6, (M, K), device=DEV, generator=g)],
+                            torch.full((M, K // 32), 127, dtype=torch.uint8, device=DEV), None, None)
+        call = focus.mxfp4_linear
+    else:
+        x = torch.randint(-4, 5, (M, K), device=DEV, generator=g).to(torch.bfloat16)
+        call = focus.w4a16_linear
+    y = call(x, focus.Quantized(codes, scales, None, s2), out_dtype=torch.bfloat16)
+    for part in (slice(0, cut), slice(N - cut, N)):
+        w = focus.Quantized(codes[part].clone(), scales[part].clone(), None, s2)
+        assert torch.equal(y[:, part], call(x, w, out_dtype=torch.bfloat16))
+    assert torch.isfinite(y[M - 1]).all()
