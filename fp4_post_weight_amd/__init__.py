@@ -575,11 +575,14 @@ _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_get
     lambda index: torch.cuda.current_stream(index).cuda_stream
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _launch(fn, dev, *args):
     """Call ``fn`` with ``dev`` current and its current stream as the last
     argument."""
     index = dev.index
-    if torch.cuda.current_device() != index:
+    if _current_device() != index:
         with torch.cuda.device(dev):
             st = fn(*args, _raw_stream(index))
     else:
@@ -616,19 +619,20 @@ def _rows_2d(name, t, unit):
 def _bf16_out(out, like, label="out"):
     """A BF16 output of ``like``'s shape (contiguous)."""
     if out is None:
-        return torch.empty_like(like, memory_format=torch.contiguous_format)
+        return torch.empty_like(like) if like.is_contiguous() else like.new_empty(like.shape)
     if not (_fits(out, torch.bfloat16, like.get_device()) and out.numel() == like.numel()):
         _check_buf(label, out, torch.bfloat16, like.device, like.numel())
     return out
 
 
-def _mxfp8_outs(out, rows, cols, dev, dequant):
-    """Output buffers of an MXFP8 quantizer call: codes [rows, cols], scales
-    [rows, cols/32], deq [rows, cols] when dequant."""
+def _mxfp8_outs(out, rows, cols, like, dequant):
+    """Output buffers of an MXFP8 quantizer call on ``like``'s device: codes
+    [rows, cols], scales [rows, cols/32], deq [rows, cols] when dequant."""
     if out is None:
-        return Quantized(torch.empty((rows, cols), dtype=torch.uint8, device=dev),
-                         torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev),
-                         torch.empty((rows, cols), dtype=torch.bfloat16, device=dev) if dequant else None, None)
+        return Quantized(like.new_empty((rows, cols), dtype=torch.uint8),
+                         like.new_empty((rows, cols // 32), dtype=torch.uint8),
+                         _bf16_out(None, like) if dequant else None, None)
+    dev = like.device
     if not isinstance(out, Quantized):
         raise TypeError("out must be a Quantized tuple of buffers")
     _check_buf("out.codes", out.codes, torch.uint8, dev, rows * cols)
@@ -640,8 +644,13 @@ def _mxfp8_outs(out, rows, cols, dev, dequant):
     return Quantized(out.codes, out.scales, out.deq if dequant else None, None)
 
 
-def _token_nvfp4_outs(out, rows, cols, dev, dequant):
+def _token_nvfp4_outs(out, rows, cols, like, dequant):
     """Output buffers of a per-token NVFP4 result (s2 [rows], also for no rows)."""
+    if out is None:
+        return Quantized(like.new_empty((rows, cols // 2), dtype=torch.uint8),
+                         like.new_empty((rows, cols // 16), dtype=torch.uint8),
+                         _bf16_out(None, like) if dequant else None, like.new_empty((rows,), dtype=torch.float32))
+    dev = like.device
     codes, scales, deq, s2 = _quant_outs(out, rows, cols, dev, dequant, s2_rows=rows)
     return Quantized(codes, scales, deq, torch.empty(0, dtype=torch.float32, device=dev) if s2 is None else s2)
 
@@ -685,7 +694,7 @@ def rmsnorm_nvfp4(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
     input of ``nvfp4_linear``.  Returns (Quantized, h or None)."""
     t, h, res = _norm_inputs(x, weight, residual, residual_out, 16)
     dev = x.device
-    q = _token_nvfp4_outs(out, t, h, dev, dequant)
+    q = _token_nvfp4_outs(out, t, h, x, dequant)
     _launch(_lib.lib().focus_rmsnorm_nvfp4, dev, _p(x), _p(residual), _p(weight), eps, t, h, _p(res), _p(q.codes),
             _p(q.scales), _p(q.s2), _p(q.deq))
     return q, res
@@ -699,7 +708,7 @@ def rmsnorm_mxfp8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
     [tokens, hidden/32] and s2 None, h or None)."""
     t, h, res = _norm_inputs(x, weight, residual, residual_out, 32)
     dev = x.device
-    q = _mxfp8_outs(out, t, h, dev, dequant)
+    q = _mxfp8_outs(out, t, h, x, dequant)
     _launch(_lib.lib().focus_rmsnorm_mxfp8, dev, _p(x), _p(residual), _p(weight), eps, t, h, _p(res), _p(q.codes),
             _p(q.scales), _p(q.deq))
     return q, res
@@ -754,7 +763,7 @@ def silu_mul_nvfp4(gate: torch.Tensor, up: torch.Tensor, dequant: bool = False,
                    out: Optional[Quantized] = None) -> Quantized:
     """``silu_mul`` with the result in per-token NVFP4 (hidden % 16 == 0)."""
     t, h, dev, gs, us = _gated_inputs(gate, up, 16)
-    q = _token_nvfp4_outs(out, t, h, dev, dequant)
+    q = _token_nvfp4_outs(out, t, h, gate, dequant)
     _launch(_lib.lib().focus_silu_mul_nvfp4, dev, _p(gate), gs, _p(up), us, t, h, _p(q.codes), _p(q.scales),
             _p(q.s2), _p(q.deq))
     return q
@@ -764,7 +773,7 @@ def silu_mul_mxfp8(gate: torch.Tensor, up: torch.Tensor, dequant: bool = False,
                    out: Optional[Quantized] = None) -> Quantized:
     """``silu_mul`` with the result in MXFP8 (hidden % 32 == 0)."""
     t, h, dev, gs, us = _gated_inputs(gate, up, 32)
-    q = _mxfp8_outs(out, t, h, dev, dequant)
+    q = _mxfp8_outs(out, t, h, gate, dequant)
     _launch(_lib.lib().focus_silu_mul_mxfp8, dev, _p(gate), gs, _p(up), us, t, h, _p(q.codes), _p(q.scales),
             _p(q.deq))
     return q
@@ -774,7 +783,7 @@ def quantize_mxfp8(x: torch.Tensor, dequant: bool = False, out: Optional[Quantiz
     """MXFP8 of activations X [tokens, hidden] BF16 (hidden % 32 == 0): E4M3
     codes [tokens, hidden], E8M0 scale bytes [tokens, hidden/32]."""
     t, h, _ = _rows_2d("x", x, 32)
-    q = _mxfp8_outs(out, t, h, x.device, dequant)
+    q = _mxfp8_outs(out, t, h, x, dequant)
     _launch(_lib.lib().focus_quantize_mxfp8, x.device, _p(x), t, h, _p(q.codes), _p(q.scales), _p(q.deq))
     return q
 
@@ -783,12 +792,12 @@ def quantize_mxfp8(x: torch.Tensor, dequant: bool = False, out: Optional[Quantiz
 # linear layers with 4-bit weights and 8- or 16-bit activations
 # ---------------------------------------------------------------------------
 
-def _w4_out(out, M, N, out_dtype, dev):
+def _w4_out(out, M, N, out_dtype, like):
     if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise TypeError("out_dtype must be bfloat16 or float32")
     if out is None:
-        return torch.empty((M, N), dtype=out_dtype, device=dev)
-    _check_dev("out", out, out_dtype, dev)
+        return like.new_empty((M, N), dtype=out_dtype)
+    _check_dev("out", out, out_dtype, like.device)
     if tuple(out.shape) != (M, N):
         raise ValueError(f"out must be a contiguous [{M}, {N}] tensor")
     return out
@@ -810,7 +819,7 @@ def mxfp4_linear(x: Quantized, w: Quantized, out_dtype: torch.dtype = torch.bflo
     N = w.codes.shape[0]
     if K % 32 or w.codes.shape[1] * 2 != K or x.scales.shape != (M, K // 32) or w.scales.shape != (N, K // 32):
         raise ValueError("operand shapes do not match: x [M, K], w [N, K] with K % 32 == 0")
-    y = _w4_out(out, M, N, out_dtype, dev)
+    y = _w4_out(out, M, N, out_dtype, x.codes)
     _launch(_lib.lib().focus_mxfp4_linear, dev, _p(x.codes), _p(x.scales), M, _p(w.codes), _p(w.scales), N, K, _p(y),
             0 if out_dtype == torch.float32 else 1)
     return y
@@ -839,7 +848,7 @@ def w4a16_linear(x: torch.Tensor, w: Quantized, out_dtype: torch.dtype = torch.b
             _check_dev("w.s2", w.s2, torch.float32, dev)
         if w.s2.numel() != 1:
             raise ValueError("w.s2 must hold one float")
-    y = _w4_out(out, M, N, out_dtype, dev)
+    y = _w4_out(out, M, N, out_dtype, x)
     _launch(_lib.lib().focus_w4a16_linear, dev, _p(x), M, 1 if w.s2 is None else 0, _p(w.codes), _p(w.scales),
             _p(w.s2), N, K, _p(y), 0 if out_dtype == torch.float32 else 1)
     return y
