@@ -589,6 +589,13 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void k_w4_tiled(W4Args a, uint32
         xpiece[i] = (lane % kXPer) ^ (row & kXMask);
         xoff[i] = (uint32_t)min(row, mlast) * (uint32_t)(K * (kMx ? 1 : 2)) + 16 * xpiece[i];
     }
+    // Direct: transfers whose rows are all behind the last token are left out;
+    // what LDS holds there feeds outputs that are never stored.
+    int nx = kXInst;
+    if (kDirect) {
+        const int rows = 64 / kXPer > 0 ? 64 / kXPer : 1;
+        nx = min(max((mlast / rows + 1) - wave * kXInst, 0), kXInst);
+    }
     auto wperm = [](int r) { return kWPer == 2 ? 0 : kWPer == 4 ? (r >> 1) & 3 : r & kWMask; };
 #pragma unroll
     for (int i = 0; i < kWInst; ++i) {
@@ -638,7 +645,8 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void k_w4_tiled(W4Args a, uint32
         }
         if (kDirect || s < full) {
 #pragma unroll
-            for (int i = 0; i < kXInst; ++i) to_lds16(xb, xoff[i], lds_address(xd + i * 1024));
+            for (int i = 0; i < kXInst; ++i)
+                if (i < nx) to_lds16(xb, xoff[i], lds_address(xd + i * 1024));
 #pragma unroll
             for (int i = 0; i < kWInst; ++i) to_lds16(wb, woff[i], lds_address(wd + i * 1024));
         } else {
@@ -762,6 +770,15 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void k_w4_tiled(W4Args a, uint32
                         wv[j][q], __builtin_bit_cast(bf16x8, xf[i % kRing][q]), acc[j][i], 0, 0, 0);
             }
     };
+    // all but this wavefront's last steps' transfers (with left-out ones among
+    // them at least those)
+    auto wait_steps = [&](auto steps) {
+        constexpr int n = decltype(steps)::value;
+        if (nx == kXInst)
+            wait_transfers<n * kInst>();
+        else
+            wait_transfers<n * (kInst - kXInst)>();
+    };
     // step s with its fragments f, in stage `cur`; reads the next step's
     // fragments into n.  The transfer that starts goes into the stage of s - 1.
     auto step = [&](int s, const uint8_t* cur, uint8_t* next, uint8_t* last, const Frags& f, Frags& n) {
@@ -772,8 +789,9 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void k_w4_tiled(W4Args a, uint32
             products(i, f);
         }
         if (s + 1 < nsteps) store_scales(next);
+        // s + 1 has landed, s + 2 .. s + kStages - 2 are under way
         if (kStages > 3 && s + kStages - 2 < nsteps)
-            wait_transfers<(kStages - 3) * kInst>();  // s + 1 has landed, s + 2 .. s + kStages - 2 are under way
+            wait_steps(std::integral_constant<int, kStages - 3>{});
         else
             wait_transfers<0>();
         __syncthreads();
@@ -793,7 +811,7 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void k_w4_tiled(W4Args a, uint32
         for (int i = 1; i < kStages - 1; ++i)
             if (i < nsteps) load(i, lds + i * kStageBytes);
         if (kStages > 3 && kStages - 2 < nsteps)
-            wait_transfers<(kStages - 2) * kInst>();
+            wait_steps(std::integral_constant<int, kStages - 2>{});
         else
             wait_transfers<0>();
         __syncthreads();
@@ -1179,8 +1197,8 @@ hipError_t decode_16(const W4Args& a, int64_t cus, hipStream_t stream) {
 inline int64_t tiles(const W4Args& a, int bm, int bn) { return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); }
 
 // Up to 4 tokens always, up to 8 where tiles of 32 x 32 would all be resident:
-// 8 x 4096 x 4096 5.1 against 5.5 (MXFP8), 6.3 against 8.5 (BF16 x NVFP4); but
-// 8 x 14336 x 4096 10.6 against 8.4, and 13.3 against 12.1; 16 x 4096 x 4096 6.1
+// 8 x 4096 x 4096 5.1 against 5.5 (MXFP8), 6.3 against 8.0 (BF16 x NVFP4); but
+// 8 x 14336 x 4096 10.6 against 8.4, and 13.1 against 11.9; 16 x 4096 x 4096 6.1
 // against 5.5, 16 x 4096 x 14336 21.6 against 21.4 (NVFP4).
 bool decode_fits(const W4Args& a, int64_t cus) { return a.M <= 4 || (a.M <= 8 && tiles(a, 32, 32) <= cus); }
 
@@ -1216,23 +1234,25 @@ hipError_t direct_mx(const W4Args& a, int64_t cus, hipStream_t stream) {
 }
 
 // BF16 activations likewise, but with two workgroups per CU where their stages
-// leave room (32 x 64 in steps of 256, 64 x 64 for NVFP4, whose widening costs
-// more, and 128 x 128).  NVFP4, tiles of 32 x 32, 32 x 64 in steps of 512, 32 x 64,
-// 64 x 64, 64 x 128: 61 x 4096 x 4096 10.0, 11.4, 12.7, 16.3, -; 61 x 6144 x 4096
-// 17.1, 11.8, 13.0, 16.5, -; 61 x 14336 x 4096 31, 21.3, 18.8, 17.7, 26;
-// 32 x 28672 x 8192 70, 50, 45, 67, -; 64 x 128, 128 x 128, 256 x 256:
-// 512 x 4096 x 4096 24.9, 40, 89; 256 x 14336 x 4096 45.9, 42.0, 90;
-// 512 x 14336 x 4096 89, 82, 90; 1024 x 14336 x 4096 154, -, 106.
+// leave room (64 x 64 for NVFP4, whose widening costs more, and 128 x 128).
+// NVFP4, tiles of 32 x 32, 32 x 64 in steps of 512 and of 256, 64 x 64, 32 x 128,
+// 64 x 128: 61 x 4096 x 4096 10.3, 11.9, 13.0, 17, -, -; 61 x 6144 x 4096 17.1, 11.8,
+// 13.0, 16.5, -, -; 61 x 14336 x 4096 31, 21.5, 19.1, 17.6, 18.3, 23;
+// 8 x 28672 x 8192 55, 39, 36, 64, 34.2, 42; 64 x 28672 x 8192 -, -, 75, 70, 64, 48;
+// 64 x 128, 128 x 128, 256 x 256: 512 x 4096 x 4096 24.9, 40, 89;
+// 256 x 14336 x 4096 45.9, 42.0, 90; 512 x 14336 x 4096 89, 82, 90;
+// 1024 x 14336 x 4096 154, -, 106.
 template <int KIND, bool BF16_OUT>
 hipError_t direct_bf16(const W4Args& a, int64_t cus, hipStream_t stream) {
     if (a.K % 512 == 0) {
         if (tiles(a, 32, 32) <= cus) return run_tiled<KIND, 512, 32, 32, 1, 2, 4, 3, BF16_OUT>(a, stream);
         if (tiles(a, 32, 64) <= cus) return run_tiled<KIND, 512, 32, 64, 1, 4, 4, 3, BF16_OUT>(a, stream);
     }
+    if (tiles(a, 32, 64) <= cus) return run_tiled<KIND, 256, 32, 64, 1, 4, 2, 4, BF16_OUT>(a, stream);
     if constexpr (KIND == kW4Bf16Nvfp4) {
         if (a.M > 32 && tiles(a, 64, 64) <= cus) return run_tiled<KIND, 256, 64, 64, 1, 4, 2, 3, BF16_OUT>(a, stream);
     }
-    if (tiles(a, 32, 64) <= 2 * cus) return run_tiled<KIND, 256, 32, 64, 1, 4, 2, 3, BF16_OUT>(a, stream);
+    if (tiles(a, 32, 128) <= cus) return run_tiled<KIND, 256, 32, 128, 1, 4, 2, 4, BF16_OUT>(a, stream);
     if (tiles(a, 64, 128) <= cus) return run_tiled<KIND, 256, 64, 128, 1, 4, 2, 3, BF16_OUT>(a, stream);
     if (tiles(a, 128, 128) <= 2 * cus) return run_tiled<KIND, 128, 128, 128, 2, 4, 1, 3, BF16_OUT>(a, stream);
     if (big_fits<KIND>(a.K)) return run_big<KIND, BF16_OUT>(a, cus, stream);

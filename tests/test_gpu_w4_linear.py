@@ -306,7 +306,7 @@ def test_many_tiles_spread(focus, fmt):
 @pytest.mark.parametrize("M,N,K", [(9, 40, 512), (33, 129, 2560), (61, 4000, 1536), (20, 9000, 1536), (61, 6000, 1024),
                                    (100, 4100, 768), (70, 300, 256), (61, 14000, 768), (20, 14000, 1280),
                                    (8, 9000, 4608), (100, 14003, 512), (250, 14000, 1024), (500, 14000, 768),
-                                   (130, 4001, 4352)])
+                                   (130, 4001, 4352), (30, 4000, 1280), (10, 18100, 2048), (17, 2050, 1024)])
 def test_whole_steps(focus, fmt, M, N, K):
     c = Case(focus, fmt, M, N, K, seed=M + K, exact=True)
     buf = torch.full((M + 1, N), 7.0, device=DEV)
