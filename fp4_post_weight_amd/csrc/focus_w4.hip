@@ -1212,13 +1212,14 @@ bool direct_fits(const W4Args& a) {
 // of few workgroups costs as much as a full one), else the largest, which moves
 // the fewest bytes per product.  Small tiles have several wavefronts per output
 // that split the step (61 x 6144 x 4096 of NVFP4: 11.8 with four, 13.0 with two,
-// 15.7 with one) and up to six stages (100 x 4096 x 4096 of MXFP8 8.5 with four,
-// 9.3 with three).
+// 15.7 with one; 1024 x 4096 x 4096 of MXFP8 in 128 x 128: 22.4 with two, 26.5 with
+// one) and up to four stages (100 x 4096 x 4096 of MXFP8 8.5 with four, 9.3 with
+// three).
 // MXFP8, tiles of 32 x 32, 32 x 64, 64 x 64, 64 x 128: 32 x 4096 x 4096 5.8, 6.7,
 // 8.6, -; 100 x 4096 x 4096 -, 7.7, 10.3, -; 100 x 14336 x 4096 -, -, 15.1, 13.6;
-// 64 x 128, 128 x 128, 256 x 128, 256 x 256: 300 x 4096 x 4096 13.2, 23, 31, 46;
-// 512 x 6144 x 4096 24.5, 22.8, 36, 47; 512 x 14336 x 4096 49, 44, 37, 47;
-// 1024 x 14336 x 4096 85, 81, 77, 53.
+// 64 x 128, 128 x 128, 256 x 128, 256 x 256: 512 x 4096 x 4096 15.3, 20.3, 36, 46;
+// 512 x 6144 x 4096 25.3, 20.8, 36, 47; 512 x 14336 x 4096 49, 39.5, 37, 47;
+// 1024 x 14336 x 4096 82, 75, 77, 53.
 template <bool BF16_OUT>
 hipError_t direct_mx(const W4Args& a, int64_t cus, hipStream_t stream) {
     if (a.K % 512 == 0) {
@@ -1227,7 +1228,7 @@ hipError_t direct_mx(const W4Args& a, int64_t cus, hipStream_t stream) {
     }
     if (tiles(a, 64, 64) <= cus) return run_tiled<kW4Mx, 256, 64, 64, 2, 2, 2, 4, BF16_OUT>(a, stream);
     if (tiles(a, 64, 128) <= cus) return run_tiled<kW4Mx, 256, 64, 128, 2, 2, 2, 4, BF16_OUT>(a, stream);
-    if (tiles(a, 128, 128) <= cus) return run_tiled<kW4Mx, 128, 128, 128, 2, 4, 1, 6, BF16_OUT>(a, stream);
+    if (tiles(a, 128, 128) <= cus) return run_tiled<kW4Mx, 256, 128, 128, 2, 2, 2, 3, BF16_OUT>(a, stream);
     if (tiles(a, 256, 128) <= cus) return run_tiled<kW4Mx, 128, 256, 128, 4, 2, 1, 3, BF16_OUT>(a, stream);
     if (big_fits<kW4Mx>(a.K)) return run_big<kW4Mx, BF16_OUT>(a, cus, stream);
     return run_tiled<kW4Mx, 128, 256, 256, 2, 4, 1, 0, BF16_OUT>(a, stream);
