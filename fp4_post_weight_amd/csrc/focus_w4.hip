@@ -490,7 +490,10 @@ __device__ __forceinline__ int w_row(int t) {
 // Stores a wavefront's accumulators: register r of lane (c16, g) in acc[j][i] is
 // column n0 + 16 j + 4 g + r of token m0 + 16 i (m0 includes c16), or with PAIR
 // column n0 + 32 (j / 2) + 8 g + 4 (j % 2) + r.  wide: a lane's columns are
-// aligned in y and all present or all absent; whole: all of it is in range.
+// aligned in y and all present or all absent; whole: all of it is in range.  The
+// stores are ordinary ones: the L2 joins lines that a wavefront writes in parts
+// (rows of 18000 bytes, 5000 x 9000 x 640 of MXFP8: 39 us against 72 with stores
+// past the caches; rows of 28672 bytes, 8192 x 14336 x 4096, the same within 1 %).
 template <int TM, int TN, bool BF16_OUT, bool PAIR>
 __device__ __forceinline__ void store_tile(f32x4 (&acc)[TN][TM], const W4Args& a, int64_t m0, int64_t n0, int g, float s2,
                                            bool wide, bool whole) {
@@ -510,11 +513,11 @@ __device__ __forceinline__ void store_tile(f32x4 (&acc)[TN][TM], const W4Args& a
                 if constexpr (PAIR) {
                     const u32x4 p = {bf16_pair(v[0][0], v[0][1]), bf16_pair(v[0][2], v[0][3]),
                                      bf16_pair(v[C - 1][0], v[C - 1][1]), bf16_pair(v[C - 1][2], v[C - 1][3])};
-                    __builtin_nontemporal_store(p, reinterpret_cast<u32x4*>(h));
+                    *reinterpret_cast<u32x4*>(h) = p;
                 } else if constexpr (BF16_OUT) {
                     *reinterpret_cast<uint2*>(h) = make_uint2(bf16_pair(v[0][0], v[0][1]), bf16_pair(v[0][2], v[0][3]));
                 } else {
-                    __builtin_nontemporal_store(v[0], reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.y) + row * a.N + col));
+                    *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.y) + row * a.N + col) = v[0];
                 }
             } else {
 #pragma unroll
@@ -878,9 +881,10 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void k_w4_tiled(W4Args a, uint32
 // reading phase, the rest between the products that do not need them yet.
 //
 // Measured against the same tile with one barrier per step and fragments read
-// under a wavefront's own products (k_w4_tiled), us: MXFP8 8192 x 14336 x 4096 366
-// against 473, 2.63 PFLOP/s; BF16 4096 x 14336 x 4096 405 against 471 (NVFP4, 1.19
-// PFLOP/s), 361 against 446 (MXFP4, 1.33).  MXFP8: 331 if nothing is stored; the
+// under a wavefront's own products (k_w4_tiled), us: MXFP8 8192 x 14336 x 4096 358
+// against 434, 2.69 PFLOP/s (366 with a byte read per subtile's scales instead
+// of one dword for four); BF16 4096 x 14336 x 4096 405 against 471 (NVFP4, 1.19
+// PFLOP/s), 361 against 446 (MXFP4, 1.33).  MXFP8: 331 of those 366 if nothing is stored; the
 // products alone would take 243 (the clock falls under them: 4.9 PFLOP/s on zeros,
 // 4.0 on random codes).
 // ---------------------------------------------------------------------------
@@ -892,6 +896,19 @@ __device__ __forceinline__ void phase_barrier() {
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
+}
+
+// Byte i of the result in lanes 16 g .. 16 g + 15: byte g of v in the lane 16 i
+// + (this lane mod 16).
+__device__ __forceinline__ uint32_t transpose_bytes(uint32_t v, int g) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(v, v, false, false));        // lanes 0..31, 32..63
+    const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(a[0], a[0], false, false));  // of 0, 1
+    const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(a[1], a[1], false, false));  // of 2, 3
+    // bytes 0..3 of a selector name the second operand's, 4..7 the first's, 12 is 0
+    const uint32_t l = __builtin_amdgcn_perm(lo[1], lo[0], 0x0C0C0400u + 0x0101u * g);
+    const uint32_t h = __builtin_amdgcn_perm(hi[1], hi[0], 0x04000C0Cu + 0x01010000u * g);
+    return l | h;
 }
 
 template <int KIND, bool BF16_OUT>
@@ -959,11 +976,21 @@ __global__ __launch_bounds__(512) void k_w4_big(W4Args a, uint32_t tiles_m, uint
             if (lt < total) source();
         }
     };
-    // Chunks of scales alternate between two areas.
+    // Chunks of scales alternate between two areas.  MXFP8: by step, then 64 rows
+    // at a time a dword of lane (c16, g): block g of the rows c16 + 16 i, so that
+    // one read gives a lane its scales of 4 subtiles and the instruction selects
+    // one.  Else 16 bytes per row.
     uint8_t* const scales = lds + 3 * kStage;
     int filled = 0;
     auto store_scales = [&]() {
-        if (kSRows == 512 || tid < kSRows) *reinterpret_cast<u32x4*>(scales + filled * kSBytes + tid * 16) = sreg;
+        uint8_t* const area = scales + filled * kSBytes;
+        if constexpr (kMx) {
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                *reinterpret_cast<uint32_t*>(area + b * kSRows * 4 + tid * 4) = transpose_bytes(sreg[b], g);
+        } else if (tid < kSRows) {
+            *reinterpret_cast<u32x4*>(area + tid * 16) = sreg;
+        }
         filled ^= 1;
     };
 
@@ -973,27 +1000,31 @@ __global__ __launch_bounds__(512) void k_w4_big(W4Args a, uint32_t tiles_m, uint
     const int xat = (mrow + c16) * kXRow + 16 * ((kMx ? g : 2 * g) ^ (c16 & 7)), xother = kMx ? 64 : 16;
     const int wat = kXBytes + (nrow + c16) * kWRow + (kMx ? 16 * (g ^ ((c16 >> 1) & 3)) : 8 * g);
     const int sg = kSb == 2 ? g >> 1 : g;
-    const int sxat = (mrow + c16) * 16 + sg, swat = ((kMx ? BM : 0) + nrow + c16) * 16 + sg;
+    const int sxat = (mrow + lane) * 4, swat = kMx ? (BM + nrow + lane) * 4 : (nrow + c16) * 16 + sg;
     uint4 w[kMx ? TN : 1], x[TM][2];
-    uint32_t ws[TN], xs[kMx ? TM : 1];
+    uint32_t ws[kMx ? TN / 4 : TN], xs[TM / 4];
     bf16x8 wv[kMx ? 1 : TN][2];
     auto read_x = [&](const uint8_t* st, const uint8_t* sc) {
+        if constexpr (kMx) {
+#pragma unroll
+            for (int i = 0; i < TM / 4; ++i) xs[i] = *reinterpret_cast<const uint32_t*>(sc + sxat + i * 256);
+        }
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
             x[i][0] = *reinterpret_cast<const uint4*>(st + xat + i * 16 * kXRow);
             x[i][1] = *reinterpret_cast<const uint4*>(st + (xat ^ xother) + i * 16 * kXRow);
-            if constexpr (kMx) xs[i] = sc[sxat + i * 256];
         }
     };
     uint2 wc[kMx ? 1 : TN];
     auto read_w = [&](const uint8_t* st, const uint8_t* sc) {
+        if constexpr (kMx) ws[0] = *reinterpret_cast<const uint32_t*>(sc + swat);
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
             if constexpr (kMx)
                 w[j] = *reinterpret_cast<const uint4*>(st + wat + j * 16 * kWRow);
             else
                 wc[j] = *reinterpret_cast<const uint2*>(st + wat + j * 16 * kWRow);
-            ws[j] = sc[swat + j * 256];
+            if constexpr (!kMx) ws[j] = sc[swat + j * 256];
         }
     };
     auto widen = [&](int from, int to) {
@@ -1020,7 +1051,7 @@ __global__ __launch_bounds__(512) void k_w4_big(W4Args a, uint32_t tiles_m, uint
             for (int i = 0; i < TM; ++i)
 #pragma unroll
                 for (int j = 0; j < TN; ++j)
-                    acc[j][i] = mfma_tile<0, 0>(w[j], x[i][0], x[i][1], ws[j], xs[i], acc[j][i]);
+                    acc[j][i] = mfma_tile(j, i % 4, w[j], x[i][0], x[i][1], ws[0], xs[i / 4], acc[j][i]);
         } else {
             // columns 16 .. 63 are widened under the first columns' products
             widen(1, TN);
@@ -1079,7 +1110,8 @@ __global__ __launch_bounds__(512) void k_w4_big(W4Args a, uint32_t tiles_m, uint
                 load_scales();
                 chunk = true;
             }
-            const uint8_t* const sc = scales + used * kSBytes + s * kSb - min((s - s % kChunk) * kSb, nb - 16);
+            const int at = s * kSb - min((s - s % kChunk) * kSb, nb - 16);  // in the chunk's 16 bytes
+            const uint8_t* const sc = scales + used * kSBytes + (kMx ? at * kSRows : at);
             __builtin_amdgcn_sched_barrier(0);
             if (!kMx) read_w(s0, sc);  // widened while the rest comes
             __builtin_amdgcn_sched_barrier(0);
