@@ -730,7 +730,7 @@ def _gated_input(name, t):
     stride, one = t.stride()
     if cols > 1 and one != 1:
         raise ValueError(f"the elements of {name}'s rows must be contiguous")
-    if rows <= 1:
+    if rows <= 1 or cols == 0:
         return cols
     if stride < cols or stride % 8:
         raise ValueError(f"{name}'s rows must be at least {cols} elements apart, by a multiple of 8")
