@@ -11,7 +11,13 @@
 //    are stored.  A lane holds one 32-block of a W row and its scale byte, and
 //    two 16-element halves of the X row.  The instruction aligns the products
 //    of each 8 consecutive k to the largest exponent among them and truncates
-//    to 2^-13 of it (measured); the sums of those groups are binary32.
+//    to 2^-13 of it (measured); the sums of those groups are binary32.  A BF16
+//    result takes that: on ordinary activations it is 1.2e-5 of the result, and
+//    the rounding to BF16 1.7e-3.  For an FP32 result the X codes go through the
+//    instruction in two parts (codes_part) and no product loses a bit: 2e-8 of
+//    the result, that of a binary32 sum.  Measured for FP32 results, two parts
+//    against one, us: 1 x 4096 x 14336 9.1 and 8.9, 8 x 14336 x 4096 10.5 and 8.4,
+//    100 x 14336 x 4096 21.6 and 15.0, 8192 x 14336 x 4096 708 and 407.
 //  * BF16 activations: every c * S is exact in BF16 (at most 6 significant
 //    bits), so weights are widened in registers and the product runs on
 //    v_mfma_f32_16x16x32_bf16 with binary32 sums.  MXFP4's power-of-two scale
@@ -91,6 +97,32 @@ __device__ __forceinline__ f32x4 mfma_mx(const uint4& lo, const uint4& hi, const
     const i32x8 a = {(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
     const i32x8 b = {(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0};
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 0, 4, J, (int)xs, J, (int)ws);
+}
+
+// Part P of 16 E4M3 codes in PARTS: of 2, part 0 keeps those of magnitude 2 and
+// above (bit 6; NaN among them) and part 1 the rest, with zeros elsewhere.  The
+// exponents are then at most 8 and at least 1, or at most 0 with a last bit of
+// at least 2^-9; E2M1's are at most 2 with a last bit of at least 2^-1.  So every
+// product is a multiple of 2^-3 where the exponent sums are at most 10, and of
+// 2^-10 where they are at most 2: nothing lies below 2^-13 of the largest.
+template <int PARTS, int P>
+__device__ __forceinline__ uint4 codes_part(const uint4& v) {
+    if constexpr (PARTS == 1) {
+        return v;
+    } else {
+        auto one = [](uint32_t c) {
+            const uint32_t b = (c >> 6) & 0x01010101u, m = (b << 8) - b;
+            return P == 0 ? c & m : c & ~m;
+        };
+        return make_uint4(one(v.x), one(v.y), one(v.z), one(v.w));
+    }
+}
+
+// Calls f(part number) for each of PARTS.
+template <int PARTS, typename F>
+__device__ __forceinline__ void for_parts(F f) {
+    f(std::integral_constant<int, 0>{});
+    if constexpr (PARTS == 2) f(std::integral_constant<int, 1>{});
 }
 
 __device__ __forceinline__ uint32_t pick(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
@@ -180,6 +212,7 @@ struct QuarterX {
 template <int KIND, bool BF16_OUT, int WAVES, int T, int MT>
 __global__ __launch_bounds__(64 * WAVES) void k_w4_decode(W4Args a, int64_t tiles_n) {
     constexpr bool kMx = KIND == kW4Mx, kNv = KIND == kW4Bf16Nvfp4;
+    constexpr int kParts = BF16_OUT ? 1 : 2;
     constexpr int kScaleDwords = StepW<KIND, T>::kDwords;
     constexpr int kStage = WAVES * 16 * T * kStageRow;
     constexpr int kRed = WAVES * MT * T * 256 * 4;
@@ -253,9 +286,12 @@ __global__ __launch_bounds__(64 * WAVES) void k_w4_decode(W4Args a, int64_t tile
         if constexpr (kMx) {
 #pragma unroll
             for (int m = 0; m < MT; ++m)
+                for_parts<kParts>([&](auto pc) {
+                    constexpr int p = decltype(pc)::value;
+                    const uint4 lo = codes_part<kParts, p>(x.v[m][0]), hi = codes_part<kParts, p>(x.v[m][1]);
 #pragma unroll
-                for (int t = 0; t < T; ++t)
-                    acc[m][t] = mfma_mx<j>(x.v[m][0], x.v[m][1], wf[t], xsc[m], sc[t][0], acc[m][t]);
+                    for (int t = 0; t < T; ++t) acc[m][t] = mfma_mx<j>(lo, hi, wf[t], xsc[m], sc[t][0], acc[m][t]);
+                });
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -544,6 +580,7 @@ template <int KIND, int KS, int BM, int BN, int WM, int WN, int WK, int STAGES, 
 __global__ __launch_bounds__(64 * WM * WN * WK) void k_w4_tiled(W4Args a, uint32_t tiles_m, uint32_t tiles_n) {
     constexpr bool kMx = KIND == kW4Mx, kNv = KIND == kW4Bf16Nvfp4;
     constexpr int kWaves = WM * WN * WK, kThreads = 64 * kWaves;
+    constexpr int kParts = BF16_OUT ? 1 : 2;                                      // of X, for MXFP8
     constexpr bool kDirect = STAGES > 0;                                          // whole steps; scales transferred too
     constexpr int kStages = kDirect ? STAGES : 3;
     constexpr int TM = BM / WM / 16, TN = BN / WN / 16;                          // 16 x 16 subtiles per wavefront
@@ -761,17 +798,24 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void k_w4_tiled(W4Args a, uint32
     };
     auto products = [&](int i, const Frags& f) {
 #pragma unroll
-        for (int q = 0; q < (kMx ? NJ : NP); ++q)
+        for (int q = 0; q < (kMx ? NJ : NP); ++q) {
+            if constexpr (kMx) {
+                for_parts<kParts>([&](auto pc) {
+                    constexpr int p = decltype(pc)::value;
+                    const uint4 lo = codes_part<kParts, p>(xf[i % kRing][kMx ? 2 * q : 0]);
+                    const uint4 hi = codes_part<kParts, p>(xf[i % kRing][kMx ? 2 * q + 1 : 0]);
 #pragma unroll
-            for (int j = 0; j < TN; ++j) {
-                if constexpr (kMx)
-                    acc[j][i] = mfma_tile(kGroup ? j % 4 : q, kGroup ? i % 4 : q, f.w[j][q], xf[i % kRing][kMx ? 2 * q : 0],
-                                          xf[i % kRing][kMx ? 2 * q + 1 : 0], f.ws[kGroup ? j / 4 : j],
-                                          f.xs[kGroup ? i / 4 : i], acc[j][i]);
-                else
+                    for (int j = 0; j < TN; ++j)
+                        acc[j][i] = mfma_tile(kGroup ? j % 4 : q, kGroup ? i % 4 : q, f.w[j][q], lo, hi, f.ws[kGroup ? j / 4 : j],
+                                              f.xs[kGroup ? i / 4 : i], acc[j][i]);
+                });
+            } else {
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
                     acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
                         wv[j][q], __builtin_bit_cast(bf16x8, xf[i % kRing][q]), acc[j][i], 0, 0, 0);
             }
+        }
     };
     // all but this wavefront's last steps' transfers (with left-out ones among
     // them at least those)
@@ -915,6 +959,7 @@ template <int KIND, bool BF16_OUT>
 __global__ __launch_bounds__(512) void k_w4_big(W4Args a, uint32_t tiles_m, uint32_t tiles_n) {
     constexpr bool kMx = KIND == kW4Mx, kNv = KIND == kW4Bf16Nvfp4;
     constexpr int BM = 256, BN = 256, TM = 8, TN = 4;  // subtiles of 16 x 16 per wavefront
+    constexpr int kParts = BF16_OUT ? 1 : 2;           // of X, for MXFP8
     constexpr int KS = kMx ? 128 : 64, kXRow = 128, kWRow = KS / 2;
     constexpr int kXInst = BM * kXRow / 8192, kWInst = BN * kWRow / 8192;  // transfers per wavefront and step
     constexpr int kWPer = kWRow / 16;
@@ -1049,9 +1094,12 @@ __global__ __launch_bounds__(512) void k_w4_big(W4Args a, uint32_t tiles_m, uint
         if constexpr (kMx) {
 #pragma unroll
             for (int i = 0; i < TM; ++i)
+                for_parts<kParts>([&](auto pc) {
+                    constexpr int p = decltype(pc)::value;
+                    const uint4 lo = codes_part<kParts, p>(x[i][0]), hi = codes_part<kParts, p>(x[i][1]);
 #pragma unroll
-                for (int j = 0; j < TN; ++j)
-                    acc[j][i] = mfma_tile(j, i % 4, w[j], x[i][0], x[i][1], ws[0], xs[i / 4], acc[j][i]);
+                    for (int j = 0; j < TN; ++j) acc[j][i] = mfma_tile(j, i % 4, w[j], lo, hi, ws[0], xs[i / 4], acc[j][i]);
+                });
         } else {
             // columns 16 .. 63 are widened under the first columns' products
             widen(1, TN);
