@@ -400,7 +400,8 @@ W4Args rows_from(const W4Args& args, int64_t row, int64_t most) {
 // per lane, and a wavefront waits by count, so that STAGES - 2 steps are under
 // way.  STAGES = 0: any K; three stages, the scale bytes of a row's step loaded a
 // step ahead into a register of the thread that owns the row, and a last step
-// begun only is filled up with zeros.
+// begun only is filled up with zeros.  W_REG (NVFP4 with K % 32 == 16, whose rows
+// of codes start at multiples of 8 bytes): W comes by registers too, a step ahead.
 //
 // A step has two halves around its one barrier, which says that every
 // wavefront has left step s - 1 and that the data of step s + 1 are in LDS.
@@ -576,7 +577,7 @@ __device__ __forceinline__ bool wide_rows(const W4Args& a) {
     return a.N % (PAIR ? 8 : 4) == 0 && ((uintptr_t)a.y & (BF16_OUT && !PAIR ? 7 : 15)) == 0;
 }
 
-template <int KIND, int KS, int BM, int BN, int WM, int WN, int WK, int STAGES, bool BF16_OUT>
+template <int KIND, int KS, int BM, int BN, int WM, int WN, int WK, int STAGES, bool BF16_OUT, bool W_REG>
 __global__ __launch_bounds__(64 * WM * WN * WK) void k_w4_tiled(W4Args a, uint32_t tiles_m, uint32_t tiles_n) {
     constexpr bool kMx = KIND == kW4Mx, kNv = KIND == kW4Bf16Nvfp4;
     constexpr int kWaves = WM * WN * WK, kThreads = 64 * kWaves;
@@ -604,6 +605,7 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void k_w4_tiled(W4Args a, uint32
     static_assert((kDirect || kSRows <= kThreads) && TM % kRing == 0, "one row's scales per thread; fragment ring");
     static_assert(!kDirect || ((!kMx || BM * kSb % 256 == 0) && kStages >= 3), "a transfer of scales is of one operand");
     static_assert(WK == 1 || (kDirect && KW >= 128), "a wavefront's part of a step");
+    static_assert(!W_REG || (kNv && !kDirect), "codes in registers");
     static_assert((WK - 1) * BM * BN * 4 <= kStages * kStageBytes, "room for partial sums");
     constexpr int kInst = kXInst + kWInst + kSInst;
     __shared__ __attribute__((aligned(256))) uint8_t lds[kStages * kStageBytes];
@@ -658,6 +660,7 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void k_w4_tiled(W4Args a, uint32
     const uint8_t* ssrc = kMx && tid < BM ? a.xs + (m0 + srow) * nb : a.ws + (n0 + srow) * nb;
     constexpr int kSDwords = (kSb + 3) / 4;
     uint32_t sreg[kSDwords];
+    uint4 wreg[W_REG ? kWInst : 1];
 
     auto load = [&](int s, uint8_t* st) {
         if (!kDirect && (kSRows == kThreads || tid < kSRows)) {
@@ -683,12 +686,17 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void k_w4_tiled(W4Args a, uint32
                 to_lds4(sb + (int64_t)s * kSb, soff[i], lds_address(st + kXBytes + kWBytes + at));
             }
         }
+        if constexpr (W_REG) {
+#pragma unroll
+            for (int i = 0; i < kWInst; ++i)
+                wreg[i] = s < full ? ld16_a8(wb + woff[i]) : codes_until(wb + woff[i], 32 * wpiece[i], K - s * KS);
+        }
         if (kDirect || s < full) {
 #pragma unroll
             for (int i = 0; i < kXInst; ++i)
                 if (i < nx) to_lds16(xb, xoff[i], lds_address(xd + i * 1024));
 #pragma unroll
-            for (int i = 0; i < kWInst; ++i) to_lds16(wb, woff[i], lds_address(wd + i * 1024));
+            for (int i = 0; i < (W_REG ? 0 : kWInst); ++i) to_lds16(wb, woff[i], lds_address(wd + i * 1024));
         } else {
             // the last, partial step: pieces past K are zeros
             const int left = K - s * KS;
@@ -699,16 +707,22 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void k_w4_tiled(W4Args a, uint32
                 *reinterpret_cast<uint4*>(xd + i * 1024 + 16 * lane) = v;
             }
 #pragma unroll
-            for (int i = 0; i < kWInst; ++i) {
+            for (int i = 0; i < (W_REG ? 0 : kWInst); ++i) {
                 uint4 v = make_uint4(0, 0, 0, 0);
                 if (32 * wpiece[i] < left) v = *reinterpret_cast<const uint4*>(wb + woff[i]);
                 *reinterpret_cast<uint4*>(wd + i * 1024 + 16 * lane) = v;
             }
         }
     };
-    auto store_scales = [&](uint8_t* st) {
+    // what `load` left in registers
+    auto store_regs = [&](uint8_t* st) {
         uint8_t* p = st + kXBytes + kWBytes;
         if (kDirect) return;
+        if constexpr (W_REG) {
+#pragma unroll
+            for (int i = 0; i < kWInst; ++i)
+                *reinterpret_cast<uint4*>(st + kXBytes + (wave * kWInst + i) * 1024 + 16 * lane) = wreg[i];
+        }
         if (kSRows == kThreads || tid < kSRows) {
             if (kGroup) {  // BM % 64 == 0
 #pragma unroll
@@ -835,7 +849,7 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void k_w4_tiled(W4Args a, uint32
             read_x(cur, i + kAhead);
             products(i, f);
         }
-        if (s + 1 < nsteps) store_scales(next);
+        if (s + 1 < nsteps) store_regs(next);
         // s + 1 has landed, s + 2 .. s + kStages - 2 are under way
         if (kStages > 3 && s + kStages - 2 < nsteps)
             wait_steps(std::integral_constant<int, kStages - 3>{});
@@ -853,7 +867,7 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void k_w4_tiled(W4Args a, uint32
     Frags f0, f1;
     if (nsteps > 0) {
         load(0, lds);
-        store_scales(lds);
+        store_regs(lds);
 #pragma unroll
         for (int i = 1; i < kStages - 1; ++i)
             if (i < nsteps) load(i, lds + i * kStageBytes);
@@ -1213,7 +1227,7 @@ hipError_t run_big(const W4Args& args, int64_t cus, hipStream_t stream) {
     return hipSuccess;
 }
 
-template <int KIND, int KS, int BM, int BN, int WM, int WN, int WK, int STAGES, bool BF16_OUT>
+template <int KIND, int KS, int BM, int BN, int WM, int WN, int WK, int STAGES, bool BF16_OUT, bool W_REG = false>
 hipError_t run_tiled(const W4Args& args, hipStream_t stream) {
     const int64_t tiles_n = (args.N + BN - 1) / BN;
     // runs of token tiles whose grid stays within 2^31 threads
@@ -1222,8 +1236,9 @@ hipError_t run_tiled(const W4Args& args, hipStream_t stream) {
     for (int64_t row = 0; row < args.M; row += most * BM) {
         const W4Args a = rows_from<KIND, BF16_OUT>(args, row, most * BM);
         const int64_t tiles_m = (a.M + BM - 1) / BM;
-        const hipError_t e = launch(&k_w4_tiled<KIND, KS, BM, BN, WM, WN, WK, STAGES, BF16_OUT>, dim3((unsigned)(tiles_m * tiles_n)),
-                                    dim3(64 * WM * WN * WK), stream, a, (uint32_t)tiles_m, (uint32_t)tiles_n);
+        const hipError_t e = launch(&k_w4_tiled<KIND, KS, BM, BN, WM, WN, WK, STAGES, BF16_OUT, W_REG>,
+                                    dim3((unsigned)(tiles_m * tiles_n)), dim3(64 * WM * WN * WK), stream, a, (uint32_t)tiles_m,
+                                    (uint32_t)tiles_n);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
@@ -1340,6 +1355,18 @@ hipError_t direct_bf16(const W4Args& a, int64_t cus, hipStream_t stream) {
     return run_tiled<KIND, 64, 256, 256, 2, 4, 1, 0, BF16_OUT>(a, stream);
 }
 
+// BF16 activations, tiles for other lengths.  W_REG: K % 32 == 16, for which
+// 16-byte transfers of W are not aligned.  K = 4112 and 4128: 61 x 14336 27.9 and
+// 25.3, 128 x 14336 37.8 and 35.2, 1024 x 4096 53 and 53, 8192 x 14336 980 and 890
+// (with the decode kernel 43.7, 80, 148, 4300 at K = 4112).
+template <int KIND, bool BF16_OUT, bool W_REG>
+hipError_t any_bf16(const W4Args& a, int64_t cus, hipStream_t stream) {
+    if (tiles(a, 32, 64) <= 2 * cus) return run_tiled<KIND, 256, 32, 64, 1, 4, 1, 0, BF16_OUT, W_REG>(a, stream);
+    if (tiles(a, 64, 128) <= 4 * cus) return run_tiled<KIND, 128, 64, 128, 1, 4, 1, 0, BF16_OUT, W_REG>(a, stream);
+    if (!W_REG && big_fits<KIND>(a.K)) return run_big<KIND, BF16_OUT>(a, cus, stream);
+    return run_tiled<KIND, 64, 256, 256, 2, 4, 1, 0, BF16_OUT, W_REG>(a, stream);
+}
+
 // Other lengths: decode up to 64 tokens, with two token tiles per wavefront from
 // 17, while at most 32 columns per workgroup fill the device (32 x 4096 x 14336
 // 20.7 against 27.5 with tiles of 32 x 64, but 32 x 14336 x 4096 13.5 against 11.3);
@@ -1359,12 +1386,10 @@ hipError_t pick_any(const W4Args& a, int64_t cus, hipStream_t stream) {
         if (big_fits<KIND>(a.K)) return run_big<KIND, BF16_OUT>(a, cus, stream);
         return run_tiled<KIND, 128, 256, 256, 2, 4, 1, 0, BF16_OUT>(a, stream);
     } else {
-        // the tiles' transfers of 16 bytes want K % 32 == 0
-        if (KIND == kW4Bf16Nvfp4 && a.K % 32 != 0) return run_decode<KIND, BF16_OUT, 4, 4, 2>(a, stream);
-        if (tiles(a, 32, 64) <= 2 * cus) return run_tiled<KIND, 256, 32, 64, 1, 4, 1, 0, BF16_OUT>(a, stream);
-        if (tiles(a, 64, 128) <= 4 * cus) return run_tiled<KIND, 128, 64, 128, 1, 4, 1, 0, BF16_OUT>(a, stream);
-        if (big_fits<KIND>(a.K)) return run_big<KIND, BF16_OUT>(a, cus, stream);
-        return run_tiled<KIND, 64, 256, 256, 2, 4, 1, 0, BF16_OUT>(a, stream);
+        if constexpr (KIND == kW4Bf16Nvfp4) {
+            if (a.K % 32 != 0) return any_bf16<KIND, BF16_OUT, true>(a, cus, stream);
+        }
+        return any_bf16<KIND, BF16_OUT, false>(a, cus, stream);
     }
 }
 
