@@ -427,8 +427,11 @@ __device__ __forceinline__ uint32_t lds_address(const uint8_t* p) {
 // base uniform).  The instruction has no register result, and its address
 // registers are read when it issues; it is complete after wait_transfers<0>().
 // Written out because the compiler, which cannot tell the stages apart, would
-// wait for every transfer before any LDS read.  m0 holds nothing of the
-// compiler's here: no other instruction of these kernels reads it.
+// wait for every transfer before any LDS read.  m0 is named as overwritten: the
+// compiler reserves it, sets it where an instruction of its own reads it, and so
+// never has such a pair around this one (it warns of any reserved register here).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void to_lds16(const uint8_t* base, uint32_t offset, uint32_t dst) {
     asm volatile(
         "s_mov_b32 m0, %0\n\t"
@@ -436,7 +439,7 @@ __device__ __forceinline__ void to_lds16(const uint8_t* base, uint32_t offset, u
         "global_load_lds_dwordx4 %1, %2"
         :
         : "s"(dst), "v"(offset), "s"(base)
-        : "memory");
+        : "memory", "m0");
 }
 
 // 4 bytes per lane, likewise; to `dst` + 4 * lane.
@@ -447,8 +450,10 @@ __device__ __forceinline__ void to_lds4(const uint8_t* base, uint32_t offset, ui
         "global_load_lds_dword %1, %2"
         :
         : "s"(dst), "v"(offset), "s"(base)
-        : "memory");
+        : "memory", "m0");
 }
+
+#pragma clang diagnostic pop
 
 // All but this wavefront's last N have landed (they do so in order).
 template <int N>
