@@ -152,7 +152,7 @@ __device__ __forceinline__ bf16x8 widen_nv(uint32_t c, float S) {
 }
 
 // Loads take a uniform address and a 32-bit offset of the lane (K <= kMaxW4K,
-// and a workgroup's rows are at most 128).  MASK: the last step, of which only
+// and a workgroup has at most 32 tokens and 64 columns).  MASK: the last step, of which only
 // the first `left` < kStep values of k exist.
 
 // One wavefront step's W: 4 T row pieces as loaded, and the scale bytes of
@@ -945,11 +945,12 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void k_w4_tiled(W4Args a, uint32
 //
 // Measured against the same tile with one barrier per step and fragments read
 // under a wavefront's own products (k_w4_tiled), us: MXFP8 8192 x 14336 x 4096 358
-// against 434, 2.69 PFLOP/s (366 with a byte read per subtile's scales instead
-// of one dword for four); BF16 4096 x 14336 x 4096 405 against 471 (NVFP4, 1.19
-// PFLOP/s), 361 against 446 (MXFP4, 1.33).  MXFP8: 331 of those 366 if nothing is stored; the
-// products alone would take 243 (the clock falls under them: 4.9 PFLOP/s on zeros,
-// 4.0 on random codes).
+// against 434, 2.69 PFLOP/s; BF16 4096 x 14336 x 4096 405 against 471 (NVFP4, 1.19
+// PFLOP/s), 361 against 446 (MXFP4, 1.33).  With a byte read per subtile's scales
+// instead of one dword for four the MXFP8 layer took 366, and 331 of these if
+// nothing was stored; the products alone take 243 (the clock falls under them:
+// 4.9 PFLOP/s on zeros, 4.0 on random codes).  An FP32 result, whose X codes go
+// through in two parts, takes 700-708.
 // ---------------------------------------------------------------------------
 
 // A barrier alone (the waits stand before it); nothing moves across it.
@@ -1319,7 +1320,8 @@ bool direct_fits(const W4Args& a) {
 // 8.6, -; 100 x 4096 x 4096 -, 7.7, 10.3, -; 100 x 14336 x 4096 -, -, 15.1, 13.6;
 // 64 x 128, 128 x 128, 256 x 128, 256 x 256: 512 x 4096 x 4096 15.3, 20.3, 36, 46;
 // 512 x 6144 x 4096 25.3, 20.8, 36, 47; 512 x 14336 x 4096 49, 39.5, 37, 47;
-// 1024 x 14336 x 4096 82, 75, 77, 53.
+// 1024 x 14336 x 4096 82, 75, 77, 53.  (BF16 results; FP32 results follow the same
+// rule.)
 template <bool BF16_OUT>
 hipError_t direct_mx(const W4Args& a, int64_t cus, hipStream_t stream) {
     if (a.K % 512 == 0) {
