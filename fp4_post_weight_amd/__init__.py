@@ -30,6 +30,9 @@ Calls (same names as the C ABI, without the ``focus_`` prefix):
   ``..._mxfp8``, a quantized one; ``quantize_mxfp8``
 * ``mxfp4_linear`` (MXFP8 activations, MXFP4 weights) and ``w4a16_linear``
   (BF16 activations, NVFP4 or MXFP4 weights)
+* The paged 8-bit cache of keys and values: ``KVCache`` and ``KVBatch`` name
+  its tensors and a step's rows, ``kv_cache_write`` (with the keys' rotation,
+  by the table of ``rope_table``), ``kv_cache_read`` and ``kv_attention``
 
 BF16 inputs are ``torch.bfloat16`` tensors; codes and scales are ``uint8``
 ([rows, cols/2] with element 2j in the low nibble, and [rows, cols/16] E4M3
@@ -51,6 +54,8 @@ __all__ = ["tensor_scale", "quantize", "dequantize", "quantize_act_per_token", "
            "quantize_mx", "quantize_mx_many", "dequantize_mx",
            "rmsnorm", "rmsnorm_nvfp4", "rmsnorm_mxfp8", "silu_mul", "silu_mul_nvfp4", "silu_mul_mxfp8",
            "quantize_mxfp8", "mxfp4_linear", "w4a16_linear",
+           "KVCache", "KVBatch", "rope_table", "kv_cache_write", "kv_cache_read", "kv_attention",
+           "kv_attention_workspace_bytes",
            "tensor_scale_many", "quantize_many", "dequantize_many", "Batch",
            "FocusError", "FocusLibraryMissing", "abi_version", "status_string", "library_path"]
 
@@ -856,6 +861,228 @@ def w4a16_linear(x: torch.Tensor, w: Quantized, out_dtype: torch.dtype = torch.b
     _launch(_lib.lib().focus_w4a16_linear, dev, _p(x), M, 1 if w.s2 is None else 0, _p(w.codes), _p(w.scales),
             _p(w.s2), N, K, _p(y), 0 if out_dtype == torch.float32 else 1)
     return y
+
+
+# ---------------------------------------------------------------------------
+# the paged 8-bit cache of keys and values, and the attention over it
+# ---------------------------------------------------------------------------
+
+class KVCache:
+    """The tensors of a paged cache, all ``uint8``: ``k_codes`` [pages,
+    kv_heads, page_tokens, head_dim] and ``v_codes`` [pages, kv_heads,
+    head_dim, page_tokens] E4M3, ``k_scales`` and ``v_scales`` [pages,
+    kv_heads] E8M0; head_dim 64 or 128, page_tokens 16, 32, 64 or 128.  The
+    object keeps them alive and may serve any number of calls."""
+
+    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "pages", "kv_heads", "head_dim", "page_tokens",
+                 "device", "_desc")
+
+    def __init__(self, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor,
+                 v_scales: torch.Tensor):
+        index = _on_gpu("k_codes", k_codes, torch.uint8)
+        dev = k_codes.device
+        for name, t in (("k_scales", k_scales), ("v_codes", v_codes), ("v_scales", v_scales)):
+            if not _fits(t, torch.uint8, index):
+                _check_dev(name, t, torch.uint8, dev)
+        if k_codes.dim() != 4:
+            raise ValueError("k_codes must be [pages, kv_heads, page_tokens, head_dim]")
+        pages, heads, page, dim = k_codes.shape
+        if dim not in (64, 128) or page not in (16, 32, 64, 128):
+            raise ValueError("head_dim must be 64 or 128 and page_tokens 16, 32, 64 or 128")
+        if not 1 <= heads <= 1024:
+            raise ValueError("kv_heads must be 1 to 1024")
+        if v_codes.shape != (pages, heads, dim, page):
+            raise ValueError(f"v_codes must be [{pages}, {heads}, {dim}, {page}]")
+        if k_scales.shape != (pages, heads) or v_scales.shape != (pages, heads):
+            raise ValueError(f"k_scales and v_scales must be [{pages}, {heads}]")
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.pages, self.kv_heads, self.head_dim, self.page_tokens = pages, heads, dim, page
+        self.device = dev
+        self._desc = _lib.KVCacheDesc(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+                                      v_scales.data_ptr(), pages, heads, dim, page)
+
+    @classmethod
+    def zeros(cls, pages: int, kv_heads: int, head_dim: int, page_tokens: int = 64, device="cuda") -> "KVCache":
+        """A new cache whose pages hold zeros."""
+        def z(*shape):
+            return torch.zeros(shape, dtype=torch.uint8, device=device)
+        return cls(z(pages, kv_heads, page_tokens, head_dim), z(pages, kv_heads),
+                   z(pages, kv_heads, head_dim, page_tokens), z(pages, kv_heads))
+
+
+class KVBatch:
+    """A step's rows and their sequences: ``page_table`` [sequences, max_pages]
+    int32 (rows may lie further apart), ``lengths`` [sequences] int32 (tokens of
+    each sequence, the step's rows included) and, unless every sequence has one
+    row, ``cu_tokens`` [sequences + 1] int32 (sequence b has the rows
+    cu_tokens[b] .. cu_tokens[b+1]-1, its last ones) with ``tokens``, the number
+    of rows of the step's tensors.  Their values are read by the kernels of each
+    call, on the device.  The object keeps the tensors alive and may serve every
+    layer of a step."""
+
+    __slots__ = ("page_table", "lengths", "cu_tokens", "sequences", "tokens", "device", "_desc")
+
+    def __init__(self, page_table: torch.Tensor, lengths: torch.Tensor, cu_tokens: Optional[torch.Tensor] = None,
+                 tokens: Optional[int] = None):
+        index = _on_gpu("lengths", lengths, torch.int32)
+        dev = lengths.device
+        if lengths.dim() != 1:
+            raise ValueError("lengths must be 1-D [sequences]")
+        n = lengths.shape[0]
+        if not isinstance(page_table, torch.Tensor):
+            raise TypeError("page_table must be a torch.Tensor")
+        if page_table.dtype is not torch.int32:
+            raise TypeError(f"page_table must be {torch.int32}, got {page_table.dtype}")
+        if page_table.get_device() != index:
+            raise ValueError(f"page_table is on {page_table.device}, expected {dev}")
+        if page_table.dim() != 2 or page_table.shape[0] != n:
+            raise ValueError(f"page_table must be [{n}, max_pages]")
+        width = page_table.shape[1]
+        stride, one = page_table.stride()
+        if n <= 1 or width == 0:
+            stride = width
+        if (width > 1 and one != 1) or stride < width:
+            raise ValueError("page_table's rows must be contiguous and not overlap")
+        if cu_tokens is None:
+            if tokens is not None and tokens != n:
+                raise ValueError(f"without cu_tokens the batch has one row per sequence: {n}, not {tokens}")
+            tokens = n
+        else:
+            if not _fits(cu_tokens, torch.int32, index):
+                _check_dev("cu_tokens", cu_tokens, torch.int32, dev)
+            if cu_tokens.shape != (n + 1,):
+                raise ValueError(f"cu_tokens must be [{n + 1}]")
+            if tokens is None:
+                raise ValueError("cu_tokens needs tokens, the number of rows")
+            if tokens < 0:
+                raise ValueError("tokens must not be negative")
+        self.page_table, self.lengths, self.cu_tokens = page_table, lengths, cu_tokens
+        self.sequences, self.tokens, self.device = n, tokens, dev
+        self._desc = _lib.KVBatchDesc(page_table.data_ptr(), stride, width, lengths.data_ptr(), _p(cu_tokens), n,
+                                      tokens)
+
+
+def rope_table(positions: int, head_dim: int, base: float = 500000.0, inv_freq: Optional[torch.Tensor] = None,
+               device="cuda") -> torch.Tensor:
+    """The rotation's table [positions, head_dim] FP32: row p holds the cosines
+    and then the sines of p * inv_freq, formed in binary64.  ``inv_freq``
+    [head_dim / 2] float64 is base^(-2 i / head_dim) when None."""
+    if head_dim < 2 or head_dim % 2 or positions < 0:
+        raise ValueError("head_dim must be even and positive, positions not negative")
+    if inv_freq is None:
+        inv_freq = torch.tensor([float(base) ** (-2.0 * i / head_dim) for i in range(head_dim // 2)],
+                                dtype=torch.float64, device=device)
+    _check_buf("inv_freq", inv_freq, torch.float64, inv_freq.device, head_dim // 2)
+    out = torch.empty((positions, head_dim), dtype=torch.float32, device=inv_freq.device)
+    _launch(_lib.lib().focus_rope_table, inv_freq.device, _p(inv_freq), positions, head_dim, _p(out))
+    return out
+
+
+def _kv_rows(name, t, rows, cols, index):
+    """Row stride of a step's BF16 tensor [rows, cols] whose rows may lie apart."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected HIP device {index}")
+    if t.dim() != 2 or t.shape[0] != rows or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name} must be [{rows}, {'heads * head_dim' if cols is None else cols}]")
+    stride, one = t.stride()
+    width = t.shape[1]
+    if width > 1 and one != 1:
+        raise ValueError(f"the elements of {name}'s rows must be contiguous")
+    if rows <= 1:
+        return width
+    if stride < width or stride % 8:
+        raise ValueError(f"{name}'s rows must be at least {width} elements apart, by a multiple of 8")
+    return stride
+
+
+def _kv_rope(rope, dim, index):
+    if rope is None:
+        return 0, 0
+    if not _fits(rope, torch.float32, index):
+        _check_dev("rope", rope, torch.float32, torch.device("cuda", index))
+    if rope.dim() != 2 or rope.shape[1] != dim:
+        raise ValueError(f"rope must be [positions, {dim}]")
+    return rope.data_ptr(), rope.shape[0]
+
+
+def _kv_device(cache, batch):
+    if not isinstance(cache, KVCache) or not isinstance(batch, KVBatch):
+        raise TypeError("cache must be a KVCache and batch a KVBatch")
+    if cache.device != batch.device:
+        raise ValueError(f"the batch is on {batch.device}, the cache on {cache.device}")
+    return cache.device.index
+
+
+def kv_cache_write(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor,
+                   rope: Optional[torch.Tensor] = None) -> None:
+    """Write the batch's keys and values, [tokens, kv_heads * head_dim] BF16
+    (rows a multiple of 8 elements apart, as parts of one product's rows are),
+    into the cache.  ``rope`` (``rope_table``): keys turn by their position
+    first.  A page that gains tokens takes the larger scale, and its older codes
+    move to it.  Pages that are written must belong to one sequence each."""
+    index = _kv_device(cache, batch)
+    width = cache.kv_heads * cache.head_dim
+    ks, vs = _kv_rows("k", k, batch.tokens, width, index), _kv_rows("v", v, batch.tokens, width, index)
+    r, n = _kv_rope(rope, cache.head_dim, index)
+    _launch(_lib.lib().focus_kv_cache_write, cache.device, cache._desc, batch._desc, k.data_ptr(), ks, v.data_ptr(),
+            vs, r, n)
+
+
+def kv_cache_read(cache: KVCache, batch: KVBatch, k_out: Optional[torch.Tensor] = None,
+                  v_out: Optional[torch.Tensor] = None):
+    """Read the batch's rows back: (k, v), each [tokens, kv_heads, head_dim]
+    BF16.  Rows of no sequence are left as they are."""
+    _kv_device(cache, batch)
+    shape = (batch.tokens, cache.kv_heads, cache.head_dim)
+    outs = []
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if t is None:
+            t = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+        else:
+            _check_buf(name, t, torch.bfloat16, cache.device, shape[0] * shape[1] * shape[2])
+        outs.append(t)
+    _launch(_lib.lib().focus_kv_cache_read, cache.device, cache._desc, batch._desc, _p(outs[0]), _p(outs[1]))
+    return outs[0], outs[1]
+
+
+def kv_attention_workspace_bytes(cache: KVCache, batch: KVBatch, heads: int) -> int:
+    """Bytes of the workspace with which ``kv_attention`` splits the keys of
+    sequences with few rows as far as it helps."""
+    _kv_device(cache, batch)
+    return _lib.lib().focus_kv_attention_workspace_bytes(cache._desc, batch._desc, heads)
+
+
+def kv_attention(cache: KVCache, batch: KVBatch, q: torch.Tensor, rope: Optional[torch.Tensor] = None,
+                 scale: Optional[float] = None, softcap: float = 0.0, window: int = 0,
+                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Causal attention of the batch's queries ``q`` [tokens, heads * head_dim]
+    BF16 (rows a multiple of 8 elements apart) over the cache, each row over its
+    sequence's tokens up to its own position -> [tokens, heads * head_dim] BF16.
+    ``heads`` is a multiple of kv_heads.  ``rope``: queries turn by their
+    position first; ``scale`` is head_dim^-0.5 when None; ``softcap`` > 0 caps
+    scores, softcap * tanh(s / softcap); ``window`` > 0: a row sees that many
+    tokens at most, its own among them.  A row that sees no token gives zeros."""
+    index = _kv_device(cache, batch)
+    stride = _kv_rows("q", q, batch.tokens, None, index)
+    width, dim = q.shape[1], cache.head_dim
+    heads = width // dim
+    if heads < 1 or width % (cache.kv_heads * dim):
+        raise ValueError(f"q's rows must hold a multiple of {cache.kv_heads} heads of {dim}")
+    r, n = _kv_rope(rope, dim, index)
+    if out is None:
+        out = q.new_empty((batch.tokens, width))
+    else:
+        _check_buf("out", out, torch.bfloat16, cache.device, batch.tokens * width)
+    lib = _lib.lib()
+    need = lib.focus_kv_attention_workspace_bytes(cache._desc, batch._desc, heads)
+    ws = q.new_empty(need, dtype=torch.uint8) if need else None
+    _launch(lib.focus_kv_attention, cache.device, cache._desc, batch._desc, q.data_ptr(), stride, heads, r, n,
+            dim ** -0.5 if scale is None else scale, softcap, window, out.data_ptr(), _p(ws), need)
+    return out
 
 
 # ---------------------------------------------------------------------------

@@ -41,6 +41,18 @@ class LinearWeight(ct.Structure):
     _fields_ = [("w_codes", _VP), ("w_scales", _VP), ("w_s2", _VP), ("N", _I64), ("y", _VP)]
 
 
+class KVCacheDesc(ct.Structure):
+    _fields_ = [("k_codes", _VP), ("k_scales", _VP), ("v_codes", _VP), ("v_scales", _VP), ("pages", _I64),
+                ("kv_heads", _I64), ("head_dim", _I64), ("page_tokens", _I64)]
+
+
+class KVBatchDesc(ct.Structure):
+    _fields_ = [("page_table", _VP), ("table_stride", _I64), ("max_pages", _I64), ("lengths", _VP),
+                ("cu_tokens", _VP), ("sequences", _I64), ("tokens", _I64)]
+
+
+_CACHE, _BATCH = ct.POINTER(KVCacheDesc), ct.POINTER(KVBatchDesc)
+
 _SIGNATURES = {
     "focus_abi_version": (_INT, []),
     "focus_status_string": (ct.c_char_p, [_INT]),
@@ -77,6 +89,11 @@ _SIGNATURES = {
     "focus_quantize_mxfp8": (_INT, [_VP, _I64, _I64, _VP, _VP, _VP, _VP]),
     "focus_mxfp4_linear": (_INT, [_VP, _VP, _I64, _VP, _VP, _I64, _I64, _VP, _INT, _VP]),
     "focus_w4a16_linear": (_INT, [_VP, _I64, _INT, _VP, _VP, _VP, _I64, _I64, _VP, _INT, _VP]),
+    "focus_rope_table": (_INT, [_VP, _I64, _I64, _VP, _VP]),
+    "focus_kv_cache_write": (_INT, [_CACHE, _BATCH, _VP, _I64, _VP, _I64, _VP, _I64, _VP]),
+    "focus_kv_cache_read": (_INT, [_CACHE, _BATCH, _VP, _VP, _VP]),
+    "focus_kv_attention": (_INT, [_CACHE, _BATCH, _VP, _I64, _I64, _VP, _I64, _F32, _F32, _I64, _VP, _VP, _I64, _VP]),
+    "focus_kv_attention_workspace_bytes": (_I64, [_CACHE, _BATCH, _I64]),
 }
 
 EXPORTED = tuple(_SIGNATURES)

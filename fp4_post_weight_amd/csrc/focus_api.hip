@@ -2,9 +2,9 @@
 //
 // Every entry point validates all of its arguments on the host before the
 // first HIP call (so every error path runs without a GPU), then launches the
-// kernels of focus_kernels.hip, focus_gemm.hip, focus_rows.hip and
-// focus_w4.hip on the caller's stream.  Nothing is allocated
-// and no state is kept.  Batched calls read their descriptor arrays during
+// kernels of focus_kernels.hip, focus_gemm.hip, focus_rows.hip, focus_w4.hip,
+// focus_kv.hip and focus_attention.hip on the caller's stream.  Nothing is
+// allocated and no state is kept.  Batched calls read their descriptor arrays during
 // the call only and launch one kernel (one per phase for the tensor scale)
 // per run of up to focus::kBatch tensors.  The declarations, with the
 // meaning, layout and ownership of each argument, are in
@@ -13,6 +13,7 @@
 #include "focus_nvfp4.h"
 #include "focus_gemm.h"
 #include "focus_internal.h"
+#include "focus_kv.h"
 #include "focus_rows.h"
 #include "focus_w4.h"
 
@@ -693,6 +694,123 @@ int focus_w4a16_linear(const uint16_t* x_bf16, int64_t M, int w_format, const ui
                              w_format == 0 ? w_s2 : nullptr, N, K, y};
     return run_w4(a, w_format == 0 ? focus::kW4Bf16Nvfp4 : focus::kW4Bf16Mxfp4, w_format == 0 ? 16 : 32, y_dtype,
                   stream);
+}
+
+namespace {
+
+bool kv_empty(const focus_kv_batch& b) { return b.tokens == 0 || b.sequences == 0; }
+
+// The two descriptors; FOCUS_OK also for a batch without rows, whose pointers
+// are not looked at.
+int check_kv(const focus_kv_cache* c, const focus_kv_batch* b) {
+    if (!c || !b) return FOCUS_ERR_NULL;
+    if (c->pages < 0 || c->kv_heads < 1 || (c->head_dim != 64 && c->head_dim != 128)) return FOCUS_ERR_SHAPE;
+    if (c->page_tokens != 16 && c->page_tokens != 32 && c->page_tokens != 64 && c->page_tokens != 128)
+        return FOCUS_ERR_SHAPE;
+    if (c->pages >= kMaxTokens || c->kv_heads > 1024) return FOCUS_ERR_RANGE;
+    if (b->sequences < 0 || b->tokens < 0 || b->max_pages < 0 || b->table_stride < b->max_pages) return FOCUS_ERR_SHAPE;
+    if (b->sequences > ((int64_t)1 << 20) || b->tokens >= kMaxTokens || b->table_stride > ((int64_t)1 << 32) ||
+        b->max_pages > ((int64_t)1 << 30) / c->page_tokens)
+        return FOCUS_ERR_RANGE;
+    if (!b->cu_tokens && b->tokens != b->sequences) return FOCUS_ERR_SHAPE;
+    if (kv_empty(*b)) return FOCUS_OK;
+    if (c->pages == 0) return FOCUS_ERR_SHAPE;
+    if (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales || !b->lengths || (b->max_pages > 0 && !b->page_table))
+        return FOCUS_ERR_NULL;
+    if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(b->page_table, 4) || !aligned(b->lengths, 4) ||
+        !aligned(b->cu_tokens, 4))
+        return FOCUS_ERR_ALIGN;
+    return FOCUS_OK;
+}
+
+focus::KvCacheArgs kv_cache_args(const focus_kv_cache& c) {
+    int log_page = 4;
+    while (((int64_t)1 << log_page) < c.page_tokens) ++log_page;
+    return {c.k_codes, c.k_scales, c.v_codes, c.v_scales, (int)c.pages, (int)c.kv_heads, (int)c.head_dim, log_page};
+}
+
+focus::KvBatchArgs kv_batch_args(const focus_kv_batch& b) {
+    return {b.page_table, b.table_stride, (int)b.max_pages, b.lengths, b.cu_tokens, (int)b.sequences, (int)b.tokens};
+}
+
+// Rows of `width` BF16 elements, stride elements apart.
+int check_kv_rows(int64_t stride, int64_t width, int64_t tokens) {
+    if (stride < width || stride % 8 != 0) return FOCUS_ERR_SHAPE;
+    if (tokens != 0 && stride > kMaxElems / tokens) return FOCUS_ERR_SHAPE;
+    return FOCUS_OK;
+}
+
+int check_rope(const float* rope, int64_t positions) {
+    if (positions < 0) return FOCUS_ERR_SHAPE;
+    return aligned(rope, 16) ? FOCUS_OK : FOCUS_ERR_ALIGN;
+}
+
+}  // namespace
+
+int focus_rope_table(const double* inv_freq, int64_t positions, int64_t head_dim, float* table, void* stream) {
+    if (positions < 0 || head_dim < 0 || head_dim % 2 != 0) return FOCUS_ERR_SHAPE;
+    if (positions == 0 || head_dim == 0) return FOCUS_OK;
+    if (positions > ((int64_t)1 << 38) / head_dim) return FOCUS_ERR_RANGE;
+    if (!inv_freq || !table) return FOCUS_ERR_NULL;
+    if (!aligned(inv_freq, 8) || !aligned(table, 16)) return FOCUS_ERR_ALIGN;
+    return hip_status(focus::launch_rope_table(inv_freq, positions, head_dim, table, (hipStream_t)stream));
+}
+
+int focus_kv_cache_write(const focus_kv_cache* cache, const focus_kv_batch* batch, const uint16_t* k, int64_t k_stride,
+                         const uint16_t* v, int64_t v_stride, const float* rope, int64_t rope_positions, void* stream) {
+    int st = check_kv(cache, batch);
+    if (st != FOCUS_OK) return st;
+    const int64_t width = cache->kv_heads * cache->head_dim;
+    if ((st = check_kv_rows(k_stride, width, batch->tokens)) != FOCUS_OK) return st;
+    if ((st = check_kv_rows(v_stride, width, batch->tokens)) != FOCUS_OK) return st;
+    if ((st = check_rope(rope, rope_positions)) != FOCUS_OK) return st;
+    if (kv_empty(*batch)) return FOCUS_OK;
+    if (!k || !v) return FOCUS_ERR_NULL;
+    if (!aligned(k, 16) || !aligned(v, 16)) return FOCUS_ERR_ALIGN;
+    const focus::KvCacheArgs c = kv_cache_args(*cache);
+    const focus::KvBatchArgs b = kv_batch_args(*batch);
+    if (!focus::kv_pages_fit(c, b)) return FOCUS_ERR_RANGE;
+    return hip_status(focus::launch_kv_write(c, b, {rope, rope_positions}, k, k_stride, v, v_stride, (hipStream_t)stream));
+}
+
+int focus_kv_cache_read(const focus_kv_cache* cache, const focus_kv_batch* batch, uint16_t* k, uint16_t* v,
+                        void* stream) {
+    int st = check_kv(cache, batch);
+    if (st != FOCUS_OK || kv_empty(*batch)) return st;
+    if (!k || !v) return FOCUS_ERR_NULL;
+    if (!aligned(k, 16) || !aligned(v, 16)) return FOCUS_ERR_ALIGN;
+    const focus::KvCacheArgs c = kv_cache_args(*cache);
+    const focus::KvBatchArgs b = kv_batch_args(*batch);
+    if (!focus::kv_pages_fit(c, b)) return FOCUS_ERR_RANGE;
+    return hip_status(focus::launch_kv_read(c, b, k, v, (hipStream_t)stream));
+}
+
+int focus_kv_attention(const focus_kv_cache* cache, const focus_kv_batch* batch, const uint16_t* q, int64_t q_stride,
+                       int64_t heads, const float* rope, int64_t rope_positions, float scale, float softcap,
+                       int64_t window, uint16_t* y, void* workspace, int64_t workspace_bytes, void* stream) {
+    int st = check_kv(cache, batch);
+    if (st != FOCUS_OK) return st;
+    if (heads < 1 || heads % cache->kv_heads != 0) return FOCUS_ERR_SHAPE;
+    if (heads > 65536) return FOCUS_ERR_RANGE;
+    if ((st = check_kv_rows(q_stride, heads * cache->head_dim, batch->tokens)) != FOCUS_OK) return st;
+    if ((st = check_rope(rope, rope_positions)) != FOCUS_OK) return st;
+    const float big = 3.4028234e38f;
+    if (!(scale >= -big && scale <= big) || !(softcap >= 0.0f && softcap <= big)) return FOCUS_ERR_RANGE;
+    if (window < 0 || window >= kMaxTokens || workspace_bytes < 0) return FOCUS_ERR_RANGE;
+    if (kv_empty(*batch)) return FOCUS_OK;
+    if (!q || !y) return FOCUS_ERR_NULL;
+    if (!aligned(q, 16) || !aligned(y, 16) || !aligned(workspace, 16)) return FOCUS_ERR_ALIGN;
+    const focus::KvAttentionArgs a = {kv_cache_args(*cache), kv_batch_args(*batch), {rope, rope_positions}, q, q_stride,
+                                      (int)heads, scale, softcap, (int)window, y, static_cast<float*>(workspace),
+                                      workspace ? workspace_bytes : 0};
+    if (!focus::kv_attention_fits(a)) return FOCUS_ERR_RANGE;
+    return hip_status(focus::launch_kv_attention(a, (hipStream_t)stream));
+}
+
+int64_t focus_kv_attention_workspace_bytes(const focus_kv_cache* cache, const focus_kv_batch* batch, int64_t heads) {
+    if (check_kv(cache, batch) != FOCUS_OK || kv_empty(*batch)) return 0;
+    if (heads < 1 || heads % cache->kv_heads != 0 || heads > 65536) return 0;
+    return focus::kv_attention_workspace_bytes(kv_cache_args(*cache), kv_batch_args(*batch), (int)heads);
 }
 
 }  // extern "C"

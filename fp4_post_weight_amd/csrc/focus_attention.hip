@@ -1,0 +1,890 @@
+// focus_attention.hip -- attention over the paged 8-bit cache of keys and
+// values (focus_kv.hip) on gfx950 matrix cores:
+//     y_i = sum_j p_ij v_j / sum_j p_ij,   p_ij = exp(cap(scale q_i . k_j) - m_i)
+// over the tokens j of row i's sequence with pos_i - window < j <= pos_i, in
+// one pass with a running maximum m and sum.  Heads of the queries that share
+// a head of the cache are rows of one tile: row r of a sequence is its token
+// r / group and head r % group, so the cache is read once for all of them.
+//
+// Numbers.  Keys enter as FP16, which holds every E4M3 code exactly; their
+// page's power of two goes into the factor that takes a score to base 2
+// (16 tokens of a page share it).  Queries enter as FP16 too, times a power of
+// two per row that brings the row's largest element to 2^14..2^15: a BF16 query
+// loses nothing that is above 2^-28 of that largest one, and a turned one keeps
+// 11 bits.  Scores, maxima, sums and results are binary32.  Probabilities
+// meet the values in BF16: values are exact in it with their page's scale
+// (an operand of the conversion), whatever the scale, where FP16 would
+// not hold them.
+//
+// Both products are formed transposed, S^T = K Q^T and Y^T = V^T P^T: a lane
+// then holds scores of one query row (its column), and the four or eight
+// tokens that it holds are those that the second product wants from it, so P
+// goes from one product to the next in registers.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "focus_kv.h"
+#include "focus_launch.h"
+#include "focus_numerics.h"
+
+namespace focus {
+
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr int kShortRows = 64;  // rows (tokens x group) up to which a sequence is split over its keys
+
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Eight E4M3 codes in FP16 (exact).
+__device__ __forceinline__ f16x8 widen_f16(uint32_t lo, uint32_t hi) {
+    const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false), b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
+    const f16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false), d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
+    return (f16x8){a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// Eight E4M3 codes times S, a power of two, in BF16.
+__device__ __forceinline__ bf16x8 widen_bf16(uint32_t lo, uint32_t hi, float S) {
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, S, false), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, S, true);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, S, false), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, S, true);
+    return (bf16x8){a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+__device__ __forceinline__ float e8m0_f32(uint32_t byte) { return __uint_as_float(max(byte << 23, 0x00400000u)); }
+
+// Bytes of a dword whose E4M3 code is NaN (0x7F or 0xFF): their bit 7, moved to bit 0.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t c) {
+    const uint32_t m = c & 0x7F7F7F7Fu;
+    return ((m + 0x01010101u) >> 7) & 0x01010101u;
+}
+
+// The first n (0..4, or beyond) bytes of a dword.
+__device__ __forceinline__ uint32_t first_bytes(int n) { return n >= 4 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << (8 * n)) - 1u; }
+
+// A query row's elements d .. d+7 and their partners d + dim/2 .., turned.
+__device__ __forceinline__ void turn8(float (&lo)[8], float (&hi)[8], const RopeArgs& rope, int dim, int pos, int d) {
+    const int half = dim / 2;
+    const bool known = pos >= 0 && pos < rope.positions;
+    const float* t = rope.table + (known ? (int64_t)pos * dim + d : 0);
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+        const float4 c = *reinterpret_cast<const float4*>(t + i), s = *reinterpret_cast<const float4*>(t + half + i);
+        const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float a = lo[i + j], b = hi[i + j];
+            lo[i + j] = known ? a * cs[j] - b * sn[j] : __builtin_nanf("");
+            hi[i + j] = known ? b * cs[j] + a * sn[j] : __builtin_nanf("");
+        }
+    }
+}
+
+__device__ __forceinline__ void load8(const uint16_t* p, float (&f)[8]) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    f[0] = bf16_lo(v.x), f[1] = bf16_hi(v.x), f[2] = bf16_lo(v.y), f[3] = bf16_hi(v.y);
+    f[4] = bf16_lo(v.z), f[5] = bf16_hi(v.z), f[6] = bf16_lo(v.w), f[7] = bf16_hi(v.w);
+}
+
+// The exponent that brings a row of largest magnitude amax to 2^14..2^15.
+__device__ __forceinline__ int query_shift(float amax) {
+    if (!(amax > 0.0f) || !(amax < __builtin_inff())) return 0;
+    return 15 - __builtin_amdgcn_frexp_expf(amax);
+}
+
+// The products with exponents up to 2^15 and 2^8 over 128 elements stay far
+// within binary32.
+__device__ __forceinline__ f16x8 narrow(const float (&f)[8], int shift) {
+    f16x8 r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = (_Float16)__builtin_ldexpf(f[i], shift);
+    return r;
+}
+
+// What the scores' factor and cap need of the call.
+struct Scoring {
+    float c0;    // to base 2, or to the cap's argument
+    float cap2;  // cap * log2(e), 0 without a cap
+};
+
+__device__ __forceinline__ float capped(float s, float cap2) {
+    // tanh(s) = 1 - 2 / (exp(2 s) + 1)
+    const float e = exp2_hw(s * (2.0f * kLog2e));
+    return cap2 * (1.0f - 2.0f * __builtin_amdgcn_rcpf(e + 1.0f));
+}
+
+inline Scoring scoring(const KvAttentionArgs& a) {
+    if (a.softcap > 0.0f) return {a.scale / a.softcap, a.softcap * kLog2e};
+    return {a.scale * kLog2e, 0.0f};
+}
+
+// ---------------------------------------------------------------------------
+// few rows per sequence: split over the keys
+// ---------------------------------------------------------------------------
+//
+// The keys of all sequences are cut into chunks of equal length, so many that
+// they fill the GPU, and a workgroup takes one chunk of one head.  The lengths
+// are device memory: every workgroup adds them up, derives the chunk length and
+// finds its own.  A sequence of several chunks leaves unnormalised sums, and
+// their maximum, in the workspace, and a second kernel joins them in order.
+
+struct ShortPlan {
+    int64_t target;  // chunks per head to aim at; 0: one per sequence
+    int slots;       // workgroups per head and tile
+    int tiles;       // tiles of 16 rows
+    int rows;        // rows of a sequence, at most
+};
+
+constexpr int kShortWaves = 4, kShortStep = 64, kChunkUnit = kShortWaves * kShortStep;
+
+struct ShortSequence {
+    KvSequence s;
+    int begin, end;  // keys that some row sees, begin a multiple of 64
+};
+
+__device__ __forceinline__ bool is_short(int rows, int group) { return rows == 1 || (int64_t)rows * group <= kShortRows; }
+
+// False: no rows, or too many.
+__device__ __forceinline__ bool short_sequence(const KvAttentionArgs& a, int group, int i, ShortSequence& q) {
+    q.s = kv_sequence(a.batch, i);
+    const int64_t room = (int64_t)a.batch.max_pages << a.cache.log_page;
+    const int64_t first = q.s.first();
+    q.end = (int)(q.s.length < room ? q.s.length : room);
+    q.begin = 0;
+    if (a.window > 0 && first >= a.window) q.begin = (int)min((first - a.window + 1) & ~(int64_t)(kShortStep - 1), (int64_t)q.end);
+    return q.s.rows > 0 && is_short(q.s.rows, group);
+}
+
+struct Share {
+    int seq, number, count, slot0;
+    int64_t chunk;  // keys, a multiple of kChunkUnit
+};
+
+__device__ __forceinline__ int chunks_of(int keys, int64_t chunk) { return keys > 0 ? (int)((keys + chunk - 1) / chunk) : 1; }
+
+__device__ __forceinline__ int64_t chunk_length(const KvAttentionArgs& a, const ShortPlan& pl, int group) {
+    if (pl.target == 0) return (int64_t)1 << 31;
+    const int lane = threadIdx.x & 63;
+    int64_t keys = 0;
+    for (int base = 0; base < a.batch.sequences; base += 64) {
+        ShortSequence q;
+        if (base + lane < a.batch.sequences && short_sequence(a, group, base + lane, q)) keys += q.end - q.begin;
+    }
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) keys += __shfl_xor(keys, m);
+    const int64_t each = (keys + pl.target - 1) / pl.target;
+    return max((each + kChunkUnit - 1) / kChunkUnit, (int64_t)1) * kChunkUnit;
+}
+
+// The share of workgroup `slot`; false: none.
+__device__ __forceinline__ bool find_share(const KvAttentionArgs& a, const ShortPlan& pl, int group, int slot, Share& out) {
+    const int lane = threadIdx.x & 63;
+    out.chunk = chunk_length(a, pl, group);
+    int before = 0;
+    for (int base = 0; base < a.batch.sequences; base += 64) {
+        ShortSequence q;
+        int mine = 0;
+        if (base + lane < a.batch.sequences && short_sequence(a, group, base + lane, q)) mine = chunks_of(q.end - q.begin, out.chunk);
+        int upto = mine;
+#pragma unroll
+        for (int m = 1; m < 64; m *= 2) {
+            const int n = __shfl_up(upto, m);
+            if (lane >= m) upto += n;
+        }
+        const uint64_t past = __ballot(slot < before + upto);
+        if (past) {
+            const int at = __builtin_ctzll(past);
+            out.seq = base + at;
+            out.count = __shfl(mine, at);
+            out.slot0 = before + __shfl(upto, at) - out.count;
+            out.number = slot - out.slot0;
+            return true;
+        }
+        before += __shfl(upto, 63);
+    }
+    return false;
+}
+
+// Workspace: per slot, head and row the sums [dim], then per slot, head and row
+// the maximum (base 2) and the sum of the probabilities.
+__device__ __forceinline__ float* part_at(const KvAttentionArgs& a, const ShortPlan& pl, int slot, int head, int row) {
+    return a.workspace + (((int64_t)slot * a.cache.kv_heads + head) * pl.rows + row) * a.cache.dim;
+}
+__device__ __forceinline__ float2* part_stat(const KvAttentionArgs& a, const ShortPlan& pl, int slot, int head, int row) {
+    float* p = a.workspace + (int64_t)pl.slots * a.cache.kv_heads * pl.rows * a.cache.dim;
+    return reinterpret_cast<float2*>(p) + ((int64_t)slot * a.cache.kv_heads + head) * pl.rows + row;
+}
+
+// What a row's sum becomes: no key (zeros), keys that have no page (NaN).
+__device__ __forceinline__ float row_result(float sum, float total, int64_t pos, int64_t room) {
+    if (pos < 0) return 0.0f;
+    return pos < room ? sum / total : __builtin_nanf("");
+}
+
+template <int D>
+__global__ __launch_bounds__(64 * kShortWaves, 2) void k_attention_short(KvAttentionArgs a, ShortPlan pl, Scoring sc) {
+    constexpr int kQ = D / 32;       // products per 16 tokens
+    constexpr int kV = D / 16;       // tiles of the result
+    constexpr int kOutRow = D + 4;
+    __shared__ __attribute__((aligned(16))) float out[kShortWaves][16 * kOutRow];
+    __shared__ float2 stat[kShortWaves][16];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int x = lane & 15, c = lane >> 4;
+    const int kvh = a.cache.kv_heads, group = a.heads / kvh;
+    const int head = (int)(blockIdx.x % (uint32_t)kvh);
+    const int tile = (int)(blockIdx.x / (uint32_t)kvh % (uint32_t)pl.tiles), slot = (int)(blockIdx.x / (uint32_t)kvh / (uint32_t)pl.tiles);
+
+    Share sh;
+    if (!find_share(a, pl, group, slot, sh)) return;
+    ShortSequence sq;
+    short_sequence(a, group, sh.seq, sq);
+    const int rows = sq.s.rows * group;
+    if (16 * tile >= rows) return;
+    const int log_page = a.cache.log_page, page = 1 << log_page;
+    const int first = (int)sq.s.first();
+
+    // the lane's query row
+    const int r = 16 * tile + x, token = min(r, rows - 1) / group, member = min(r, rows - 1) - token * group;
+    const int pos = r < rows ? first + token : -1;
+    const int pos_lo = first + 16 * tile / group, pos_hi = first + min(16 * tile + 15, rows - 1) / group;
+    f16x8 q[kQ];
+    float c0 = sc.c0;
+    int shift;
+    {
+        const uint16_t* qp = a.q + (int64_t)(sq.s.row0 + token) * a.q_stride + (int64_t)(head * group + member) * D + c * (D / 4);
+        float f[kQ][8];
+#pragma unroll
+        for (int k = 0; k < kQ; ++k) load8(qp + 8 * k, f[k]);
+        if (a.rope.table) {
+            // lanes 32 apart hold a pair's halves
+            const int d = (c & 1) * (D / 4);
+#pragma unroll
+            for (int k = 0; k < kQ; ++k) {
+                float lo[8], hi[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float other = __shfl_xor(f[k][i], 32);
+                    lo[i] = c < 2 ? f[k][i] : other;
+                    hi[i] = c < 2 ? other : f[k][i];
+                }
+                turn8(lo, hi, a.rope, D, first + token, d + 8 * k);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[k][i] = c < 2 ? lo[i] : hi[i];
+            }
+        }
+        float amax = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kQ; ++k)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[k][i]));
+        amax = fmaxf(amax, __shfl_xor(amax, 16));
+        amax = fmaxf(amax, __shfl_xor(amax, 32));
+        shift = query_shift(amax);
+#pragma unroll
+        for (int k = 0; k < kQ; ++k) q[k] = narrow(f[k], shift);
+    }
+
+    const int jlo = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
+    const int begin = (int)min((int64_t)sq.begin + sh.number * sh.chunk, (int64_t)sq.end);
+    const int end = (int)min((int64_t)sq.end, (int64_t)begin + sh.chunk);
+    const int jhi = min(pos, end - 1);
+    // keys that every row of the tile sees, and that any sees
+    const int all_lo = a.window > 0 ? max(pos_hi - a.window + 1, 0) : 0, all_hi = min(pos_lo, end - 1);
+    const int any_lo = a.window > 0 ? max(pos_lo - a.window + 1, 0) : 0, any_hi = min(pos_hi, end - 1);
+
+    const int* table = a.batch.table + (int64_t)sh.seq * a.batch.table_stride;
+    const int kgroup = 16 * (x >> 2);  // tokens that the lane's keys are of, within a step; its scores and values: 16 c
+
+    uint4 kb[4][D / 64];
+    uint4 vb[kV];
+    int kpage, vpage;  // physical, -1: none
+    float ks, vs;
+
+    auto page_of = [&](int t) {
+        const int e = t < end ? table[t >> log_page] : -1;
+        return e >= 0 && e < a.cache.pages ? e : -1;
+    };
+    auto load_k = [&](int t) {
+        const int j = t + kgroup;
+        const uint8_t* p = a.cache.kc + (((int64_t)max(kpage, 0) * kvh + head) * page + (j & (page - 1)) + (x & 3)) * D + c * (D / 4);
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) kb[g][i] = *reinterpret_cast<const uint4*>(p + 4 * g * D + 16 * i);
+    };
+    auto load_v = [&](int t) {
+        const int j = t + 16 * c;
+        const uint8_t* p = a.cache.vc + (((int64_t)max(vpage, 0) * kvh + head) * D + x) * page + (j & (page - 1));
+#pragma unroll
+        for (int i = 0; i < kV; ++i) vb[i] = *reinterpret_cast<const uint4*>(p + (int64_t)16 * i * page);
+    };
+    auto load_s = [&]() {
+        const int64_t at = (int64_t)max(vpage, 0) * kvh + head;
+        ks = vpage < 0 ? -1.0f : (float)a.cache.ks[at];
+        vs = e8m0_f32(a.cache.vs[at]);
+    };
+
+    f32x4 acc[kV];
+#pragma unroll
+    for (int i = 0; i < kV; ++i) acc[i] = (f32x4){};
+    float m = -__builtin_inff(), l = 0.0f;
+
+    int t = begin + kShortStep * wave;
+    if (t < end) {
+        kpage = page_of(t + kgroup);
+        vpage = page_of(t + 16 * c);
+        load_k(t);
+        load_s();
+        load_v(t);
+    }
+    while (t < end) {
+        const int tn = t + kChunkUnit;
+        const int kpage_n = page_of(tn + kgroup), vpage_n = page_of(tn + 16 * c);
+        // scores: s[g][i] is of token t + 16 c + 4 g + i
+        f32x4 s[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            s[g] = (f32x4){};
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+                s[g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen_f16(kb[g][i].x, kb[g][i].y), q[2 * i], s[g], 0, 0, 0);
+                s[g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen_f16(kb[g][i].z, kb[g][i].w), q[2 * i + 1], s[g], 0, 0, 0);
+            }
+        }
+        const float factor = ks < 0.0f ? __builtin_nanf("") : __builtin_ldexpf(c0, (int)ks - 127 - shift);
+        const float vscale = vs;
+        const int vpage_now = vpage;
+        kpage = kpage_n;
+        vpage = vpage_n;
+        if (tn < end) {
+            load_k(tn);
+            load_s();
+        }
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[g][i] *= factor;
+        if (sc.cap2 > 0.0f) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[g][i] = capped(s[g][i], sc.cap2);
+        }
+        const bool whole = t >= all_lo && t + kShortStep - 1 <= all_hi;
+        if (!whole) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int j = t + 16 * c + 4 * g + i;
+                    s[g][i] = j >= jlo && j <= jhi ? s[g][i] : -__builtin_inff();
+                }
+        }
+        float mt = -__builtin_inff();
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mt = fmaxf(mt, s[g][i]);
+        mt = fmaxf(mt, __shfl_xor(mt, 16));
+        mt = fmaxf(mt, __shfl_xor(mt, 32));
+        if (__any(mt > m)) {
+            const float mn = fmaxf(m, mt);
+            const float alpha = mn > m ? exp2_hw(m - mn) : 1.0f;
+            m = mn;
+            l *= alpha;
+#pragma unroll
+            for (int i = 0; i < kV; ++i) acc[i] *= alpha;
+        }
+        const float mu = m == -__builtin_inff() ? 0.0f : m;
+        // P in two BF16 parts, so that its rounding does not show in the result
+        bf16x8 ph[2], pl_[2];
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float p = exp2_hw(s[g][i] - mu);
+                l += p;
+                const __bf16 h = (__bf16)p;
+                ph[g >> 1][4 * (g & 1) + i] = h;
+                pl_[g >> 1][4 * (g & 1) + i] = (__bf16)(p - (float)h);
+            }
+        bool odd = false;
+        if (!whole) {
+            // values of tokens that no row sees are whatever the page holds
+#pragma unroll
+            for (int i = 0; i < kV; ++i) {
+                uint32_t w[4] = {vb[i].x, vb[i].y, vb[i].z, vb[i].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int j = t + 16 * c + 4 * k;
+                    w[k] &= first_bytes(any_hi + 1 - j) & ~first_bytes(any_lo - j);
+                    w[k] = vpage_now < 0 ? 0u : w[k];
+                    odd = odd || nan_bytes(w[k]) != 0;
+                }
+                vb[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+        if (!whole && __any(odd)) {
+            // A NaN value reaches exactly the rows that see its token: count
+            // such tokens per row by a product of ones.
+            bf16x8 seen[2];
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int j = t + 16 * c + 4 * g + i;
+                    seen[g >> 1][4 * (g & 1) + i] = (__bf16)(j >= jlo && j <= jhi ? 1.0f : 0.0f);
+                }
+#pragma unroll
+            for (int i = 0; i < kV; ++i) {
+                uint32_t w[4] = {vb[i].x, vb[i].y, vb[i].z, vb[i].w}, n[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t b = nan_bytes(w[k]);
+                    n[k] = b * 0x38u;  // the code of 1
+                    w[k] &= ~(b * 0xFFu);
+                }
+                vb[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                f32x4 cnt = {};
+                cnt = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_bf16(n[0], n[1], 1.0f), seen[0], cnt, 0, 0, 0);
+                cnt = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_bf16(n[2], n[3], 1.0f), seen[1], cnt, 0, 0, 0);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[i][k] = cnt[k] > 0.0f ? __builtin_nanf("") : acc[i][k];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            const bf16x8 v0 = widen_bf16(vb[i].x, vb[i].y, vscale), v1 = widen_bf16(vb[i].z, vb[i].w, vscale);
+            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, ph[0], acc[i], 0, 0, 0);
+            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, ph[1], acc[i], 0, 0, 0);
+            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, pl_[0], acc[i], 0, 0, 0);
+            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, pl_[1], acc[i], 0, 0, 0);
+        }
+        if (tn < end) load_v(tn);
+        t = tn;
+    }
+
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    if (c == 0) stat[wave][x] = make_float2(m, l);
+#pragma unroll
+    for (int i = 0; i < kV; ++i) *reinterpret_cast<f32x4*>(&out[wave][x * kOutRow + 16 * i + 4 * c]) = acc[i];
+    __syncthreads();
+    const int64_t room = (int64_t)a.batch.max_pages << log_page;
+    for (int i = tid; i < 16 * (D / 4); i += 64 * kShortWaves) {
+        const int row = i / (D / 4), d = 4 * (i % (D / 4)), rr = 16 * tile + row;
+        if (rr >= rows) continue;
+        float mx = stat[0][row].x;
+#pragma unroll
+        for (int w = 1; w < kShortWaves; ++w) mx = fmaxf(mx, stat[w][row].x);
+        float total = 0.0f;
+        f32x4 o = {};
+#pragma unroll
+        for (int w = 0; w < kShortWaves; ++w) {
+            const float f = mx == -__builtin_inff() ? 0.0f : exp2_hw(stat[w][row].x - mx);
+            total += f * stat[w][row].y;
+            o += f * *reinterpret_cast<const f32x4*>(&out[w][row * kOutRow + d]);
+        }
+        if (sh.count == 1) {
+            const int tok = rr / group, mem = rr - tok * group;
+            const int64_t p = (int64_t)first + tok;
+            uint2 v;
+            v.x = bf16_pair(row_result(o[0], total, p, room), row_result(o[1], total, p, room));
+            v.y = bf16_pair(row_result(o[2], total, p, room), row_result(o[3], total, p, room));
+            *reinterpret_cast<uint2*>(a.y + ((int64_t)(sq.s.row0 + tok) * a.heads + head * group + mem) * D + d) = v;
+        } else {
+            *reinterpret_cast<f32x4*>(part_at(a, pl, slot, head, rr) + d) = o;
+            if (d == 0) *part_stat(a, pl, slot, head, rr) = make_float2(mx, total);
+        }
+    }
+}
+
+// A workgroup joins the chunks of one row and head, in order.
+template <int D>
+__global__ __launch_bounds__(D) void k_attention_join(KvAttentionArgs a, ShortPlan pl) {
+    const int kvh = a.cache.kv_heads, group = a.heads / kvh;
+    const int head = (int)(blockIdx.x % (uint32_t)kvh);
+    const int row = (int)(blockIdx.x / (uint32_t)kvh % (uint32_t)pl.rows), seq = (int)(blockIdx.x / (uint32_t)kvh / (uint32_t)pl.rows);
+    ShortSequence sq;
+    if (!short_sequence(a, group, seq, sq) || row >= sq.s.rows * group) return;
+    const int64_t chunk = chunk_length(a, pl, group);
+    const int count = chunks_of(sq.end - sq.begin, chunk);
+    if (count == 1) return;
+    // the first slot: the chunks of the sequences before
+    const int lane = threadIdx.x & 63;
+    int slot0 = 0;
+    for (int base = 0; base < seq; base += 64) {
+        ShortSequence o;
+        if (base + lane < seq && short_sequence(a, group, base + lane, o)) slot0 += chunks_of(o.end - o.begin, chunk);
+    }
+#pragma unroll
+    for (int k = 1; k < 64; k *= 2) slot0 += __shfl_xor(slot0, k);
+    const int d = threadIdx.x;
+    float mx = -__builtin_inff();
+    for (int i = lane; i < count; i += 64) mx = fmaxf(mx, part_stat(a, pl, slot0 + i, head, row)->x);
+#pragma unroll
+    for (int k = 1; k < 64; k *= 2) mx = fmaxf(mx, __shfl_xor(mx, k));
+    float total = 0.0f, o = 0.0f;
+    for (int i = 0; i < count; ++i) {
+        const float2 st = *part_stat(a, pl, slot0 + i, head, row);
+        const float f = mx == -__builtin_inff() ? 0.0f : exp2_hw(st.x - mx);
+        total += f * st.y;
+        o += f * part_at(a, pl, slot0 + i, head, row)[d];
+    }
+    const int token = row / group, member = row - token * group;
+    const float r = row_result(o, total, sq.s.first() + token, (int64_t)a.batch.max_pages << a.cache.log_page);
+    a.y[((int64_t)(sq.s.row0 + token) * a.heads + head * group + member) * D + d] = (uint16_t)bf16_pair(r, 0.0f);
+}
+
+// ---------------------------------------------------------------------------
+// many rows per sequence
+// ---------------------------------------------------------------------------
+//
+// A workgroup owns 256 rows of one sequence and head and goes over their keys
+// in tiles of 64.  Keys and values are widened once per workgroup on their way
+// to LDS, so that the conversions cost a wavefront little beside its products,
+// and each of 8 wavefronts multiplies them with its 32 rows.  A tile's global
+// loads are in flight while the tile before is multiplied.
+
+constexpr int kLongWaves = 8, kLongRows = 32 * kLongWaves, kLongKeys = 64;
+
+struct LongPlan {
+    int slots;  // tiles of kLongRows rows of any sequence, at most
+};
+
+// LDS places, in 16-byte pieces whose order within a row is exchanged so that
+// 16 lanes that read one piece of 16 rows meet every bank once.
+template <int D>
+__device__ __forceinline__ int key_place(int token, int piece) {
+    return D == 128 ? token * 16 + (piece ^ (token & 15)) : token * 8 + (piece ^ ((token >> 1) & 7));
+}
+__device__ __forceinline__ int value_place(int d, int piece) { return d * 8 + (piece ^ ((d >> 1) & 7)); }
+
+template <int D>
+__global__ __launch_bounds__(64 * kLongWaves) void k_attention_long(KvAttentionArgs a, LongPlan pl, Scoring sc) {
+    constexpr int kQ = D / 16;  // products per 32 keys
+    constexpr int kV = D / 32;  // tiles of the result
+    __shared__ uint4 keys[2][kLongKeys * D / 8];
+    __shared__ uint4 values[2][kLongKeys * D / 8];
+    __shared__ int kscale[2][4];  // exponents of the 16-key groups, 256: no page
+    __shared__ int nan_tile[2];   // the tile, if a value of it is NaN
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n = lane & 31, hf = lane >> 5;
+    const int kvh = a.cache.kv_heads, group = a.heads / kvh;
+    const int head = (int)(blockIdx.x % (uint32_t)kvh);
+    // the last tiles of a sequence see the most keys: they go first
+    int number;
+    const int seq = kv_find(a.batch, group, 8, 1, pl.slots - 1 - (int)(blockIdx.x / (uint32_t)kvh), number);
+    const KvSequence s = kv_sequence(a.batch, seq);
+    if (number < 0 || s.rows == 0 || is_short(s.rows, group)) return;
+    const int64_t rows = (int64_t)s.rows * group, row0 = (int64_t)number * kLongRows;
+    if (row0 >= rows) return;
+    const int log_page = a.cache.log_page, page = 1 << log_page;
+    const int first = (int)s.first();
+    const int64_t room = (int64_t)a.batch.max_pages << log_page;
+    const int length = (int)min(s.length, room);
+
+    const int64_t r = row0 + 32 * wave + n;
+    const int token = (int)(min(r, rows - 1) / group), member = (int)(min(r, rows - 1) - (int64_t)token * group);
+    const int pos = first + token;
+    // positions of the wavefront's and the workgroup's first and last rows
+    const int w_lo = first + (int)(min(row0 + 32 * wave, rows - 1) / group), w_hi = first + (int)(min(row0 + 32 * wave + 31, rows - 1) / group);
+    const int g_lo = first + (int)(row0 / group), g_hi = first + (int)(min(row0 + kLongRows - 1, rows - 1) / group);
+
+    f16x8 q[kQ];
+    int shift;
+    {
+        const uint16_t* qp = a.q + (int64_t)(s.row0 + token) * a.q_stride + (int64_t)(head * group + member) * D + 8 * hf;
+        float f[kQ][8];
+#pragma unroll
+        for (int k = 0; k < kQ; ++k) load8(qp + 16 * k, f[k]);
+        if (a.rope.table) {
+#pragma unroll
+            for (int k = 0; k < kQ / 2; ++k) turn8(f[k], f[k + kQ / 2], a.rope, D, pos, 16 * k + 8 * hf);
+        }
+        float amax = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kQ; ++k)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[k][i]));
+        amax = fmaxf(amax, __shfl_xor(amax, 32));
+        shift = query_shift(amax);
+#pragma unroll
+        for (int k = 0; k < kQ; ++k) q[k] = narrow(f[k], shift);
+    }
+    const int jlo = a.window > 0 ? max(pos - a.window + 1, 0) : 0, jhi = min(pos, length - 1);
+    const int all_lo = a.window > 0 ? max(w_hi - a.window + 1, 0) : 0, all_hi = min(w_lo, length - 1);
+    const int any_lo = a.window > 0 ? max(w_lo - a.window + 1, 0) : 0, any_hi = min(w_hi, length - 1);
+    const int begin = a.window > 0 ? max(g_lo - a.window + 1, 0) & ~(kLongKeys - 1) : 0;
+    const int end = min(g_hi + 1, length);  // keys that the workgroup sees
+
+    // What the thread loads of a tile: 16 bytes of a key, 16 tokens of a row of values.
+    constexpr bool kBoth = D == 128;  // else the first half of the threads loads keys, the other values
+    const int part = kBoth ? tid : tid & 255;
+    const bool of_k = kBoth || tid < 256, of_v = kBoth || tid >= 256;
+    const int k_token = part / (D / 16), k_piece = part % (D / 16);
+    const int v_d = part >> 2, v_group = part & 3;
+    const int* table = a.batch.table + (int64_t)seq * a.batch.table_stride;
+    auto page_of = [&](int t) {
+        const int e = t < end ? table[t >> log_page] : -1;
+        return e >= 0 && e < a.cache.pages ? e : -1;
+    };
+    uint4 kl = {}, vl = {};
+    int ke = 0;
+    float vs = 1.0f;
+    int kp = -1, vp = -1;
+    auto load = [&](int t) {
+        if (of_k) {
+            const int64_t at = (int64_t)max(kp, 0) * kvh + head;
+            kl = *reinterpret_cast<const uint4*>(a.cache.kc + (at * page + ((t + k_token) & (page - 1))) * D + 16 * k_piece);
+            ke = kp < 0 ? 256 : (int)a.cache.ks[at] - 127;
+        }
+        if (of_v) {
+            const int64_t at = (int64_t)max(vp, 0) * kvh + head;
+            vl = *reinterpret_cast<const uint4*>(a.cache.vc + (at * D + v_d) * page + ((t + 16 * v_group) & (page - 1)));
+            vs = vp < 0 ? 0.0f : e8m0_f32(a.cache.vs[at]);
+        }
+    };
+    auto find_pages = [&](int t) {
+        kp = page_of(t + (k_token & ~15));
+        vp = page_of(t + 16 * v_group);
+    };
+    auto store = [&](int buf, int t) {
+        if (of_k) {
+            keys[buf][key_place<D>(k_token, 2 * k_piece)] = __builtin_bit_cast(uint4, widen_f16(kl.x, kl.y));
+            keys[buf][key_place<D>(k_token, 2 * k_piece + 1)] = __builtin_bit_cast(uint4, widen_f16(kl.z, kl.w));
+            if (k_piece == 0 && (k_token & 15) == 0) kscale[buf][k_token >> 4] = ke;
+        }
+        if (of_v) {
+            uint32_t w[4] = {vl.x, vl.y, vl.z, vl.w};
+            if (t + kLongKeys > end) {
+                // values behind the last token are whatever the page holds
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[k] &= first_bytes(end - (t + 16 * v_group + 4 * k));
+            }
+            bool odd = false;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                w[k] = vs == 0.0f ? 0u : w[k];
+                odd = odd || nan_bytes(w[k]) != 0;
+            }
+            if (odd) nan_tile[buf] = t;
+            // a lane of the second product wants tokens 4 h .. and 8 + 4 h .. of 16
+            values[buf][value_place(v_d, 2 * v_group)] = __builtin_bit_cast(uint4, widen_bf16(w[0], w[2], vs));
+            values[buf][value_place(v_d, 2 * v_group + 1)] = __builtin_bit_cast(uint4, widen_bf16(w[1], w[3], vs));
+        }
+    };
+
+    f32x16 acc[kV];
+#pragma unroll
+    for (int i = 0; i < kV; ++i) acc[i] = (f32x16){};
+    float m = -__builtin_inff(), l = 0.0f;
+
+    auto multiply = [&](int buf, int t) {
+        f32x16 sc_[2];
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+            sc_[st] = (f32x16){};
+#pragma unroll
+            for (int k = 0; k < kQ; ++k) {
+                const f16x8 kf = __builtin_bit_cast(f16x8, keys[buf][key_place<D>(32 * st + n, 2 * k + hf)]);
+                sc_[st] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, q[k], sc_[st], 0, 0, 0);
+            }
+        }
+        // register i of score tile st is of token t + 32 st + 8 (i / 4) + 4 hf + i % 4
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int e = kscale[buf][u];
+            const float factor = e == 256 ? __builtin_nanf("") : __builtin_ldexpf(sc.c0, e - shift);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sc_[u >> 1][8 * (u & 1) + i] *= factor;
+        }
+        if (sc.cap2 > 0.0f) {
+#pragma unroll
+            for (int st = 0; st < 2; ++st)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sc_[st][i] = capped(sc_[st][i], sc.cap2);
+        }
+        const bool whole = t >= all_lo && t + kLongKeys - 1 <= all_hi;
+        if (!whole) {
+#pragma unroll
+            for (int st = 0; st < 2; ++st)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int j = t + 32 * st + 8 * (i >> 2) + 4 * hf + (i & 3);
+                    sc_[st][i] = j >= jlo && j <= jhi ? sc_[st][i] : -__builtin_inff();
+                }
+        }
+        float mt = -__builtin_inff();
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) mt = fmaxf(mt, sc_[st][i]);
+        mt = fmaxf(mt, __shfl_xor(mt, 32));
+        if (__any(mt > m)) {
+            const float mn = fmaxf(m, mt);
+            const float alpha = mn > m ? exp2_hw(m - mn) : 1.0f;
+            m = mn;
+            l *= alpha;
+#pragma unroll
+            for (int i = 0; i < kV; ++i) acc[i] *= alpha;
+        }
+        const float mu = m == -__builtin_inff() ? 0.0f : m;
+        bf16x8 p[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float e = exp2_hw(sc_[u >> 1][8 * (u & 1) + i] - mu);
+                l += e;
+                p[u][i] = (__bf16)e;
+            }
+        if (!whole && nan_tile[buf] == t) {
+            // A NaN value reaches exactly the rows that see its token: count
+            // such tokens per row by a product of ones.
+            bf16x8 seen[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int j = t + 16 * u + 8 * (i >> 2) + 4 * hf + (i & 3);
+                    seen[u][i] = (__bf16)(j >= jlo && j <= jhi ? 1.0f : 0.0f);
+                }
+#pragma unroll
+            for (int i = 0; i < kV; ++i) {
+                f32x16 cnt = {};
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    bf16x8 vf = __builtin_bit_cast(bf16x8, values[buf][value_place(32 * i + n, 2 * u + hf)]), ones;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const bool bad = vf[k] != vf[k];
+                        ones[k] = (__bf16)(bad ? 1.0f : 0.0f);
+                        vf[k] = bad ? (__bf16)0.0f : vf[k];
+                    }
+                    cnt = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ones, seen[u], cnt, 0, 0, 0);
+                    acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, p[u], acc[i], 0, 0, 0);
+                }
+#pragma unroll
+                for (int k = 0; k < 16; ++k) acc[i][k] = cnt[k] > 0.0f ? __builtin_nanf("") : acc[i][k];
+            }
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < kV; ++i)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const bf16x8 vf = __builtin_bit_cast(bf16x8, values[buf][value_place(32 * i + n, 2 * u + hf)]);
+                acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, p[u], acc[i], 0, 0, 0);
+            }
+    };
+
+    if (tid < 2) nan_tile[tid] = -1;
+    __syncthreads();
+    if (begin < end) {
+        find_pages(begin);
+        load(begin);
+        find_pages(begin + kLongKeys);
+        store(0, begin);
+    }
+    __syncthreads();
+    int buf = 0;
+    for (int t = begin; t < end; t += kLongKeys, buf ^= 1) {
+        const bool more = t + kLongKeys < end;
+        if (more) {
+            load(t + kLongKeys);
+            find_pages(t + 2 * kLongKeys);
+        }
+        if (t <= any_hi && t + kLongKeys > any_lo) multiply(buf, t);
+        if (more) store(buf ^ 1, t + kLongKeys);
+        __syncthreads();
+    }
+
+    l += __shfl_xor(l, 32);
+    if (r < rows) {
+        uint16_t* y = a.y + ((int64_t)(s.row0 + token) * a.heads + head * group + member) * D;
+#pragma unroll
+        for (int i = 0; i < kV; ++i)
+#pragma unroll
+            for (int k = 0; k < 16; k += 4) {
+                uint2 v;
+                v.x = bf16_pair(row_result(acc[i][k], l, pos, room), row_result(acc[i][k + 1], l, pos, room));
+                v.y = bf16_pair(row_result(acc[i][k + 2], l, pos, room), row_result(acc[i][k + 3], l, pos, room));
+                *reinterpret_cast<uint2*>(y + 32 * i + 2 * k + 4 * hf) = v;
+            }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------
+
+constexpr int kFill = 1024;  // workgroups to aim at: four per compute unit
+
+// Workspace bytes per slot.
+int64_t slot_bytes(const KvCacheArgs& c, int rows) { return (int64_t)c.kv_heads * rows * (c.dim + 2) * 4; }
+
+ShortPlan short_plan(const KvCacheArgs& c, const KvBatchArgs& b, int heads, int64_t workspace_bytes) {
+    ShortPlan pl;
+    const int group = heads / c.kv_heads;
+    pl.rows = b.cu ? (group > kShortRows ? group : kShortRows) : group;
+    if (b.cu && (int64_t)b.tokens * group < pl.rows) pl.rows = b.tokens * group;
+    pl.tiles = (pl.rows + 15) / 16;
+    // no sequence is longer than a chunk of the least length: nothing to split
+    const bool splits = ((int64_t)b.max_pages << c.log_page) > kChunkUnit;
+    const int64_t fit = workspace_bytes / slot_bytes(c, pl.rows) - b.sequences, want = (kFill + c.kv_heads - 1) / c.kv_heads;
+    pl.target = splits ? (fit < want ? fit : want) : 0;
+    if (pl.target < 1) pl.target = 0;
+    pl.slots = (int)(pl.target + b.sequences);
+    return pl;
+}
+
+template <int D>
+hipError_t launch_attention(const KvAttentionArgs& a, hipStream_t stream) {
+    const KvCacheArgs& c = a.cache;
+    const KvBatchArgs& b = a.batch;
+    const int group = a.heads / c.kv_heads;
+    const Scoring sc = scoring(a);
+    if (b.cu && (int64_t)b.tokens * group > kShortRows) {
+        LongPlan pl;
+        pl.slots = (int)kv_items(b, group, 8, 1);
+        const hipError_t e = launch(k_attention_long<D>, dim3((uint32_t)(pl.slots * c.kv_heads)), dim3(64 * kLongWaves), stream, a, pl, sc);
+        if (e != hipSuccess) return e;
+    }
+    const ShortPlan pl = short_plan(c, b, a.heads, a.workspace_bytes);
+    hipError_t e = launch(k_attention_short<D>, dim3((uint32_t)((int64_t)pl.slots * pl.tiles * c.kv_heads)), dim3(64 * kShortWaves), stream, a, pl, sc);
+    if (e != hipSuccess || pl.target == 0) return e;
+    return launch(k_attention_join<D>, dim3((uint32_t)((int64_t)b.sequences * pl.rows * c.kv_heads)), dim3(D), stream, a, pl);
+}
+
+}  // namespace
+
+int64_t kv_attention_workspace_bytes(const KvCacheArgs& c, const KvBatchArgs& b, int heads) {
+    const ShortPlan pl = short_plan(c, b, heads, (int64_t)1 << 60);
+    return pl.target == 0 ? 0 : pl.slots * slot_bytes(c, pl.rows);
+}
+
+bool kv_attention_fits(const KvAttentionArgs& a) {
+    const KvCacheArgs& c = a.cache;
+    const KvBatchArgs& b = a.batch;
+    const int64_t most = 0xFFFFFFFFll;
+    const ShortPlan pl = short_plan(c, b, a.heads, a.workspace_bytes);
+    const int64_t tiles = b.cu ? kv_items(b, a.heads / c.kv_heads, 8, 1) : 0;
+    return tiles * c.kv_heads <= most / (64 * kLongWaves) &&
+           (int64_t)pl.slots * pl.tiles * c.kv_heads <= most / (64 * kShortWaves) &&
+           (int64_t)b.sequences * pl.rows * c.kv_heads <= most / c.dim;
+}
+
+hipError_t launch_kv_attention(const KvAttentionArgs& a, hipStream_t stream) {
+    return a.cache.dim == 128 ? launch_attention<128>(a, stream) : launch_attention<64>(a, stream);
+}
+
+}  // namespace focus

@@ -500,6 +500,118 @@ int focus_w4a16_linear(const uint16_t* x_bf16, int64_t M, int w_format, const ui
                        const uint8_t* w_scales, const float* w_s2, int64_t N, int64_t K, void* y, int y_dtype,
                        void* stream);
 
+/*
+ * The paged cache of keys and values in 8 bits, and the attention over it:
+ * what stands between a decoder layer's q, k, v product and its o product.
+ *
+ * The cache.  A page holds page_tokens consecutive tokens of one sequence.
+ * Per page and key/value head it has the keys' E4M3 codes [page_tokens,
+ * head_dim], the values' E4M3 codes [head_dim, page_tokens] and one E8M0 scale
+ * byte (exponent + 127) for each of the two:
+ *     S = 2^e, e the least integer with max|x| <= 448 * 2^e, -127 <= e <= 119
+ *     code = E4M3(clamp(x / S, -448, 448))  (nearest, ties to even)
+ * over the page's tokens.  A page that gains tokens keeps the larger of its
+ * exponent and the new tokens' and moves its older codes to it,
+ * E4M3(code * 2^(e_old - e)); a page whose first token is written takes
+ * nothing from before.  Infinities and NaN are left out of the maximum and
+ * stored as E4M3's NaN: they show wherever their token is seen, and nowhere
+ * else.
+ *
+ * The batch.  Sequence b has the rows cu_tokens[b] .. cu_tokens[b+1]-1 of a
+ * step's tensors (cu_tokens NULL: row b alone); they are its last ones, the
+ * last at position lengths[b]-1.  Its token j lies in page
+ * page_table[b, j / page_tokens].  The same batch serves the write of a
+ * step's keys and values, the attention of its queries after it, and a read.
+ * The arrays are device memory and never read on the host.  Values in them
+ * that make no sense lead to no access outside the tensors: rows at negative
+ * positions (lengths[b] below the number of rows) are not written, and read
+ * or attend as zeros; tokens past the table's row, or whose entry is no page
+ * of the cache, are not written, and read as NaN or make the rows that see
+ * them NaN; positions past the rotation's table turn to NaN.  Pages that a
+ * write changes must belong to one sequence each (pages that several
+ * sequences share may be read by all of them).  Rows of no sequence stay as
+ * they are.
+ */
+typedef struct focus_kv_cache {
+    uint8_t* k_codes;   /* [pages, kv_heads, page_tokens, head_dim], 16-byte aligned */
+    uint8_t* k_scales;  /* [pages, kv_heads] */
+    uint8_t* v_codes;   /* [pages, kv_heads, head_dim, page_tokens], 16-byte aligned */
+    uint8_t* v_scales;  /* [pages, kv_heads] */
+    int64_t pages;      /* below 2^31 */
+    int64_t kv_heads;   /* 1 .. 1024 */
+    int64_t head_dim;   /* 64 or 128 */
+    int64_t page_tokens;  /* 16, 32, 64 or 128 */
+} focus_kv_cache;
+
+typedef struct focus_kv_batch {
+    const int32_t* page_table;  /* [sequences] rows of max_pages entries */
+    int64_t table_stride;       /* entries from row to row, at least max_pages */
+    int64_t max_pages;          /* max_pages * page_tokens <= 2^30 */
+    const int32_t* lengths;     /* [sequences] tokens, the step's rows included */
+    const int32_t* cu_tokens;   /* [sequences + 1], or NULL: tokens == sequences */
+    int64_t sequences;          /* at most 2^20 */
+    int64_t tokens;             /* rows of the step's tensors, below 2^31 */
+} focus_kv_batch;
+
+/* The rotation's table for the calls below: table [positions, head_dim] FP32
+ * (16-byte aligned), row p the cosines and then the sines of p * inv_freq[i],
+ * i < head_dim / 2, formed in binary64 and rounded once.  inv_freq
+ * [head_dim / 2] FP64, 8-byte aligned.  head_dim even; positions * head_dim
+ * <= 2^38. */
+int focus_rope_table(const double* inv_freq, int64_t positions, int64_t head_dim, float* table, void* stream);
+
+/*
+ * Write a step's keys and values into the cache.
+ *   k, v      [tokens, kv_heads * head_dim] BF16, 16-byte aligned, rows k_stride
+ *             and v_stride elements apart (at least a row, a multiple of 8), so
+ *             that they may be parts of one product's rows
+ *   rope      NULL, or the table of focus_rope_table [rope_positions, head_dim]:
+ *             keys are turned by their position's angles first, each operation
+ *             one binary32 operation (k[i]*c - k[i+h]*s, k[i+h]*c + k[i]*s,
+ *             h = head_dim / 2), and stored from binary32
+ * One launch; (tokens / page_tokens + 2 * sequences) * kv_heads below 2^24
+ * (FOCUS_ERR_RANGE otherwise).
+ */
+int focus_kv_cache_write(const focus_kv_cache* cache, const focus_kv_batch* batch, const uint16_t* k, int64_t k_stride,
+                         const uint16_t* v, int64_t v_stride, const float* rope, int64_t rope_positions, void* stream);
+
+/* Read the batch's rows back: k, v [tokens, kv_heads * head_dim] BF16 (16-byte
+ * aligned), BF16(code * S).  One launch, with the limit of the write. */
+int focus_kv_cache_read(const focus_kv_cache* cache, const focus_kv_batch* batch, uint16_t* k, uint16_t* v,
+                        void* stream);
+
+/*
+ * Attention of the batch's rows over the cache, causal:
+ *     s_ij = scale * sum_d q_id k_jd        (softcap > 0: softcap * tanh(s_ij / softcap))
+ *     y_i  = sum_j exp(s_ij - m_i) v_j / sum_j exp(s_ij - m_i)
+ * over the tokens j of row i's sequence with j <= pos_i and, where window > 0,
+ * j > pos_i - window; a row that sees no token gives zeros.  Query heads
+ * g * kv_head .. (g = heads / kv_heads) share a head of the cache.
+ *   q         [tokens, heads * head_dim] BF16, 16-byte aligned, rows q_stride
+ *             elements apart (at least a row, a multiple of 8)
+ *   heads     a multiple of kv_heads, at most 65536
+ *   rope      as for focus_kv_cache_write: queries are turned by it
+ *   scale     finite;  softcap finite, 0: none;  window < 2^31, 0: none
+ *   y         [tokens, heads * head_dim] BF16, 16-byte aligned
+ *   workspace NULL, or workspace_bytes of device memory, 16-byte aligned, that
+ *             no other call uses until this one is done: sequences with few
+ *             rows are split over their keys as far as it goes.  Nothing in it
+ *             has to be set.
+ * Arithmetic: queries keep 8 bits or, turned, 11; keys and values are exact;
+ * products and sums are binary32 (order fixed by sizes and lengths, so that
+ * equal calls give equal results); probabilities meet the values in BF16 (in
+ * two parts where a sequence has few rows); the result is rounded once.
+ * At most three launches.  FOCUS_ERR_RANGE where they would need more than
+ * 2^32 threads.
+ */
+int focus_kv_attention(const focus_kv_cache* cache, const focus_kv_batch* batch, const uint16_t* q, int64_t q_stride,
+                       int64_t heads, const float* rope, int64_t rope_positions, float scale, float softcap,
+                       int64_t window, uint16_t* y, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Workspace for the full split of focus_kv_attention (0: none helps, or an
+ * argument is out of range).  It depends on the host's values alone. */
+int64_t focus_kv_attention_workspace_bytes(const focus_kv_cache* cache, const focus_kv_batch* batch, int64_t heads);
+
 #ifdef __cplusplus
 }
 #endif
