@@ -24,6 +24,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "focus_kv.h"
 #include "focus_launch.h"
 #include "focus_numerics.h"
@@ -65,6 +67,22 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t c) {
     return ((m + 0x01010101u) >> 7) & 0x01010101u;
 }
 
+__device__ __forceinline__ bool any_nan(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    const uint32_t m = 0x7F7F7F7Fu, o = 0x01010101u;
+    return ((((a & m) + o) | ((b & m) + o) | ((c & m) + o) | ((d & m) + o)) & 0x80808080u) != 0;
+}
+
+// The larger of a lane's value and that of the lane 32 from it.
+__device__ __forceinline__ float max_halves(float x) {
+    const u32x2 r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// acc + the two BF16 values of a pair.
+__device__ __forceinline__ float sum_pair(uint32_t pair, float acc) {
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pair), __builtin_bit_cast(bf16x2, 0x3F803F80u), acc, false);
+}
+
 // The first n (0..4, or beyond) bytes of a dword.
 __device__ __forceinline__ uint32_t first_bytes(int n) { return n >= 4 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << (8 * n)) - 1u; }
 
@@ -100,18 +118,31 @@ __device__ __forceinline__ int query_shift(float amax) {
 
 // The products with exponents up to 2^15 and 2^8 over 128 elements stay far
 // within binary32.
-__device__ __forceinline__ f16x8 narrow(const float (&f)[8], int shift) {
+__device__ __forceinline__ f16x8 narrow(const float (&f)[8], int shift, float sign) {
     f16x8 r;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = (_Float16)__builtin_ldexpf(f[i], shift);
+    for (int i = 0; i < 8; ++i) r[i] = (_Float16)(sign * __builtin_ldexpf(f[i], shift));
     return r;
 }
 
 // What the scores' factor and cap need of the call.
 struct Scoring {
-    float c0;    // to base 2, or to the cap's argument
+    float c0;    // to base 2, or to the cap's argument; not negative
+    float sign;  // of the scale, given to the queries
     float cap2;  // cap * log2(e), 0 without a cap
 };
+
+// Score times this is to base 2: c0 * 2^(e - shift), e the exponent of the
+// key's page.  Kept normal and finite, so that a score of minus
+// infinity, a hidden one's, stays it and 0 stays 0.
+__device__ __forceinline__ float score_factor(float c0, int e, int shift) {
+    return __builtin_amdgcn_fmed3f(__builtin_ldexpf(c0, e - shift), 1.1754944e-38f, 3.4028235e38f);
+}
+
+// A maximum is replaced only by one that is 2^kSlack above it (base 2):
+// probabilities then reach 2^kSlack, which costs neither sum a bit, and a
+// result is rescaled a few times instead of at every new maximum.
+constexpr float kSlack = 8.0f;
 
 __device__ __forceinline__ float capped(float s, float cap2) {
     // tanh(s) = 1 - 2 / (exp(2 s) + 1)
@@ -120,8 +151,9 @@ __device__ __forceinline__ float capped(float s, float cap2) {
 }
 
 inline Scoring scoring(const KvAttentionArgs& a) {
-    if (a.softcap > 0.0f) return {a.scale / a.softcap, a.softcap * kLog2e};
-    return {a.scale * kLog2e, 0.0f};
+    const float mag = a.scale < 0.0f ? -a.scale : a.scale, sign = a.scale < 0.0f ? -1.0f : a.scale > 0.0f ? 1.0f : 0.0f;
+    if (a.softcap > 0.0f) return {mag / a.softcap, sign, a.softcap * kLog2e};
+    return {mag * kLog2e, sign, 0.0f};
 }
 
 // ---------------------------------------------------------------------------
@@ -141,6 +173,7 @@ struct ShortPlan {
     int rows;        // rows of a sequence, at most
 };
 
+constexpr int kNoPage = 1 << 16;  // in the place of a page's exponent
 constexpr int kShortWaves = 4, kShortStep = 64, kChunkUnit = kShortWaves * kShortStep;
 
 struct ShortSequence {
@@ -255,7 +288,6 @@ __global__ __launch_bounds__(64 * kShortWaves, 2) void k_attention_short(KvAtten
     const int pos = r < rows ? first + token : -1;
     const int pos_lo = first + 16 * tile / group, pos_hi = first + min(16 * tile + 15, rows - 1) / group;
     f16x8 q[kQ];
-    float c0 = sc.c0;
     int shift;
     {
         const uint16_t* qp = a.q + (int64_t)(sq.s.row0 + token) * a.q_stride + (int64_t)(head * group + member) * D + c * (D / 4);
@@ -288,7 +320,7 @@ __global__ __launch_bounds__(64 * kShortWaves, 2) void k_attention_short(KvAtten
         amax = fmaxf(amax, __shfl_xor(amax, 32));
         shift = query_shift(amax);
 #pragma unroll
-        for (int k = 0; k < kQ; ++k) q[k] = narrow(f[k], shift);
+        for (int k = 0; k < kQ; ++k) q[k] = narrow(f[k], shift, sc.sign);
     }
 
     const int jlo = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
@@ -305,7 +337,8 @@ __global__ __launch_bounds__(64 * kShortWaves, 2) void k_attention_short(KvAtten
     uint4 kb[4][D / 64];
     uint4 vb[kV];
     int kpage, vpage;  // physical, -1: none
-    float ks, vs;
+    int ks;
+    float vs;
 
     auto page_of = [&](int t) {
         const int e = t < end ? table[t >> log_page] : -1;
@@ -327,7 +360,7 @@ __global__ __launch_bounds__(64 * kShortWaves, 2) void k_attention_short(KvAtten
     };
     auto load_s = [&]() {
         const int64_t at = (int64_t)max(vpage, 0) * kvh + head;
-        ks = vpage < 0 ? -1.0f : (float)a.cache.ks[at];
+        ks = vpage < 0 ? kNoPage : (int)a.cache.ks[at] - 127;
         vs = e8m0_f32(a.cache.vs[at]);
     };
 
@@ -358,7 +391,7 @@ __global__ __launch_bounds__(64 * kShortWaves, 2) void k_attention_short(KvAtten
                 s[g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen_f16(kb[g][i].z, kb[g][i].w), q[2 * i + 1], s[g], 0, 0, 0);
             }
         }
-        const float factor = ks < 0.0f ? __builtin_nanf("") : __builtin_ldexpf(c0, (int)ks - 127 - shift);
+        const float factor = ks == kNoPage ? __builtin_nanf("") : score_factor(sc.c0, ks, shift);
         const float vscale = vs;
         const int vpage_now = vpage;
         kpage = kpage_n;
@@ -553,6 +586,9 @@ __global__ __launch_bounds__(D) void k_attention_join(KvAttentionArgs a, ShortPl
 // and each of 8 wavefronts multiplies them with its 32 rows.  A tile's global
 // loads are in flight while the tile before is multiplied.
 
+// masks of the scheduler's groups
+constexpr int kProducts = 0x008, kReads = 0x100;
+
 constexpr int kLongWaves = 8, kLongRows = 32 * kLongWaves, kLongKeys = 64;
 
 struct LongPlan {
@@ -567,14 +603,13 @@ __device__ __forceinline__ int key_place(int token, int piece) {
 }
 __device__ __forceinline__ int value_place(int d, int piece) { return d * 8 + (piece ^ ((d >> 1) & 7)); }
 
-template <int D>
+template <int D, bool CAP>
 __global__ __launch_bounds__(64 * kLongWaves) void k_attention_long(KvAttentionArgs a, LongPlan pl, Scoring sc) {
     constexpr int kQ = D / 16;  // products per 32 keys
     constexpr int kV = D / 32;  // tiles of the result
     __shared__ uint4 keys[2][kLongKeys * D / 8];
     __shared__ uint4 values[2][kLongKeys * D / 8];
-    __shared__ int kscale[2][4];  // exponents of the 16-key groups, 256: no page
-    __shared__ int nan_tile[2];   // the tile, if a value of it is NaN
+    __shared__ int nan_seen;      // whether a value is NaN
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 31, hf = lane >> 5;
@@ -585,19 +620,19 @@ __global__ __launch_bounds__(64 * kLongWaves) void k_attention_long(KvAttentionA
     const int seq = kv_find(a.batch, group, 8, 1, pl.slots - 1 - (int)(blockIdx.x / (uint32_t)kvh), number);
     const KvSequence s = kv_sequence(a.batch, seq);
     if (number < 0 || s.rows == 0 || is_short(s.rows, group)) return;
-    const int64_t rows = (int64_t)s.rows * group, row0 = (int64_t)number * kLongRows;
-    if (row0 >= rows) return;
+    const int rows = s.rows * group, row0 = number * kLongRows;
+    if (number >= (rows + kLongRows - 1) / kLongRows) return;
     const int log_page = a.cache.log_page, page = 1 << log_page;
     const int first = (int)s.first();
     const int64_t room = (int64_t)a.batch.max_pages << log_page;
     const int length = (int)min(s.length, room);
 
-    const int64_t r = row0 + 32 * wave + n;
-    const int token = (int)(min(r, rows - 1) / group), member = (int)(min(r, rows - 1) - (int64_t)token * group);
+    const int r = row0 + 32 * wave + n;
+    const int token = min(r, rows - 1) / group, member = min(r, rows - 1) - token * group;
     const int pos = first + token;
     // positions of the wavefront's and the workgroup's first and last rows
-    const int w_lo = first + (int)(min(row0 + 32 * wave, rows - 1) / group), w_hi = first + (int)(min(row0 + 32 * wave + 31, rows - 1) / group);
-    const int g_lo = first + (int)(row0 / group), g_hi = first + (int)(min(row0 + kLongRows - 1, rows - 1) / group);
+    const int w_lo = first + min(row0 + 32 * wave, rows - 1) / group, w_hi = first + min(row0 + 32 * wave + 31, rows - 1) / group;
+    const int g_lo = first + row0 / group, g_hi = first + min(row0 + kLongRows - 1, rows - 1) / group;
 
     f16x8 q[kQ];
     int shift;
@@ -618,196 +653,308 @@ __global__ __launch_bounds__(64 * kLongWaves) void k_attention_long(KvAttentionA
         amax = fmaxf(amax, __shfl_xor(amax, 32));
         shift = query_shift(amax);
 #pragma unroll
-        for (int k = 0; k < kQ; ++k) q[k] = narrow(f[k], shift);
+        for (int k = 0; k < kQ; ++k) q[k] = narrow(f[k], shift, sc.sign);
     }
     const int jlo = a.window > 0 ? max(pos - a.window + 1, 0) : 0, jhi = min(pos, length - 1);
     const int all_lo = a.window > 0 ? max(w_hi - a.window + 1, 0) : 0, all_hi = min(w_lo, length - 1);
-    const int any_lo = a.window > 0 ? max(w_lo - a.window + 1, 0) : 0, any_hi = min(w_hi, length - 1);
     const int begin = a.window > 0 ? max(g_lo - a.window + 1, 0) & ~(kLongKeys - 1) : 0;
     const int end = min(g_hi + 1, length);  // keys that the workgroup sees
 
-    // What the thread loads of a tile: 16 bytes of a key, 16 tokens of a row of values.
-    constexpr bool kBoth = D == 128;  // else the first half of the threads loads keys, the other values
+    // What a wavefront loads of a tile: 16 bytes of a key per lane, all of one
+    // 16-key group, and 16 tokens of a row of values per lane, of one group too
+    // (dim 64: the first half of the wavefronts the keys, the other the values).
+    // Page and address are then scalars, beside a lane's constant offset.
+    constexpr bool kBoth = D == 128;
+    const bool of_k = kBoth || wave < 4, of_v = kBoth || wave >= 4;
     const int part = kBoth ? tid : tid & 255;
-    const bool of_k = kBoth || tid < 256, of_v = kBoth || tid >= 256;
     const int k_token = part / (D / 16), k_piece = part % (D / 16);
-    const int v_d = part >> 2, v_group = part & 3;
+    const int k_group = kBoth ? wave >> 1 : wave & 3, v_group = wave & 3;
+    const int v_d = kBoth ? 64 * (wave >> 2) + lane : lane;
+    const uint32_t k_lane = (uint32_t)((k_token & (page - 1)) * D + 16 * k_piece), v_lane = (uint32_t)(v_d * page);
+    const uint8_t* kc = a.cache.kc + (int64_t)head * page * D;
+    const uint8_t* vc = a.cache.vc + (int64_t)head * page * D;
+    const int64_t page_bytes = (int64_t)kvh * page * D;
     const int* table = a.batch.table + (int64_t)seq * a.batch.table_stride;
-    auto page_of = [&](int t) {
-        const int e = t < end ? table[t >> log_page] : -1;
-        return e >= 0 && e < a.cache.pages ? e : -1;
+
+    // The table is read 1024 keys at a time, lane i the entry of the 16-key
+    // group i (behind the last key that of the last one, whose page the masks
+    // hide), and the groups' scales with it, well before they are used: a tile
+    // then takes its pages and exponents from a lane, as scalars.
+    struct Block {
+        int page;  // -1: none
+        int ke, ve;  // scale bytes
     };
+    auto entries = [&](int t) __attribute__((always_inline)) { return table[min(t + 16 * lane, end - 1) >> log_page]; };
+    auto block = [&](int e) __attribute__((always_inline)) {
+        Block r;
+        r.page = e >= 0 && e < a.cache.pages ? e : -1;
+        const int64_t at = (int64_t)max(r.page, 0) * kvh + head;
+        r.ke = a.cache.ks[at];
+        r.ve = a.cache.vs[at];
+        return r;
+    };
+    auto lane_of = [&](int v, int i) __attribute__((always_inline)) { return __builtin_amdgcn_readlane(v, i); };
+
     uint4 kl = {}, vl = {};
-    int ke = 0;
-    float vs = 1.0f;
-    int kp = -1, vp = -1;
-    auto load = [&](int t) {
-        if (of_k) {
-            const int64_t at = (int64_t)max(kp, 0) * kvh + head;
-            kl = *reinterpret_cast<const uint4*>(a.cache.kc + (at * page + ((t + k_token) & (page - 1))) * D + 16 * k_piece);
-            ke = kp < 0 ? 256 : (int)a.cache.ks[at] - 127;
-        }
-        if (of_v) {
-            const int64_t at = (int64_t)max(vp, 0) * kvh + head;
-            vl = *reinterpret_cast<const uint4*>(a.cache.vc + (at * D + v_d) * page + ((t + 16 * v_group) & (page - 1)));
-            vs = vp < 0 ? 0.0f : e8m0_f32(a.cache.vs[at]);
-        }
+    int kp = 0, vp = 0;  // pages of kl and vl, -1: none
+    uint32_t vs = 0;
+    auto load_k = [&](int t, int physical) __attribute__((always_inline)) {
+        if (!of_k) return;
+        kp = physical;
+        // a page of 128 tokens has two tiles
+        kl = *reinterpret_cast<const uint4*>(kc + max(physical, 0) * page_bytes + (t & (page - 1) & 64) * D + k_lane);
     };
-    auto find_pages = [&](int t) {
-        kp = page_of(t + (k_token & ~15));
-        vp = page_of(t + 16 * v_group);
+    auto load_v = [&](int t, int physical, uint32_t scale) __attribute__((always_inline)) {
+        if (!of_v) return;
+        vp = physical;
+        vs = scale;
+        vl = *reinterpret_cast<const uint4*>(vc + max(physical, 0) * page_bytes + ((t + 16 * v_group) & (page - 1)) + v_lane);
     };
-    auto store = [&](int buf, int t) {
-        if (of_k) {
-            keys[buf][key_place<D>(k_token, 2 * k_piece)] = __builtin_bit_cast(uint4, widen_f16(kl.x, kl.y));
-            keys[buf][key_place<D>(k_token, 2 * k_piece + 1)] = __builtin_bit_cast(uint4, widen_f16(kl.z, kl.w));
-            if (k_piece == 0 && (k_token & 15) == 0) kscale[buf][k_token >> 4] = ke;
-        }
-        if (of_v) {
-            uint32_t w[4] = {vl.x, vl.y, vl.z, vl.w};
-            if (t + kLongKeys > end) {
-                // values behind the last token are whatever the page holds
+    const int k_place0 = key_place<D>(k_token, 2 * k_piece), k_place1 = key_place<D>(k_token, 2 * k_piece + 1);
+    const int v_place0 = value_place(v_d, 2 * v_group), v_place1 = value_place(v_d, 2 * v_group + 1);
+    auto store_k = [&](int buf) __attribute__((always_inline)) {
+        if (!of_k) return;
+        uint4 lo = __builtin_bit_cast(uint4, widen_f16(kl.x, kl.y)), hi = __builtin_bit_cast(uint4, widen_f16(kl.z, kl.w));
+        // a key without a page: NaN
+        if (kp < 0) lo = hi = make_uint4(0x7E007E00, 0x7E007E00, 0x7E007E00, 0x7E007E00);
+        keys[buf][k_place0] = lo;
+        keys[buf][k_place1] = hi;
+    };
+    auto store_v = [&](int buf, int t) __attribute__((always_inline)) {
+        if (!of_v) return;
+        uint32_t w[4] = {vl.x, vl.y, vl.z, vl.w};
+        if (vp < 0 || t + kLongKeys > end) {
+            // values without a page or behind the last token are whatever lies there
 #pragma unroll
-                for (int k = 0; k < 4; ++k) w[k] &= first_bytes(end - (t + 16 * v_group + 4 * k));
-            }
-            bool odd = false;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                w[k] = vs == 0.0f ? 0u : w[k];
-                odd = odd || nan_bytes(w[k]) != 0;
-            }
-            if (odd) nan_tile[buf] = t;
-            // a lane of the second product wants tokens 4 h .. and 8 + 4 h .. of 16
-            values[buf][value_place(v_d, 2 * v_group)] = __builtin_bit_cast(uint4, widen_bf16(w[0], w[2], vs));
-            values[buf][value_place(v_d, 2 * v_group + 1)] = __builtin_bit_cast(uint4, widen_bf16(w[1], w[3], vs));
+            for (int k = 0; k < 4; ++k) w[k] &= vp >= 0 ? first_bytes(end - (t + 16 * v_group + 4 * k)) : 0u;
         }
+        if (any_nan(w[0], w[1], w[2], w[3])) {
+            // see below
+            nan_seen = 1;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] &= ~(nan_bytes(w[k]) * 0xFFu);
+        }
+        const float S = e8m0_f32(vs);
+        // a lane of the second product wants tokens 4 h .. and 8 + 4 h .. of 16
+        values[buf][v_place0] = __builtin_bit_cast(uint4, widen_bf16(w[0], w[2], S));
+        values[buf][v_place1] = __builtin_bit_cast(uint4, widen_bf16(w[1], w[3], S));
     };
 
-    f32x16 acc[kV];
+    f32x16 acc[kV], score[2];
+    float f[4];  // the scores' factors
+    uint4 p[4];
 #pragma unroll
     for (int i = 0; i < kV; ++i) acc[i] = (f32x16){};
-    float m = -__builtin_inff(), l = 0.0f;
+    float m = -__builtin_inff(), l = 0.0f, l2 = 0.0f;
 
-    auto multiply = [&](int buf, int t) {
-        f32x16 sc_[2];
+    // Fragments from LDS, in eight groups: the values' 16-key groups 0..3, then
+    // a quarter of the keys' products each.  Two groups are read ahead of the
+    // one that is multiplied.
+    constexpr int kRing = 3;
+    static_assert(kQ == 2 * kV, "a group holds kV fragments of either kind");
+    uint4 frag[kRing][kV];
+    auto read = [&](auto index, int buf) __attribute__((always_inline)) {
+        constexpr int g = decltype(index)::value;
 #pragma unroll
-        for (int st = 0; st < 2; ++st) {
-            sc_[st] = (f32x16){};
-#pragma unroll
-            for (int k = 0; k < kQ; ++k) {
-                const f16x8 kf = __builtin_bit_cast(f16x8, keys[buf][key_place<D>(32 * st + n, 2 * k + hf)]);
-                sc_[st] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, q[k], sc_[st], 0, 0, 0);
+        for (int i = 0; i < kV; ++i) {
+            if (g < 4) {
+                frag[g % kRing][i] = values[buf][value_place(32 * i + n, 2 * g + hf)];
+            } else {
+                const int k = (g - 4) * (kQ / 4) + i / 2;
+                frag[g % kRing][i] = keys[buf ^ 1][key_place<D>(32 * (i & 1) + n, 2 * k + hf)];
             }
         }
-        // register i of score tile st is of token t + 32 st + 8 (i / 4) + 4 hf + i % 4
+    };
+    // Register i of score[st] is of the tile's token 32 st + 8 (i / 4) + 4 hf + i % 4.
+    auto multiply = [&](auto index) __attribute__((always_inline)) {
+        constexpr int g = decltype(index)::value;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int e = kscale[buf][u];
-            const float factor = e == 256 ? __builtin_nanf("") : __builtin_ldexpf(sc.c0, e - shift);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sc_[u >> 1][8 * (u & 1) + i] *= factor;
+        for (int i = 0; i < kV; ++i) {
+            if (g < 4) {
+                acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, frag[g % kRing][i]),
+                                                                 __builtin_bit_cast(bf16x8, p[g & 3]), acc[i], 0, 0, 0);
+            } else {
+                const int k = (g - 4) * (kQ / 4) + i / 2;
+                score[i & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, frag[g % kRing][i]), q[k],
+                                                                      k == 0 ? (f32x16){} : score[i & 1], 0, 0, 0);
+            }
         }
-        if (sc.cap2 > 0.0f) {
+    };
+    constexpr std::integral_constant<int, 0> g0{};
+    constexpr std::integral_constant<int, 1> g1{};
+    constexpr std::integral_constant<int, 2> g2{};
+    constexpr std::integral_constant<int, 3> g3{};
+    constexpr std::integral_constant<int, 4> g4{};
+    constexpr std::integral_constant<int, 5> g5{};
+    constexpr std::integral_constant<int, 6> g6{};
+    constexpr std::integral_constant<int, 7> g7{};
+    const int shift127 = shift + 127;
+    auto factors = [&](int ke, int first) __attribute__((always_inline)) {
 #pragma unroll
-            for (int st = 0; st < 2; ++st)
+        for (int u = 0; u < 4; ++u) f[u] = score_factor(sc.c0, lane_of(ke, first + u), shift127);
+    };
+    // whether the lane's row sees the key that register i of group u holds: one
+    // comparison of the distance from the row's first key with its span
+    const bool sees = jhi >= jlo;
+    const int from = 4 * hf - (sees ? jlo : 1 << 30);
+    const uint32_t span = sees ? (uint32_t)(jhi - jlo) : 0;
+    auto seen = [&](int t, int u, int i) __attribute__((always_inline)) {
+        return (uint32_t)(t + from) + (uint32_t)(16 * u + 8 * (i >> 2) + (i & 3)) <= span;
+    };
+    // score -> p, with the running maximum and sum
+    auto soften = [&](int t) __attribute__((always_inline)) {
+        if (CAP) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) sc_[st][i] = capped(sc_[st][i], sc.cap2);
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) score[u >> 1][8 * (u & 1) + i] = capped(score[u >> 1][8 * (u & 1) + i] * f[u], sc.cap2);
         }
-        const bool whole = t >= all_lo && t + kLongKeys - 1 <= all_hi;
-        if (!whole) {
+        if (t < all_lo || t + kLongKeys - 1 > all_hi) {
 #pragma unroll
-            for (int st = 0; st < 2; ++st)
+            for (int u = 0; u < 4; ++u)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int j = t + 32 * st + 8 * (i >> 2) + 4 * hf + (i & 3);
-                    sc_[st][i] = j >= jlo && j <= jhi ? sc_[st][i] : -__builtin_inff();
-                }
+                for (int i = 0; i < 8; ++i)
+                    score[u >> 1][8 * (u & 1) + i] = seen(t, u, i) ? score[u >> 1][8 * (u & 1) + i] : -__builtin_inff();
         }
         float mt = -__builtin_inff();
 #pragma unroll
-        for (int st = 0; st < 2; ++st)
+        for (int u = 0; u < 4; ++u) {
+            float g = -__builtin_inff();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) mt = fmaxf(mt, sc_[st][i]);
-        mt = fmaxf(mt, __shfl_xor(mt, 32));
-        if (__any(mt > m)) {
+            for (int i = 0; i < 8; ++i) g = fmaxf(g, score[u >> 1][8 * (u & 1) + i]);
+            mt = fmaxf(mt, CAP ? g : g * f[u]);
+        }
+        mt = max_halves(mt);
+        if (__any(mt > m + kSlack)) {
             const float mn = fmaxf(m, mt);
             const float alpha = mn > m ? exp2_hw(m - mn) : 1.0f;
             m = mn;
             l *= alpha;
+            l2 *= alpha;
 #pragma unroll
             for (int i = 0; i < kV; ++i) acc[i] *= alpha;
         }
         const float mu = m == -__builtin_inff() ? 0.0f : m;
-        bf16x8 p[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < 4; ++u) {
+            float e[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float e = exp2_hw(sc_[u >> 1][8 * (u & 1) + i] - mu);
-                l += e;
-                p[u][i] = (__bf16)e;
+                const float x = score[u >> 1][8 * (u & 1) + i];
+                e[i] = exp2_hw(CAP ? x - mu : __builtin_fmaf(x, f[u], -mu));
             }
-        if (!whole && nan_tile[buf] == t) {
-            // A NaN value reaches exactly the rows that see its token: count
-            // such tokens per row by a product of ones.
-            bf16x8 seen[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int j = t + 16 * u + 8 * (i >> 2) + 4 * hf + (i & 3);
-                    seen[u][i] = (__bf16)(j >= jlo && j <= jhi ? 1.0f : 0.0f);
-                }
-#pragma unroll
-            for (int i = 0; i < kV; ++i) {
-                f32x16 cnt = {};
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    bf16x8 vf = __builtin_bit_cast(bf16x8, values[buf][value_place(32 * i + n, 2 * u + hf)]), ones;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const bool bad = vf[k] != vf[k];
-                        ones[k] = (__bf16)(bad ? 1.0f : 0.0f);
-                        vf[k] = bad ? (__bf16)0.0f : vf[k];
-                    }
-                    cnt = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ones, seen[u], cnt, 0, 0, 0);
-                    acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, p[u], acc[i], 0, 0, 0);
-                }
-#pragma unroll
-                for (int k = 0; k < 16; ++k) acc[i][k] = cnt[k] > 0.0f ? __builtin_nanf("") : acc[i][k];
-            }
-            return;
+            p[u] = make_uint4(bf16_pair(e[0], e[1]), bf16_pair(e[2], e[3]), bf16_pair(e[4], e[5]), bf16_pair(e[6], e[7]));
+            // the sum of what the second product takes, two at a time
+            l = sum_pair(p[u].x, l);
+            l2 = sum_pair(p[u].y, l2);
+            l = sum_pair(p[u].z, l);
+            l2 = sum_pair(p[u].w, l2);
         }
-#pragma unroll
-        for (int i = 0; i < kV; ++i)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const bf16x8 vf = __builtin_bit_cast(bf16x8, values[buf][value_place(32 * i + n, 2 * u + hf)]);
-                acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, p[u], acc[i], 0, 0, 0);
-            }
     };
-
-    if (tid < 2) nan_tile[tid] = -1;
+    if (tid == 0) nan_seen = 0;
     __syncthreads();
     if (begin < end) {
-        find_pages(begin);
-        load(begin);
-        find_pages(begin + kLongKeys);
-        store(0, begin);
-    }
-    __syncthreads();
-    int buf = 0;
-    for (int t = begin; t < end; t += kLongKeys, buf ^= 1) {
-        const bool more = t + kLongKeys < end;
-        if (more) {
-            load(t + kLongKeys);
-            find_pages(t + 2 * kLongKeys);
-        }
-        if (t <= any_hi && t + kLongKeys > any_lo) multiply(buf, t);
-        if (more) store(buf ^ 1, t + kLongKeys);
+        Block now = block(entries(begin)), next = block(entries(begin + 1024));
+        int after = entries(begin + 2048), base = begin;
+        load_k(begin, lane_of(now.page, k_group));
+        load_v(begin, lane_of(now.page, v_group), lane_of(now.ve, v_group));
+        store_k(0);
+        store_v(0, begin);
+        load_k(begin + kLongKeys, lane_of(now.page, 4 + k_group));
+        store_k(1);
         __syncthreads();
+        factors(now.ke, 0);
+        read(g4, 1);
+        read(g5, 1);
+        multiply(g4);
+        read(g6, 1);
+        multiply(g5);
+        read(g7, 1);
+        multiply(g6);
+        multiply(g7);
+        // the first step stores over these keys
+        __syncthreads();
+        // A step forms tile t's probabilities, then multiplies: values of t, keys
+        // of t + 1.  What it stores at its end, keys of t + 2 and values of t + 1,
+        // goes where the step before has read its last, so one barrier a step
+        // is enough.  The last step loads, stores and multiplies keys that no
+        // row sees: without a branch around them the results stay in their
+        // registers.
+        int buf = 0;
+        for (int t = begin; t < end; t += kLongKeys, buf ^= 1) {
+            if (t + kLongKeys - base == 1024) {
+                base += 1024;
+                now = next;
+                next = block(after);
+                after = entries(base + 2048);
+            }
+            const int group = (t + kLongKeys - base) >> 4;  // of tile t + 1
+            load_k(t + 2 * kLongKeys, group < 60 ? lane_of(now.page, group + 4 + k_group) : lane_of(next.page, k_group));
+            load_v(t + kLongKeys, lane_of(now.page, group + v_group), lane_of(now.ve, group + v_group));
+            soften(t);
+            __builtin_amdgcn_sched_barrier(0);
+            read(g0, buf);
+            read(g1, buf);
+            read(g2, buf);
+            multiply(g0);
+            read(g3, buf);
+            multiply(g1);
+            read(g4, buf);
+            multiply(g2);
+            read(g5, buf);
+            multiply(g3);
+            factors(now.ke, group);
+            read(g6, buf);
+            multiply(g4);
+            read(g7, buf);
+            multiply(g5);
+            multiply(g6);
+            multiply(g7);
+            // in this order: three groups read, then one multiplied, one read ..
+            __builtin_amdgcn_sched_group_barrier(kReads, 3 * kV, 0);
+            __builtin_amdgcn_sched_group_barrier(kProducts, kV, 0);
+            __builtin_amdgcn_sched_group_barrier(kReads, kV, 0);
+            __builtin_amdgcn_sched_group_barrier(kProducts, kV, 0);
+            __builtin_amdgcn_sched_group_barrier(kReads, kV, 0);
+            __builtin_amdgcn_sched_group_barrier(kProducts, kV, 0);
+            __builtin_amdgcn_sched_group_barrier(kReads, kV, 0);
+            __builtin_amdgcn_sched_group_barrier(kProducts, kV, 0);
+            __builtin_amdgcn_sched_group_barrier(kReads, kV, 0);
+            __builtin_amdgcn_sched_group_barrier(kProducts, kV, 0);
+            __builtin_amdgcn_sched_group_barrier(kReads, kV, 0);
+            __builtin_amdgcn_sched_group_barrier(kProducts, 3 * kV, 0);
+            store_k(buf);
+            store_v(buf ^ 1, t + kLongKeys);
+            __syncthreads();
+        }
+        // the last tile's values were stored before a barrier that every
+        // wavefront has passed
+        if (__builtin_amdgcn_readfirstlane(nan_seen)) {
+            // A NaN value reaches exactly the rows that see its token, which p
+            // cannot say (0 times NaN is NaN): it was stored as 0, and here such
+            // tokens are counted per row by products of ones.
+            for (int t = begin; t < end; t += 16) {
+                const int physical = table[t >> log_page];
+                if (physical < 0 || physical >= a.cache.pages) continue;
+                const uint8_t* row = vc + physical * page_bytes + n * page + (t & (page - 1));
+                bf16x8 one;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) one[k] = (__bf16)(seen(t, 0, k) ? 1.0f : 0.0f);
+#pragma unroll
+                for (int i = 0; i < kV; ++i) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(row + 32 * i * page);
+                    const uint32_t w0 = nan_bytes(hf ? w.y : w.x), w1 = nan_bytes(hf ? w.w : w.z);
+                    if (!__any((w0 | w1) != 0)) continue;
+                    // 0x38: the code of 1
+                    const f32x16 cnt = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen_bf16(w0 * 0x38u, w1 * 0x38u, 1.0f), one, (f32x16){}, 0, 0, 0);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) acc[i][k] += cnt[k] > 0.0f ? __builtin_nanf("") : 0.0f;
+                }
+            }
+        }
     }
 
+    l += l2;
     l += __shfl_xor(l, 32);
     if (r < rows) {
         uint16_t* y = a.y + ((int64_t)(s.row0 + token) * a.heads + head * group + member) * D;
@@ -856,7 +1003,8 @@ hipError_t launch_attention(const KvAttentionArgs& a, hipStream_t stream) {
     if (b.cu && (int64_t)b.tokens * group > kShortRows) {
         LongPlan pl;
         pl.slots = (int)kv_items(b, group, 8, 1);
-        const hipError_t e = launch(k_attention_long<D>, dim3((uint32_t)(pl.slots * c.kv_heads)), dim3(64 * kLongWaves), stream, a, pl, sc);
+        const hipError_t e = launch(a.softcap > 0.0f ? k_attention_long<D, true> : k_attention_long<D, false>,
+                                    dim3((uint32_t)(pl.slots * c.kv_heads)), dim3(64 * kLongWaves), stream, a, pl, sc);
         if (e != hipSuccess) return e;
     }
     const ShortPlan pl = short_plan(c, b, a.heads, a.workspace_bytes);
@@ -877,6 +1025,8 @@ bool kv_attention_fits(const KvAttentionArgs& a) {
     const KvBatchArgs& b = a.batch;
     const int64_t most = 0xFFFFFFFFll;
     const ShortPlan pl = short_plan(c, b, a.heads, a.workspace_bytes);
+    // rows of a sequence are counted in 32 bits
+    if ((int64_t)b.tokens * (a.heads / c.kv_heads) >= ((int64_t)1 << 31) - kLongRows) return false;
     const int64_t tiles = b.cu ? kv_items(b, a.heads / c.kv_heads, 8, 1) : 0;
     return tiles * c.kv_heads <= most / (64 * kLongWaves) &&
            (int64_t)pl.slots * pl.tiles * c.kv_heads <= most / (64 * kShortWaves) &&

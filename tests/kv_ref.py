@@ -133,7 +133,9 @@ def attention(cache, table, lengths, cu, q, rope=None, scale=None, softcap=0.0, 
     8 u of the cap (tanh from an exponential and a reciprocal of 1 ulp each).
     A probability is then off by exp(d_s) - 1, the exponential's 2 ulp and the
     rounding of its argument, |s - m| u; in the numerator also by its rounding to
-    BF16 (2^-8; 2^-16 in two parts).  Sums over n keys add (1.25 n + 8) 2^-23
+    BF16 (2^-8; 2^-16 in two parts), and with one part in the sum as well, which
+    adds up what the numerator takes: with weights p (1 + d), |d| <= 2^-8, both
+    are off by at most 2^-8 of their magnitudes.  Sums over n keys add (1.25 n + 8) 2^-23
     (chunks and wavefronts included).  The quotient takes both sums' errors,
     and the result one rounding to BF16."""
     tokens, heads, dim = q.shape
@@ -191,7 +193,7 @@ def attention(cache, table, lengths, cu, q, rope=None, scale=None, softcap=0.0, 
                     total = p.sum()
                     sums = (1.25 * len(s) + 8) * 2 * u
                     num = np.abs(vv).T @ (p * (eps + 2.0 ** (-8 * parts))) + sums * (np.abs(vv).T @ p)
-                    den = (p * eps).sum() + sums * total
+                    den = (p * eps).sum() + sums * total + (2.0 ** -8 * total if parts == 1 else 0.0)
                     yy = (vv.T @ p) / total
                     y[r, hh] = yy
                     t = (num + np.abs(yy) * den) / max(total - den, 1e-300)
