@@ -161,43 +161,40 @@ inline Scoring scoring(const KvAttentionArgs& a) {
 // ---------------------------------------------------------------------------
 //
 // The keys of all sequences are cut into chunks of equal length, so many that
-// they fill the GPU, and a workgroup takes one chunk of one head.  The lengths
-// are device memory: every workgroup adds them up, derives the chunk length and
-// finds its own.  A sequence of several chunks leaves unnormalised sums, and
-// their maximum, in the workspace, and a second kernel joins them in order.
+// they fill the GPU, and a workgroup takes one chunk of one head and of 16 of
+// the sequence's rows at a time.  The lengths are device memory: every
+// workgroup adds them up, derives the chunk length and finds its own.  A
+// sequence of several chunks leaves unnormalised sums, and their maximum, in
+// the workspace, and a second kernel joins them in order.
 
 struct ShortPlan {
-    int64_t target;  // chunks per head to aim at; 0: one per sequence
-    int slots;       // workgroups per head and tile
-    int tiles;       // tiles of 16 rows
-    int rows;        // rows of a sequence, at most
+    int64_t target;  // items per head to aim at; 0: one chunk per sequence
+    int slots;       // items per head, at most
+    int unit;        // keys that a chunk is a multiple of
 };
 
 constexpr int kNoPage = 1 << 16;  // in the place of a page's exponent
-constexpr int kShortWaves = 4, kShortStep = 64, kChunkUnit = kShortWaves * kShortStep;
+constexpr int kShortStep = 64;    // keys of a wavefront's step
 
 struct ShortSequence {
     KvSequence s;
     int begin, end;  // keys that some row sees, begin a multiple of 64
+    int tiles;       // of 16 rows; 0: no rows, or too many
 };
 
 __device__ __forceinline__ bool is_short(int rows, int group) { return rows == 1 || (int64_t)rows * group <= kShortRows; }
 
-// False: no rows, or too many.
-__device__ __forceinline__ bool short_sequence(const KvAttentionArgs& a, int group, int i, ShortSequence& q) {
+__device__ __forceinline__ ShortSequence short_sequence(const KvAttentionArgs& a, int group, int i) {
+    ShortSequence q;
     q.s = kv_sequence(a.batch, i);
     const int64_t room = (int64_t)a.batch.max_pages << a.cache.log_page;
     const int64_t first = q.s.first();
     q.end = (int)(q.s.length < room ? q.s.length : room);
     q.begin = 0;
     if (a.window > 0 && first >= a.window) q.begin = (int)min((first - a.window + 1) & ~(int64_t)(kShortStep - 1), (int64_t)q.end);
-    return q.s.rows > 0 && is_short(q.s.rows, group);
+    q.tiles = q.s.rows > 0 && is_short(q.s.rows, group) ? (q.s.rows * group + 15) / 16 : 0;
+    return q;
 }
-
-struct Share {
-    int seq, number, count, slot0;
-    int64_t chunk;  // keys, a multiple of kChunkUnit
-};
 
 __device__ __forceinline__ int chunks_of(int keys, int64_t chunk) { return keys > 0 ? (int)((keys + chunk - 1) / chunk) : 1; }
 
@@ -205,53 +202,77 @@ __device__ __forceinline__ int64_t chunk_length(const KvAttentionArgs& a, const 
     if (pl.target == 0) return (int64_t)1 << 31;
     const int lane = threadIdx.x & 63;
     int64_t keys = 0;
-    for (int base = 0; base < a.batch.sequences; base += 64) {
-        ShortSequence q;
-        if (base + lane < a.batch.sequences && short_sequence(a, group, base + lane, q)) keys += q.end - q.begin;
-    }
+    for (int base = 0; base < a.batch.sequences; base += 64)
+        if (base + lane < a.batch.sequences) {
+            const ShortSequence q = short_sequence(a, group, base + lane);
+            keys += (int64_t)(q.end - q.begin) * q.tiles;
+        }
 #pragma unroll
     for (int m = 1; m < 64; m *= 2) keys += __shfl_xor(keys, m);
     const int64_t each = (keys + pl.target - 1) / pl.target;
-    return max((each + kChunkUnit - 1) / kChunkUnit, (int64_t)1) * kChunkUnit;
+    return max((each + pl.unit - 1) / pl.unit, (int64_t)1) * pl.unit;
 }
 
-// The share of workgroup `slot`; false: none.
-__device__ __forceinline__ bool find_share(const KvAttentionArgs& a, const ShortPlan& pl, int group, int slot, Share& out) {
+// Item `first + number * tiles + tile` of a head is chunk `number` of a
+// sequence's 16-row tile.
+struct Share {
+    int seq, tile, number, count;
+};
+
+__device__ __forceinline__ bool find_share(const KvAttentionArgs& a, int group, int64_t chunk, int item, Share& out) {
     const int lane = threadIdx.x & 63;
-    out.chunk = chunk_length(a, pl, group);
     int before = 0;
     for (int base = 0; base < a.batch.sequences; base += 64) {
-        ShortSequence q;
-        int mine = 0;
-        if (base + lane < a.batch.sequences && short_sequence(a, group, base + lane, q)) mine = chunks_of(q.end - q.begin, out.chunk);
-        int upto = mine;
+        int tiles = 0, count = 0;
+        if (base + lane < a.batch.sequences) {
+            const ShortSequence q = short_sequence(a, group, base + lane);
+            tiles = q.tiles;
+            count = chunks_of(q.end - q.begin, chunk);
+        }
+        int upto = tiles * count;
 #pragma unroll
         for (int m = 1; m < 64; m *= 2) {
             const int n = __shfl_up(upto, m);
             if (lane >= m) upto += n;
         }
-        const uint64_t past = __ballot(slot < before + upto);
+        const uint64_t past = __ballot(item < before + upto);
         if (past) {
             const int at = __builtin_ctzll(past);
             out.seq = base + at;
-            out.count = __shfl(mine, at);
-            out.slot0 = before + __shfl(upto, at) - out.count;
-            out.number = slot - out.slot0;
+            out.count = __builtin_amdgcn_readlane(count, at);
+            tiles = __builtin_amdgcn_readlane(tiles, at);
+            const int k = item - (before + __builtin_amdgcn_readlane(upto, at) - out.count * tiles);
+            out.number = k / tiles;
+            out.tile = k - out.number * tiles;
             return true;
         }
-        before += __shfl(upto, 63);
+        before += __builtin_amdgcn_readlane(upto, 63);
     }
     return false;
 }
 
-// Workspace: per slot, head and row the sums [dim], then per slot, head and row
-// the maximum (base 2) and the sum of the probabilities.
-__device__ __forceinline__ float* part_at(const KvAttentionArgs& a, const ShortPlan& pl, int slot, int head, int row) {
-    return a.workspace + (((int64_t)slot * a.cache.kv_heads + head) * pl.rows + row) * a.cache.dim;
+// Items of the sequences before one.
+__device__ __forceinline__ int items_before(const KvAttentionArgs& a, int group, int64_t chunk, int seq) {
+    const int lane = threadIdx.x & 63;
+    int n = 0;
+    for (int base = 0; base < seq; base += 64)
+        if (base + lane < seq) {
+            const ShortSequence q = short_sequence(a, group, base + lane);
+            n += q.tiles * chunks_of(q.end - q.begin, chunk);
+        }
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) n += __shfl_xor(n, m);
+    return n;
 }
-__device__ __forceinline__ float2* part_stat(const KvAttentionArgs& a, const ShortPlan& pl, int slot, int head, int row) {
-    float* p = a.workspace + (int64_t)pl.slots * a.cache.kv_heads * pl.rows * a.cache.dim;
-    return reinterpret_cast<float2*>(p) + ((int64_t)slot * a.cache.kv_heads + head) * pl.rows + row;
+
+// Workspace: per item, head and row of 16 the sums [dim], then per item, head
+// and row the maximum (base 2) and the sum of the probabilities.
+__device__ __forceinline__ float* part_at(const KvAttentionArgs& a, int item, int head, int row) {
+    return a.workspace + (((int64_t)item * a.cache.kv_heads + head) * 16 + row) * a.cache.dim;
+}
+__device__ __forceinline__ float2* part_stat(const KvAttentionArgs& a, int slots, int item, int head, int row) {
+    float* p = a.workspace + (int64_t)slots * a.cache.kv_heads * 16 * a.cache.dim;
+    return reinterpret_cast<float2*>(p) + ((int64_t)item * a.cache.kv_heads + head) * 16 + row;
 }
 
 // What a row's sum becomes: no key (zeros), keys that have no page (NaN).
@@ -260,33 +281,91 @@ __device__ __forceinline__ float row_result(float sum, float total, int64_t pos,
     return pos < room ? sum / total : __builtin_nanf("");
 }
 
-template <int D>
-__global__ __launch_bounds__(64 * kShortWaves, 2) void k_attention_short(KvAttentionArgs a, ShortPlan pl, Scoring sc) {
+template <int D, int WAVES>
+struct ShortLds {
+    static constexpr int kRow = D + 4;
+    __attribute__((aligned(16))) float out[WAVES][16 * kRow];
+    float2 stat[WAVES][16];
+};
+
+// One item of WAVES wavefronts.
+template <int D, int WAVES>
+__device__ __forceinline__ void short_item(const KvAttentionArgs& a, const ShortPlan& pl, const Scoring& sc, const Share& sh,
+                                           int64_t chunk, int item, int head, ShortLds<D, WAVES>& lds) {
     constexpr int kQ = D / 32;       // products per 16 tokens
     constexpr int kV = D / 16;       // tiles of the result
-    constexpr int kOutRow = D + 4;
-    __shared__ __attribute__((aligned(16))) float out[kShortWaves][16 * kOutRow];
-    __shared__ float2 stat[kShortWaves][16];
+    constexpr int kOutRow = ShortLds<D, WAVES>::kRow, kStride = WAVES * kShortStep;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int x = lane & 15, c = lane >> 4;
     const int kvh = a.cache.kv_heads, group = a.heads / kvh;
-    const int head = (int)(blockIdx.x % (uint32_t)kvh);
-    const int tile = (int)(blockIdx.x / (uint32_t)kvh % (uint32_t)pl.tiles), slot = (int)(blockIdx.x / (uint32_t)kvh / (uint32_t)pl.tiles);
-
-    Share sh;
-    if (!find_share(a, pl, group, slot, sh)) return;
-    ShortSequence sq;
-    short_sequence(a, group, sh.seq, sq);
+    const ShortSequence sq = short_sequence(a, group, sh.seq);
     const int rows = sq.s.rows * group;
-    if (16 * tile >= rows) return;
     const int log_page = a.cache.log_page, page = 1 << log_page;
     const int first = (int)sq.s.first();
 
     // the lane's query row
-    const int r = 16 * tile + x, token = min(r, rows - 1) / group, member = min(r, rows - 1) - token * group;
+    const int r = 16 * sh.tile + x, token = min(r, rows - 1) / group, member = min(r, rows - 1) - token * group;
     const int pos = r < rows ? first + token : -1;
-    const int pos_lo = first + 16 * tile / group, pos_hi = first + min(16 * tile + 15, rows - 1) / group;
+    const int pos_lo = first + 16 * sh.tile / group, pos_hi = first + min(16 * sh.tile + 15, rows - 1) / group;
+
+    const int jlo = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
+    const int begin = (int)min((int64_t)sq.begin + sh.number * chunk, (int64_t)sq.end);
+    const int end = (int)min((int64_t)sq.end, (int64_t)begin + chunk);
+    const int jhi = min(pos, end - 1);
+    // keys that every row of the tile sees, and that any sees
+    const int all_lo = a.window > 0 ? max(pos_hi - a.window + 1, 0) : 0, all_hi = min(pos_lo, end - 1);
+    const int any_lo = a.window > 0 ? max(pos_lo - a.window + 1, 0) : 0, any_hi = min(pos_hi, end - 1);
+
+    const int* table = a.batch.table + (int64_t)sh.seq * a.batch.table_stride;
+    const int kgroup = 16 * (x >> 2);  // tokens that the lane's keys are of, within a step; its scores and values: 16 c
+
+    uint4 kb[4][D / 64];
+    uint4 vb[kV];
+    bool has_page = false;
+    uint32_t ks = 0, vs = 0;
+
+    // The table's entries are read two steps ahead and looked at only where
+    // they are used; behind the last key that of the last one, whose page the
+    // masks hide.
+    auto entry_of = [&](int t) { return table[min(t, end - 1) >> log_page]; };
+    auto is_page = [&](int e) { return e >= 0 && e < a.cache.pages; };
+    auto load_k = [&](int t, int e) {
+        const int j = t + kgroup;
+        const uint8_t* p = a.cache.kc + (((int64_t)(is_page(e) ? e : 0) * kvh + head) * page + (j & (page - 1)) + (x & 3)) * D + c * (D / 4);
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) kb[g][i] = *reinterpret_cast<const uint4*>(p + 4 * g * D + 16 * i);
+    };
+    auto load_v = [&](int t, int e) {
+        const int j = t + 16 * c;
+        const uint8_t* p = a.cache.vc + (((int64_t)(is_page(e) ? e : 0) * kvh + head) * D + x) * page + (j & (page - 1));
+#pragma unroll
+        for (int i = 0; i < kV; ++i) vb[i] = *reinterpret_cast<const uint4*>(p + (int64_t)16 * i * page);
+    };
+    auto load_s = [&](int e) {
+        has_page = is_page(e);
+        const int64_t at = (int64_t)(has_page ? e : 0) * kvh + head;
+        ks = a.cache.ks[at];
+        vs = a.cache.vs[at];
+    };
+
+    f32x4 acc[kV];
+#pragma unroll
+    for (int i = 0; i < kV; ++i) acc[i] = (f32x4){};
+    float m = -__builtin_inff(), l = 0.0f;
+
+    int t = begin + kShortStep * wave;
+    int ke = 0, ve = 0;  // entries of the next step
+    if (t < end) {
+        const int k0 = entry_of(t + kgroup), v0 = entry_of(t + 16 * c);
+        ke = entry_of(t + kStride + kgroup);
+        ve = entry_of(t + kStride + 16 * c);
+        load_k(t, k0);
+        load_s(v0);
+        load_v(t, v0);
+    }
     f16x8 q[kQ];
     int shift;
     {
@@ -323,63 +402,9 @@ __global__ __launch_bounds__(64 * kShortWaves, 2) void k_attention_short(KvAtten
         for (int k = 0; k < kQ; ++k) q[k] = narrow(f[k], shift, sc.sign);
     }
 
-    const int jlo = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
-    const int begin = (int)min((int64_t)sq.begin + sh.number * sh.chunk, (int64_t)sq.end);
-    const int end = (int)min((int64_t)sq.end, (int64_t)begin + sh.chunk);
-    const int jhi = min(pos, end - 1);
-    // keys that every row of the tile sees, and that any sees
-    const int all_lo = a.window > 0 ? max(pos_hi - a.window + 1, 0) : 0, all_hi = min(pos_lo, end - 1);
-    const int any_lo = a.window > 0 ? max(pos_lo - a.window + 1, 0) : 0, any_hi = min(pos_hi, end - 1);
-
-    const int* table = a.batch.table + (int64_t)sh.seq * a.batch.table_stride;
-    const int kgroup = 16 * (x >> 2);  // tokens that the lane's keys are of, within a step; its scores and values: 16 c
-
-    uint4 kb[4][D / 64];
-    uint4 vb[kV];
-    int kpage, vpage;  // physical, -1: none
-    int ks;
-    float vs;
-
-    auto page_of = [&](int t) {
-        const int e = t < end ? table[t >> log_page] : -1;
-        return e >= 0 && e < a.cache.pages ? e : -1;
-    };
-    auto load_k = [&](int t) {
-        const int j = t + kgroup;
-        const uint8_t* p = a.cache.kc + (((int64_t)max(kpage, 0) * kvh + head) * page + (j & (page - 1)) + (x & 3)) * D + c * (D / 4);
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-#pragma unroll
-            for (int i = 0; i < D / 64; ++i) kb[g][i] = *reinterpret_cast<const uint4*>(p + 4 * g * D + 16 * i);
-    };
-    auto load_v = [&](int t) {
-        const int j = t + 16 * c;
-        const uint8_t* p = a.cache.vc + (((int64_t)max(vpage, 0) * kvh + head) * D + x) * page + (j & (page - 1));
-#pragma unroll
-        for (int i = 0; i < kV; ++i) vb[i] = *reinterpret_cast<const uint4*>(p + (int64_t)16 * i * page);
-    };
-    auto load_s = [&]() {
-        const int64_t at = (int64_t)max(vpage, 0) * kvh + head;
-        ks = vpage < 0 ? kNoPage : (int)a.cache.ks[at] - 127;
-        vs = e8m0_f32(a.cache.vs[at]);
-    };
-
-    f32x4 acc[kV];
-#pragma unroll
-    for (int i = 0; i < kV; ++i) acc[i] = (f32x4){};
-    float m = -__builtin_inff(), l = 0.0f;
-
-    int t = begin + kShortStep * wave;
-    if (t < end) {
-        kpage = page_of(t + kgroup);
-        vpage = page_of(t + 16 * c);
-        load_k(t);
-        load_s();
-        load_v(t);
-    }
     while (t < end) {
-        const int tn = t + kChunkUnit;
-        const int kpage_n = page_of(tn + kgroup), vpage_n = page_of(tn + 16 * c);
+        const int tn = t + kStride;
+        const int ke_n = entry_of(tn + kStride + kgroup), ve_n = entry_of(tn + kStride + 16 * c);
         // scores: s[g][i] is of token t + 16 c + 4 g + i
         f32x4 s[4];
 #pragma unroll
@@ -391,14 +416,12 @@ __global__ __launch_bounds__(64 * kShortWaves, 2) void k_attention_short(KvAtten
                 s[g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen_f16(kb[g][i].z, kb[g][i].w), q[2 * i + 1], s[g], 0, 0, 0);
             }
         }
-        const float factor = ks == kNoPage ? __builtin_nanf("") : score_factor(sc.c0, ks, shift);
-        const float vscale = vs;
-        const int vpage_now = vpage;
-        kpage = kpage_n;
-        vpage = vpage_n;
+        const bool here = has_page;
+        const float factor = here ? score_factor(sc.c0, (int)ks - 127, shift) : __builtin_nanf("");
+        const float vscale = e8m0_f32(vs);
         if (tn < end) {
-            load_k(tn);
-            load_s();
+            load_k(tn, ke);
+            load_s(ve);
         }
 #pragma unroll
         for (int g = 0; g < 4; ++g)
@@ -426,8 +449,8 @@ __global__ __launch_bounds__(64 * kShortWaves, 2) void k_attention_short(KvAtten
 #pragma unroll
             for (int i = 0; i < 4; ++i) mt = fmaxf(mt, s[g][i]);
         mt = fmaxf(mt, __shfl_xor(mt, 16));
-        mt = fmaxf(mt, __shfl_xor(mt, 32));
-        if (__any(mt > m)) {
+        mt = max_halves(mt);
+        if (__any(mt > m + kSlack)) {
             const float mn = fmaxf(m, mt);
             const float alpha = mn > m ? exp2_hw(m - mn) : 1.0f;
             m = mn;
@@ -437,7 +460,7 @@ __global__ __launch_bounds__(64 * kShortWaves, 2) void k_attention_short(KvAtten
         }
         const float mu = m == -__builtin_inff() ? 0.0f : m;
         // P in two BF16 parts, so that its rounding does not show in the result
-        bf16x8 ph[2], pl_[2];
+        bf16x8 ph[2], pr[2];
 #pragma unroll
         for (int g = 0; g < 4; ++g)
 #pragma unroll
@@ -446,7 +469,7 @@ __global__ __launch_bounds__(64 * kShortWaves, 2) void k_attention_short(KvAtten
                 l += p;
                 const __bf16 h = (__bf16)p;
                 ph[g >> 1][4 * (g & 1) + i] = h;
-                pl_[g >> 1][4 * (g & 1) + i] = (__bf16)(p - (float)h);
+                pr[g >> 1][4 * (g & 1) + i] = (__bf16)(p - (float)h);
             }
         bool odd = false;
         if (!whole) {
@@ -458,7 +481,7 @@ __global__ __launch_bounds__(64 * kShortWaves, 2) void k_attention_short(KvAtten
                 for (int k = 0; k < 4; ++k) {
                     const int j = t + 16 * c + 4 * k;
                     w[k] &= first_bytes(any_hi + 1 - j) & ~first_bytes(any_lo - j);
-                    w[k] = vpage_now < 0 ? 0u : w[k];
+                    w[k] = here ? w[k] : 0u;
                     odd = odd || nan_bytes(w[k]) != 0;
                 }
                 vb[i] = make_uint4(w[0], w[1], w[2], w[3]);
@@ -497,33 +520,35 @@ __global__ __launch_bounds__(64 * kShortWaves, 2) void k_attention_short(KvAtten
             const bf16x8 v0 = widen_bf16(vb[i].x, vb[i].y, vscale), v1 = widen_bf16(vb[i].z, vb[i].w, vscale);
             acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, ph[0], acc[i], 0, 0, 0);
             acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, ph[1], acc[i], 0, 0, 0);
-            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, pl_[0], acc[i], 0, 0, 0);
-            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, pl_[1], acc[i], 0, 0, 0);
+            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, pr[0], acc[i], 0, 0, 0);
+            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, pr[1], acc[i], 0, 0, 0);
         }
-        if (tn < end) load_v(tn);
+        if (tn < end) load_v(tn, ve);
+        ke = ke_n;
+        ve = ve_n;
         t = tn;
     }
 
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
-    if (c == 0) stat[wave][x] = make_float2(m, l);
+    if (c == 0) lds.stat[wave][x] = make_float2(m, l);
 #pragma unroll
-    for (int i = 0; i < kV; ++i) *reinterpret_cast<f32x4*>(&out[wave][x * kOutRow + 16 * i + 4 * c]) = acc[i];
+    for (int i = 0; i < kV; ++i) *reinterpret_cast<f32x4*>(&lds.out[wave][x * kOutRow + 16 * i + 4 * c]) = acc[i];
     __syncthreads();
     const int64_t room = (int64_t)a.batch.max_pages << log_page;
-    for (int i = tid; i < 16 * (D / 4); i += 64 * kShortWaves) {
-        const int row = i / (D / 4), d = 4 * (i % (D / 4)), rr = 16 * tile + row;
+    for (int i = tid; i < 16 * (D / 4); i += 64 * WAVES) {
+        const int row = i / (D / 4), d = 4 * (i % (D / 4)), rr = 16 * sh.tile + row;
         if (rr >= rows) continue;
-        float mx = stat[0][row].x;
+        float mx = lds.stat[0][row].x;
 #pragma unroll
-        for (int w = 1; w < kShortWaves; ++w) mx = fmaxf(mx, stat[w][row].x);
+        for (int w = 1; w < WAVES; ++w) mx = fmaxf(mx, lds.stat[w][row].x);
         float total = 0.0f;
         f32x4 o = {};
 #pragma unroll
-        for (int w = 0; w < kShortWaves; ++w) {
-            const float f = mx == -__builtin_inff() ? 0.0f : exp2_hw(stat[w][row].x - mx);
-            total += f * stat[w][row].y;
-            o += f * *reinterpret_cast<const f32x4*>(&out[w][row * kOutRow + d]);
+        for (int w = 0; w < WAVES; ++w) {
+            const float f = mx == -__builtin_inff() ? 0.0f : exp2_hw(lds.stat[w][row].x - mx);
+            total += f * lds.stat[w][row].y;
+            o += f * *reinterpret_cast<const f32x4*>(&lds.out[w][row * kOutRow + d]);
         }
         if (sh.count == 1) {
             const int tok = rr / group, mem = rr - tok * group;
@@ -533,47 +558,81 @@ __global__ __launch_bounds__(64 * kShortWaves, 2) void k_attention_short(KvAtten
             v.y = bf16_pair(row_result(o[2], total, p, room), row_result(o[3], total, p, room));
             *reinterpret_cast<uint2*>(a.y + ((int64_t)(sq.s.row0 + tok) * a.heads + head * group + mem) * D + d) = v;
         } else {
-            *reinterpret_cast<f32x4*>(part_at(a, pl, slot, head, rr) + d) = o;
-            if (d == 0) *part_stat(a, pl, slot, head, rr) = make_float2(mx, total);
+            *reinterpret_cast<f32x4*>(part_at(a, item, head, row) + d) = o;
+            if (d == 0) *part_stat(a, pl.slots, item, head, row) = make_float2(mx, total);
         }
     }
 }
 
-// A workgroup joins the chunks of one row and head, in order.
-template <int D>
-__global__ __launch_bounds__(D) void k_attention_join(KvAttentionArgs a, ShortPlan pl) {
+// The items from `w` on, `stride` apart, of all heads.
+template <int D, int WAVES>
+__device__ __forceinline__ void short_items(const KvAttentionArgs& a, const ShortPlan& pl, const Scoring& sc, int w, int stride,
+                                            ShortLds<D, WAVES>& lds) {
     const int kvh = a.cache.kv_heads, group = a.heads / kvh;
-    const int head = (int)(blockIdx.x % (uint32_t)kvh);
-    const int row = (int)(blockIdx.x / (uint32_t)kvh % (uint32_t)pl.rows), seq = (int)(blockIdx.x / (uint32_t)kvh / (uint32_t)pl.rows);
-    ShortSequence sq;
-    if (!short_sequence(a, group, seq, sq) || row >= sq.s.rows * group) return;
+    const int64_t chunk = chunk_length(a, pl, group);
+    for (;; w += stride) {
+        const int head = w % kvh, item = w / kvh;
+        Share sh;
+        if (item >= pl.slots || !find_share(a, group, chunk, item, sh)) return;
+        short_item<D, WAVES>(a, pl, sc, sh, chunk, item, head, lds);
+        __syncthreads();  // the next item writes where this one has read
+    }
+}
+
+constexpr int kShortWaves = 4;
+
+template <int D>
+__global__ __launch_bounds__(64 * kShortWaves, 2) void k_attention_short(KvAttentionArgs a, ShortPlan pl, Scoring sc) {
+    __shared__ ShortLds<D, kShortWaves> lds;
+    short_items<D, kShortWaves>(a, pl, sc, (int)blockIdx.x, (int)gridDim.x, lds);
+}
+
+// A workgroup joins the chunks of rows of one sequence and head, in order:
+// `each` workgroups share a sequence's rows, four wavefronts the chunks.
+template <int D>
+__global__ __launch_bounds__(256) void k_attention_join(KvAttentionArgs a, ShortPlan pl, int each) {
+    constexpr int kPer = D / 64;  // elements of a lane
+    __shared__ float part[4][D];
+    __shared__ float sums[4];
+    const int kvh = a.cache.kv_heads, group = a.heads / kvh;
+    const int head = (int)(blockIdx.x % (uint32_t)kvh), seq = (int)(blockIdx.x / (uint32_t)kvh / (uint32_t)each);
+    const ShortSequence sq = short_sequence(a, group, seq);
+    if (sq.tiles == 0) return;
     const int64_t chunk = chunk_length(a, pl, group);
     const int count = chunks_of(sq.end - sq.begin, chunk);
     if (count == 1) return;
-    // the first slot: the chunks of the sequences before
-    const int lane = threadIdx.x & 63;
-    int slot0 = 0;
-    for (int base = 0; base < seq; base += 64) {
-        ShortSequence o;
-        if (base + lane < seq && short_sequence(a, group, base + lane, o)) slot0 += chunks_of(o.end - o.begin, chunk);
-    }
+    const int first = items_before(a, group, chunk, seq);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int row = (int)(blockIdx.x / (uint32_t)kvh % (uint32_t)each); row < sq.s.rows * group; row += each) {
+        const int item0 = first + row / 16, r = row % 16;
+        float mx = -__builtin_inff();
+        for (int i = lane; i < count; i += 64) mx = fmaxf(mx, part_stat(a, pl.slots, item0 + i * sq.tiles, head, r)->x);
 #pragma unroll
-    for (int k = 1; k < 64; k *= 2) slot0 += __shfl_xor(slot0, k);
-    const int d = threadIdx.x;
-    float mx = -__builtin_inff();
-    for (int i = lane; i < count; i += 64) mx = fmaxf(mx, part_stat(a, pl, slot0 + i, head, row)->x);
+        for (int k = 1; k < 64; k *= 2) mx = fmaxf(mx, __shfl_xor(mx, k));
+        float total = 0.0f, o[kPer] = {};
+#pragma unroll 4
+        for (int i = wave; i < count; i += 4) {
+            const int item = item0 + i * sq.tiles;
+            const float2 st = *part_stat(a, pl.slots, item, head, r);
+            const float f = mx == -__builtin_inff() ? 0.0f : exp2_hw(st.x - mx);
+            total += f * st.y;
+            const float* p = part_at(a, item, head, r) + kPer * lane;
 #pragma unroll
-    for (int k = 1; k < 64; k *= 2) mx = fmaxf(mx, __shfl_xor(mx, k));
-    float total = 0.0f, o = 0.0f;
-    for (int i = 0; i < count; ++i) {
-        const float2 st = *part_stat(a, pl, slot0 + i, head, row);
-        const float f = mx == -__builtin_inff() ? 0.0f : exp2_hw(st.x - mx);
-        total += f * st.y;
-        o += f * part_at(a, pl, slot0 + i, head, row)[d];
+            for (int k = 0; k < kPer; ++k) o[k] += f * p[k];
+        }
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) part[wave][kPer * lane + k] = o[k];
+        if (lane == 0) sums[wave] = total;
+        __syncthreads();
+        if (threadIdx.x < D) {
+            const int d = threadIdx.x, token = row / group, member = row - token * group;
+            const float sum = (part[0][d] + part[1][d]) + (part[2][d] + part[3][d]);
+            const float res = row_result(sum, (sums[0] + sums[1]) + (sums[2] + sums[3]), sq.s.first() + token,
+                                         (int64_t)a.batch.max_pages << a.cache.log_page);
+            a.y[((int64_t)(sq.s.row0 + token) * a.heads + head * group + member) * D + d] = (uint16_t)bf16_pair(res, 0.0f);
+        }
+        __syncthreads();
     }
-    const int token = row / group, member = row - token * group;
-    const float r = row_result(o, total, sq.s.first() + token, (int64_t)a.batch.max_pages << a.cache.log_page);
-    a.y[((int64_t)(sq.s.row0 + token) * a.heads + head * group + member) * D + d] = (uint16_t)bf16_pair(r, 0.0f);
 }
 
 // ---------------------------------------------------------------------------
@@ -974,23 +1033,31 @@ __global__ __launch_bounds__(64 * kLongWaves) void k_attention_long(KvAttentionA
 // launches
 // ---------------------------------------------------------------------------
 
-constexpr int kFill = 1024;  // workgroups to aim at: four per compute unit
+// Workgroups that the GPU holds at once (four wavefronts each, two per compute
+// unit), and items to aim at: twice as many, so that chunks of unequal length
+// even out.
+constexpr int kResident = 512, kFill = 1024;
 
-// Workspace bytes per slot.
-int64_t slot_bytes(const KvCacheArgs& c, int rows) { return (int64_t)c.kv_heads * rows * (c.dim + 2) * 4; }
+// Workspace bytes per item of all heads.
+int64_t slot_bytes(const KvCacheArgs& c) { return (int64_t)c.kv_heads * 16 * (c.dim + 2) * 4; }
+
+// 16-row tiles of all sequences, at most.
+int64_t short_tiles(const KvBatchArgs& b, int group) {
+    if (!b.cu) return (int64_t)b.sequences * ((group + 15) / 16);
+    const int64_t most = (group > kShortRows ? group : kShortRows) / 16 + 1, by_rows = (int64_t)b.tokens * group / 16 + b.sequences;
+    return by_rows < b.sequences * most ? by_rows : b.sequences * most;
+}
 
 ShortPlan short_plan(const KvCacheArgs& c, const KvBatchArgs& b, int heads, int64_t workspace_bytes) {
     ShortPlan pl;
-    const int group = heads / c.kv_heads;
-    pl.rows = b.cu ? (group > kShortRows ? group : kShortRows) : group;
-    if (b.cu && (int64_t)b.tokens * group < pl.rows) pl.rows = b.tokens * group;
-    pl.tiles = (pl.rows + 15) / 16;
+    pl.unit = kShortWaves * kShortStep;
+    const int64_t tiles = short_tiles(b, heads / c.kv_heads);
     // no sequence is longer than a chunk of the least length: nothing to split
-    const bool splits = ((int64_t)b.max_pages << c.log_page) > kChunkUnit;
-    const int64_t fit = workspace_bytes / slot_bytes(c, pl.rows) - b.sequences, want = (kFill + c.kv_heads - 1) / c.kv_heads;
+    const bool splits = ((int64_t)b.max_pages << c.log_page) > pl.unit;
+    const int64_t fit = workspace_bytes / slot_bytes(c) - tiles, want = (kFill + c.kv_heads - 1) / c.kv_heads;
     pl.target = splits ? (fit < want ? fit : want) : 0;
     if (pl.target < 1) pl.target = 0;
-    pl.slots = (int)(pl.target + b.sequences);
+    pl.slots = (int)(pl.target + tiles);
     return pl;
 }
 
@@ -1008,16 +1075,18 @@ hipError_t launch_attention(const KvAttentionArgs& a, hipStream_t stream) {
         if (e != hipSuccess) return e;
     }
     const ShortPlan pl = short_plan(c, b, a.heads, a.workspace_bytes);
-    hipError_t e = launch(k_attention_short<D>, dim3((uint32_t)((int64_t)pl.slots * pl.tiles * c.kv_heads)), dim3(64 * kShortWaves), stream, a, pl, sc);
+    const int64_t items = (int64_t)pl.slots * c.kv_heads;
+    const hipError_t e = launch(k_attention_short<D>, dim3((uint32_t)(items < kResident ? items : kResident)), dim3(64 * kShortWaves), stream, a, pl, sc);
     if (e != hipSuccess || pl.target == 0) return e;
-    return launch(k_attention_join<D>, dim3((uint32_t)((int64_t)b.sequences * pl.rows * c.kv_heads)), dim3(D), stream, a, pl);
+    const int each = b.cu ? 1 : group;
+    return launch(k_attention_join<D>, dim3((uint32_t)((int64_t)b.sequences * each * c.kv_heads)), dim3(256), stream, a, pl, each);
 }
 
 }  // namespace
 
 int64_t kv_attention_workspace_bytes(const KvCacheArgs& c, const KvBatchArgs& b, int heads) {
     const ShortPlan pl = short_plan(c, b, heads, (int64_t)1 << 60);
-    return pl.target == 0 ? 0 : pl.slots * slot_bytes(c, pl.rows);
+    return pl.target == 0 ? 0 : pl.slots * slot_bytes(c);
 }
 
 bool kv_attention_fits(const KvAttentionArgs& a) {
@@ -1029,8 +1098,7 @@ bool kv_attention_fits(const KvAttentionArgs& a) {
     if ((int64_t)b.tokens * (a.heads / c.kv_heads) >= ((int64_t)1 << 31) - kLongRows) return false;
     const int64_t tiles = b.cu ? kv_items(b, a.heads / c.kv_heads, 8, 1) : 0;
     return tiles * c.kv_heads <= most / (64 * kLongWaves) &&
-           (int64_t)pl.slots * pl.tiles * c.kv_heads <= most / (64 * kShortWaves) &&
-           (int64_t)b.sequences * pl.rows * c.kv_heads <= most / c.dim;
+           (int64_t)pl.slots * c.kv_heads < (int64_t)1 << 31 && (int64_t)b.sequences * a.heads <= most / 256;
 }
 
 hipError_t launch_kv_attention(const KvAttentionArgs& a, hipStream_t stream) {
