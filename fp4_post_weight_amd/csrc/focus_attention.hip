@@ -104,11 +104,11 @@ __device__ __forceinline__ void turn8(float (&lo)[8], float (&hi)[8], const Rope
     }
 }
 
-__device__ __forceinline__ void load8(const uint16_t* p, float (&f)[8]) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
     f[0] = bf16_lo(v.x), f[1] = bf16_hi(v.x), f[2] = bf16_lo(v.y), f[3] = bf16_hi(v.y);
     f[4] = bf16_lo(v.z), f[5] = bf16_hi(v.z), f[6] = bf16_lo(v.w), f[7] = bf16_hi(v.w);
 }
+__device__ __forceinline__ void load8(const uint16_t* p, float (&f)[8]) { unpack8(*reinterpret_cast<const uint4*>(p), f); }
 
 // The exponent that brings a row of largest magnitude amax to 2^14..2^15.
 __device__ __forceinline__ int query_shift(float amax) {
@@ -160,26 +160,34 @@ inline Scoring scoring(const KvAttentionArgs& a) {
 // few rows per sequence: split over the keys
 // ---------------------------------------------------------------------------
 //
-// The keys of all sequences are cut into chunks of equal length, so many that
-// they fill the GPU, and a workgroup takes one chunk of one head and of 16 of
-// the sequence's rows at a time.  The lengths are device memory: every
-// workgroup adds them up, derives the chunk length and finds its own.  A
-// sequence of several chunks leaves unnormalised sums, and their maximum, in
-// the workspace, and a second kernel joins them in order.
+// A sequence's rows are taken 16 at a time (a tile).  Where the tiles' keys are
+// many, they are cut, one tile after the other, into ranges of equal length, one
+// for each workgroup of a head that the GPU holds at once, so that all of them
+// end together whatever the sequences' lengths; a workgroup goes through the
+// pieces of the tiles in its range.  Where they are few, a workgroup takes a
+// tile's piece of at most the least length, which a range of several tiles would
+// take one after the other.  The lengths are device memory: every workgroup adds
+// them up and finds its own.  A tile of several pieces leaves unnormalised sums,
+// and their maximum, in the workspace, and a second kernel joins them in order.
+// (Measured, us: 64 sequences up to 16384 with chunks of equal length handed out
+// in turn 251, with ranges 240; 40 up to 2000 with ranges 29, with pieces 18.)
 
 struct ShortPlan {
-    int64_t target;  // items per head to aim at; 0: one chunk per sequence
-    int slots;       // items per head, at most
-    int unit;        // keys that a chunk is a multiple of
+    int ranges;  // per head; 0: no split, tiles are handed out in turn
+    int slots;   // pieces per head, at most
 };
 
-constexpr int kNoPage = 1 << 16;  // in the place of a page's exponent
-constexpr int kShortStep = 64;    // keys of a wavefront's step
+constexpr int kShortStep = 64;    // keys of a wavefront's step, the unit of the lengths here
+
+// Steps that a range is a multiple of, and the least: shorter ones cost more in
+// the join (4 us) than they save.
+constexpr int kRangeUnit = 4, kLeastRange = 20;
 
 struct ShortSequence {
     KvSequence s;
     int begin, end;  // keys that some row sees, begin a multiple of 64
-    int tiles;       // of 16 rows; 0: no rows, or too many
+    int tiles;       // 0: no rows, or too many
+    __device__ __forceinline__ int span() const { return max((end - begin + kShortStep - 1) / kShortStep, 1); }  // steps
 };
 
 __device__ __forceinline__ bool is_short(int rows, int group) { return rows == 1 || (int64_t)rows * group <= kShortRows; }
@@ -196,84 +204,98 @@ __device__ __forceinline__ ShortSequence short_sequence(const KvAttentionArgs& a
     return q;
 }
 
-__device__ __forceinline__ int chunks_of(int keys, int64_t chunk) { return keys > 0 ? (int)((keys + chunk - 1) / chunk) : 1; }
+// What a tile counts: one, its steps, or its pieces of the least length.
+enum Count { kTiles, kSteps, kPieces };
 
-__device__ __forceinline__ int64_t chunk_length(const KvAttentionArgs& a, const ShortPlan& pl, int group) {
-    if (pl.target == 0) return (int64_t)1 << 31;
-    const int lane = threadIdx.x & 63;
-    int64_t keys = 0;
-    for (int base = 0; base < a.batch.sequences; base += 64)
-        if (base + lane < a.batch.sequences) {
-            const ShortSequence q = short_sequence(a, group, base + lane);
-            keys += (int64_t)(q.end - q.begin) * q.tiles;
-        }
-#pragma unroll
-    for (int m = 1; m < 64; m *= 2) keys += __shfl_xor(keys, m);
-    const int64_t each = (keys + pl.target - 1) / pl.target;
-    return max((each + pl.unit - 1) / pl.unit, (int64_t)1) * pl.unit;
+__device__ __forceinline__ int weight(const ShortSequence& q, Count of) {
+    return of == kTiles ? 1 : of == kSteps ? q.span() : (q.span() + kLeastRange - 1) / kLeastRange;
 }
 
-// Item `first + number * tiles + tile` of a head is chunk `number` of a
-// sequence's 16-row tile.
-struct Share {
-    int seq, tile, number, count;
+// Of the sequences before `seq`; the host has seen to it that 32 bits hold it.
+struct Sum {
+    int weight, tiles;
 };
 
-__device__ __forceinline__ bool find_share(const KvAttentionArgs& a, int group, int64_t chunk, int item, Share& out) {
+__device__ __forceinline__ Sum sum_before(const KvAttentionArgs& a, int group, Count of, int seq) {
     const int lane = threadIdx.x & 63;
-    int before = 0;
+    Sum n = {0, 0};
+    for (int base = 0; base < seq; base += 64)
+        if (base + lane < seq) {
+            const ShortSequence q = short_sequence(a, group, base + lane);
+            n.weight += weight(q, of) * q.tiles;
+            n.tiles += q.tiles;
+        }
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) {
+        n.weight += __shfl_xor(n.weight, m);
+        n.tiles += __shfl_xor(n.tiles, m);
+    }
+    return n;
+}
+
+// Steps of a range, or 0 where pieces are taken instead.
+__device__ __forceinline__ int range_length(const KvAttentionArgs& a, const ShortPlan& pl, int group) {
+    const int steps = sum_before(a, group, kSteps, a.batch.sequences).weight;
+    const int each = (steps + pl.ranges - 1) / pl.ranges;
+    return each > kLeastRange ? (each + kRangeUnit - 1) / kRangeUnit * kRangeUnit : 0;
+}
+
+// The tile that holds a place in the row of all tiles, its number, its weight
+// and the place within it.
+struct Tile {
+    int seq, tile, number, weight, rest;
+};
+
+__device__ __forceinline__ bool find_tile(const KvAttentionArgs& a, int group, Count of, int place, Tile& out) {
+    const int lane = threadIdx.x & 63;
+    int before = 0, tiles_before = 0;
     for (int base = 0; base < a.batch.sequences; base += 64) {
-        int tiles = 0, count = 0;
+        int tiles = 0, w = 1;
         if (base + lane < a.batch.sequences) {
             const ShortSequence q = short_sequence(a, group, base + lane);
             tiles = q.tiles;
-            count = chunks_of(q.end - q.begin, chunk);
+            w = weight(q, of);
         }
-        int upto = tiles * count;
+        int upto = tiles * w, tiles_upto = tiles;
 #pragma unroll
         for (int m = 1; m < 64; m *= 2) {
-            const int n = __shfl_up(upto, m);
-            if (lane >= m) upto += n;
+            const int n = __shfl_up(upto, m), k = __shfl_up(tiles_upto, m);
+            upto += lane >= m ? n : 0;
+            tiles_upto += lane >= m ? k : 0;
         }
-        const uint64_t past = __ballot(item < before + upto);
+        const uint64_t past = __ballot(place < before + upto);
         if (past) {
             const int at = __builtin_ctzll(past);
             out.seq = base + at;
-            out.count = __builtin_amdgcn_readlane(count, at);
-            tiles = __builtin_amdgcn_readlane(tiles, at);
-            const int k = item - (before + __builtin_amdgcn_readlane(upto, at) - out.count * tiles);
-            out.number = k / tiles;
-            out.tile = k - out.number * tiles;
+            out.weight = __builtin_amdgcn_readlane(w, at);
+            const int rel = place - (before + __builtin_amdgcn_readlane(upto - tiles * w, at));
+            out.tile = rel / out.weight;
+            out.rest = rel - out.tile * out.weight;
+            out.number = tiles_before + __builtin_amdgcn_readlane(tiles_upto - tiles, at) + out.tile;
             return true;
         }
         before += __builtin_amdgcn_readlane(upto, 63);
+        tiles_before += __builtin_amdgcn_readlane(tiles_upto, 63);
     }
     return false;
 }
 
-// Items of the sequences before one.
-__device__ __forceinline__ int items_before(const KvAttentionArgs& a, int group, int64_t chunk, int seq) {
-    const int lane = threadIdx.x & 63;
-    int n = 0;
-    for (int base = 0; base < seq; base += 64)
-        if (base + lane < seq) {
-            const ShortSequence q = short_sequence(a, group, base + lane);
-            n += q.tiles * chunks_of(q.end - q.begin, chunk);
-        }
-#pragma unroll
-    for (int m = 1; m < 64; m *= 2) n += __shfl_xor(n, m);
-    return n;
+// Workspace: per slot, head and row of 16 the sums [dim], then per slot, head
+// and row the maximum (base 2) and the sum of the probabilities.  The piece of
+// tile i in range k has slot i + k: going from piece to piece one of them grows.
+// Pieces of the least length have their number.
+__device__ __forceinline__ float* part_at(const KvAttentionArgs& a, int slot, int head, int row) {
+    return a.workspace + (((int64_t)slot * a.cache.kv_heads + head) * 16 + row) * a.cache.dim;
+}
+__device__ __forceinline__ float2* part_stat(const KvAttentionArgs& a, int slots, int slot, int head, int row) {
+    float* p = a.workspace + (int64_t)slots * a.cache.kv_heads * 16 * a.cache.dim;
+    return reinterpret_cast<float2*>(p) + ((int64_t)slot * a.cache.kv_heads + head) * 16 + row;
 }
 
-// Workspace: per item, head and row of 16 the sums [dim], then per item, head
-// and row the maximum (base 2) and the sum of the probabilities.
-__device__ __forceinline__ float* part_at(const KvAttentionArgs& a, int item, int head, int row) {
-    return a.workspace + (((int64_t)item * a.cache.kv_heads + head) * 16 + row) * a.cache.dim;
-}
-__device__ __forceinline__ float2* part_stat(const KvAttentionArgs& a, int slots, int item, int head, int row) {
-    float* p = a.workspace + (int64_t)slots * a.cache.kv_heads * 16 * a.cache.dim;
-    return reinterpret_cast<float2*>(p) + ((int64_t)item * a.cache.kv_heads + head) * 16 + row;
-}
+// A piece of a tile: its steps from .. from + length - 1, slot -1: all of them.
+struct Piece {
+    int seq, tile, slot, from, length;
+};
 
 // What a row's sum becomes: no key (zeros), keys that have no page (NaN).
 __device__ __forceinline__ float row_result(float sum, float total, int64_t pos, int64_t room) {
@@ -288,10 +310,10 @@ struct ShortLds {
     float2 stat[WAVES][16];
 };
 
-// One item of WAVES wavefronts.
+// One piece, by WAVES wavefronts.
 template <int D, int WAVES>
-__device__ __forceinline__ void short_item(const KvAttentionArgs& a, const ShortPlan& pl, const Scoring& sc, const Share& sh,
-                                           int64_t chunk, int item, int head, ShortLds<D, WAVES>& lds) {
+__device__ __forceinline__ void short_piece(const KvAttentionArgs& a, const ShortPlan& pl, const Scoring& sc, const Piece& sh,
+                                            int head, ShortLds<D, WAVES>& lds) {
     constexpr int kQ = D / 32;       // products per 16 tokens
     constexpr int kV = D / 16;       // tiles of the result
     constexpr int kOutRow = ShortLds<D, WAVES>::kRow, kStride = WAVES * kShortStep;
@@ -310,8 +332,8 @@ __device__ __forceinline__ void short_item(const KvAttentionArgs& a, const Short
     const int pos_lo = first + 16 * sh.tile / group, pos_hi = first + min(16 * sh.tile + 15, rows - 1) / group;
 
     const int jlo = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
-    const int begin = (int)min((int64_t)sq.begin + sh.number * chunk, (int64_t)sq.end);
-    const int end = (int)min((int64_t)sq.end, (int64_t)begin + chunk);
+    const int begin = min(sq.begin + sh.from * kShortStep, sq.end);
+    const int end = min(sq.end, begin + sh.length * kShortStep);
     const int jhi = min(pos, end - 1);
     // keys that every row of the tile sees, and that any sees
     const int all_lo = a.window > 0 ? max(pos_hi - a.window + 1, 0) : 0, all_hi = min(pos_lo, end - 1);
@@ -356,38 +378,55 @@ __device__ __forceinline__ void short_item(const KvAttentionArgs& a, const Short
     for (int i = 0; i < kV; ++i) acc[i] = (f32x4){};
     float m = -__builtin_inff(), l = 0.0f;
 
+    // Loads that wait for nothing first: the table's entries, the query and its angles.
     int t = begin + kShortStep * wave;
-    int ke = 0, ve = 0;  // entries of the next step
+    int k0 = 0, v0 = 0, ke = 0, ve = 0;  // entries of this step and the next
     if (t < end) {
-        const int k0 = entry_of(t + kgroup), v0 = entry_of(t + 16 * c);
+        k0 = entry_of(t + kgroup);
+        v0 = entry_of(t + 16 * c);
         ke = entry_of(t + kStride + kgroup);
         ve = entry_of(t + kStride + 16 * c);
-        load_k(t, k0);
-        load_s(v0);
-        load_v(t, v0);
     }
     f16x8 q[kQ];
     int shift;
     {
         const uint16_t* qp = a.q + (int64_t)(sq.s.row0 + token) * a.q_stride + (int64_t)(head * group + member) * D + c * (D / 4);
         float f[kQ][8];
+        uint4 raw[kQ];
 #pragma unroll
-        for (int k = 0; k < kQ; ++k) load8(qp + 8 * k, f[k]);
+        for (int k = 0; k < kQ; ++k) raw[k] = *reinterpret_cast<const uint4*>(qp + 8 * k);
+        float4 cs[kQ][2], sn[kQ][2];
+        const int place = first + token;
+        const bool known = place >= 0 && place < a.rope.positions;
         if (a.rope.table) {
-            // lanes 32 apart hold a pair's halves
-            const int d = (c & 1) * (D / 4);
+            const float* angle = a.rope.table + (known ? (int64_t)place * D : 0) + (c & 1) * (D / 4);
+#pragma unroll
+            for (int k = 0; k < kQ; ++k)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    cs[k][i] = *reinterpret_cast<const float4*>(angle + 8 * k + 4 * i);
+                    sn[k][i] = *reinterpret_cast<const float4*>(angle + D / 2 + 8 * k + 4 * i);
+                }
+        }
+        if (t < end) {
+            load_k(t, k0);
+            load_s(v0);
+            load_v(t, v0);
+        }
+#pragma unroll
+        for (int k = 0; k < kQ; ++k) unpack8(raw[k], f[k]);
+        if (a.rope.table) {
+            // lanes 32 apart hold a pair's halves: a c - b s on the first, b c + a s on the second
 #pragma unroll
             for (int k = 0; k < kQ; ++k) {
-                float lo[8], hi[8];
+                const float co[8] = {cs[k][0].x, cs[k][0].y, cs[k][0].z, cs[k][0].w, cs[k][1].x, cs[k][1].y, cs[k][1].z, cs[k][1].w};
+                const float si[8] = {sn[k][0].x, sn[k][0].y, sn[k][0].z, sn[k][0].w, sn[k][1].x, sn[k][1].y, sn[k][1].z, sn[k][1].w};
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float other = __shfl_xor(f[k][i], 32);
-                    lo[i] = c < 2 ? f[k][i] : other;
-                    hi[i] = c < 2 ? other : f[k][i];
+                    const float mine = f[k][i] * co[i], other = __shfl_xor(f[k][i], 32) * si[i];
+                    const float turned = c < 2 ? mine - other : mine + other;
+                    f[k][i] = known ? turned : __builtin_nanf("");
                 }
-                turn8(lo, hi, a.rope, D, first + token, d + 8 * k);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) f[k][i] = c < 2 ? lo[i] : hi[i];
             }
         }
         float amax = 0.0f;
@@ -396,7 +435,7 @@ __device__ __forceinline__ void short_item(const KvAttentionArgs& a, const Short
 #pragma unroll
             for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[k][i]));
         amax = fmaxf(amax, __shfl_xor(amax, 16));
-        amax = fmaxf(amax, __shfl_xor(amax, 32));
+        amax = max_halves(amax);
         shift = query_shift(amax);
 #pragma unroll
         for (int k = 0; k < kQ; ++k) q[k] = narrow(f[k], shift, sc.sign);
@@ -474,17 +513,19 @@ __device__ __forceinline__ void short_item(const KvAttentionArgs& a, const Short
         bool odd = false;
         if (!whole) {
             // values of tokens that no row sees are whatever the page holds
+            uint32_t keep[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int j = t + 16 * c + 4 * k;
+                keep[k] = here ? first_bytes(any_hi + 1 - j) & ~first_bytes(any_lo - j) : 0u;
+            }
 #pragma unroll
             for (int i = 0; i < kV; ++i) {
-                uint32_t w[4] = {vb[i].x, vb[i].y, vb[i].z, vb[i].w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int j = t + 16 * c + 4 * k;
-                    w[k] &= first_bytes(any_hi + 1 - j) & ~first_bytes(any_lo - j);
-                    w[k] = here ? w[k] : 0u;
-                    odd = odd || nan_bytes(w[k]) != 0;
-                }
-                vb[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                vb[i].x &= keep[0];
+                vb[i].y &= keep[1];
+                vb[i].z &= keep[2];
+                vb[i].w &= keep[3];
+                odd = odd || any_nan(vb[i].x, vb[i].y, vb[i].z, vb[i].w);
             }
         }
         if (!whole && __any(odd)) {
@@ -550,7 +591,7 @@ __device__ __forceinline__ void short_item(const KvAttentionArgs& a, const Short
             total += f * lds.stat[w][row].y;
             o += f * *reinterpret_cast<const f32x4*>(&lds.out[w][row * kOutRow + d]);
         }
-        if (sh.count == 1) {
+        if (sh.slot < 0) {
             const int tok = rr / group, mem = rr - tok * group;
             const int64_t p = (int64_t)first + tok;
             uint2 v;
@@ -558,24 +599,44 @@ __device__ __forceinline__ void short_item(const KvAttentionArgs& a, const Short
             v.y = bf16_pair(row_result(o[2], total, p, room), row_result(o[3], total, p, room));
             *reinterpret_cast<uint2*>(a.y + ((int64_t)(sq.s.row0 + tok) * a.heads + head * group + mem) * D + d) = v;
         } else {
-            *reinterpret_cast<f32x4*>(part_at(a, item, head, row) + d) = o;
-            if (d == 0) *part_stat(a, pl.slots, item, head, row) = make_float2(mx, total);
+            *reinterpret_cast<f32x4*>(part_at(a, sh.slot, head, row) + d) = o;
+            if (d == 0) *part_stat(a, pl.slots, sh.slot, head, row) = make_float2(mx, total);
         }
     }
 }
 
-// The items from `w` on, `stride` apart, of all heads.
+// The pieces of range w / kv_heads of a head, or every stride-th piece or tile
+// of all heads.
 template <int D, int WAVES>
-__device__ __forceinline__ void short_items(const KvAttentionArgs& a, const ShortPlan& pl, const Scoring& sc, int w, int stride,
-                                            ShortLds<D, WAVES>& lds) {
+__device__ __forceinline__ void short_pieces(const KvAttentionArgs& a, const ShortPlan& pl, const Scoring& sc, int w, int stride,
+                                             ShortLds<D, WAVES>& lds) {
     const int kvh = a.cache.kv_heads, group = a.heads / kvh;
-    const int64_t chunk = chunk_length(a, pl, group);
-    for (;; w += stride) {
-        const int head = w % kvh, item = w / kvh;
-        Share sh;
-        if (item >= pl.slots || !find_share(a, group, chunk, item, sh)) return;
-        short_item<D, WAVES>(a, pl, sc, sh, chunk, item, head, lds);
-        __syncthreads();  // the next item writes where this one has read
+    const int length = pl.ranges > 0 ? range_length(a, pl, group) : 0;
+    const Count of = length > 0 ? kSteps : pl.ranges > 0 ? kPieces : kTiles;
+    int range = w / kvh, place = length > 0 ? range * length : range;
+    const int head = w % kvh, stop = place + length;
+    for (;;) {
+        Tile t;
+        if (!find_tile(a, group, of, place, t)) return;
+        Piece p = {t.seq, t.tile, -1, 0, 1 << 24};
+        if (length > 0) {
+            p.from = t.rest;
+            p.length = min(t.weight - t.rest, stop - place);
+            if (p.length < t.weight) p.slot = t.number + range;
+            place += p.length;
+        } else if (of == kPieces && t.weight > 1) {
+            p.from = t.rest * kLeastRange;
+            p.length = kLeastRange;
+            p.slot = place;
+        }
+        short_piece<D, WAVES>(a, pl, sc, p, length > 0 ? head : w % kvh, lds);
+        if (length > 0) {
+            if (place >= stop) return;
+        } else {
+            w += stride;
+            place = w / kvh;
+        }
+        __syncthreads();  // the next piece writes where this one has read
     }
 }
 
@@ -584,11 +645,11 @@ constexpr int kShortWaves = 4;
 template <int D>
 __global__ __launch_bounds__(64 * kShortWaves, 2) void k_attention_short(KvAttentionArgs a, ShortPlan pl, Scoring sc) {
     __shared__ ShortLds<D, kShortWaves> lds;
-    short_items<D, kShortWaves>(a, pl, sc, (int)blockIdx.x, (int)gridDim.x, lds);
+    short_pieces<D, kShortWaves>(a, pl, sc, (int)blockIdx.x, (int)gridDim.x, lds);
 }
 
-// A workgroup joins the chunks of rows of one sequence and head, in order:
-// `each` workgroups share a sequence's rows, four wavefronts the chunks.
+// A workgroup joins the pieces of rows of one sequence and head, in order:
+// `each` workgroups share a sequence's rows, four wavefronts the pieces.
 template <int D>
 __global__ __launch_bounds__(256) void k_attention_join(KvAttentionArgs a, ShortPlan pl, int each) {
     constexpr int kPer = D / 64;  // elements of a lane
@@ -598,25 +659,32 @@ __global__ __launch_bounds__(256) void k_attention_join(KvAttentionArgs a, Short
     const int head = (int)(blockIdx.x % (uint32_t)kvh), seq = (int)(blockIdx.x / (uint32_t)kvh / (uint32_t)each);
     const ShortSequence sq = short_sequence(a, group, seq);
     if (sq.tiles == 0) return;
-    const int64_t chunk = chunk_length(a, pl, group);
-    const int count = chunks_of(sq.end - sq.begin, chunk);
-    if (count == 1) return;
-    const int first = items_before(a, group, chunk, seq);
+    const int length = range_length(a, pl, group);
+    const Sum before = sum_before(a, group, length > 0 ? kSteps : kPieces, seq);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int row = (int)(blockIdx.x / (uint32_t)kvh % (uint32_t)each); row < sq.s.rows * group; row += each) {
-        const int item0 = first + row / 16, r = row % 16;
+        const int tile = row / 16, r = row % 16;
+        int slot0, count;
+        if (length > 0) {
+            const int start = before.weight + tile * sq.span(), first = start / length;
+            count = (start + sq.span() - 1) / length - first + 1;
+            slot0 = before.tiles + tile + first;
+        } else {
+            count = weight(sq, kPieces);
+            slot0 = before.weight + tile * count;
+        }
+        if (count == 1) continue;
         float mx = -__builtin_inff();
-        for (int i = lane; i < count; i += 64) mx = fmaxf(mx, part_stat(a, pl.slots, item0 + i * sq.tiles, head, r)->x);
+        for (int i = lane; i < count; i += 64) mx = fmaxf(mx, part_stat(a, pl.slots, slot0 + i, head, r)->x);
 #pragma unroll
         for (int k = 1; k < 64; k *= 2) mx = fmaxf(mx, __shfl_xor(mx, k));
         float total = 0.0f, o[kPer] = {};
 #pragma unroll 4
         for (int i = wave; i < count; i += 4) {
-            const int item = item0 + i * sq.tiles;
-            const float2 st = *part_stat(a, pl.slots, item, head, r);
+            const float2 st = *part_stat(a, pl.slots, slot0 + i, head, r);
             const float f = mx == -__builtin_inff() ? 0.0f : exp2_hw(st.x - mx);
             total += f * st.y;
-            const float* p = part_at(a, item, head, r) + kPer * lane;
+            const float* p = part_at(a, slot0 + i, head, r) + kPer * lane;
 #pragma unroll
             for (int k = 0; k < kPer; ++k) o[k] += f * p[k];
         }
@@ -1033,12 +1101,10 @@ __global__ __launch_bounds__(64 * kLongWaves) void k_attention_long(KvAttentionA
 // launches
 // ---------------------------------------------------------------------------
 
-// Workgroups that the GPU holds at once (four wavefronts each, two per compute
-// unit), and items to aim at: twice as many, so that chunks of unequal length
-// even out.
-constexpr int kResident = 512, kFill = 1024;
+// Workgroups that the GPU holds at once: four wavefronts each, two per compute unit.
+constexpr int kResident = 512;
 
-// Workspace bytes per item of all heads.
+// Workspace bytes per slot of all heads.
 int64_t slot_bytes(const KvCacheArgs& c) { return (int64_t)c.kv_heads * 16 * (c.dim + 2) * 4; }
 
 // 16-row tiles of all sequences, at most.
@@ -1048,16 +1114,19 @@ int64_t short_tiles(const KvBatchArgs& b, int group) {
     return by_rows < b.sequences * most ? by_rows : b.sequences * most;
 }
 
-ShortPlan short_plan(const KvCacheArgs& c, const KvBatchArgs& b, int heads, int64_t workspace_bytes) {
+ShortPlan short_plan(const KvCacheArgs& c, const KvBatchArgs& b, int heads, int window, int64_t workspace_bytes) {
     ShortPlan pl;
-    pl.unit = kShortWaves * kShortStep;
     const int64_t tiles = short_tiles(b, heads / c.kv_heads);
-    // no sequence is longer than a chunk of the least length: nothing to split
-    const bool splits = ((int64_t)b.max_pages << c.log_page) > pl.unit;
-    const int64_t fit = workspace_bytes / slot_bytes(c) - tiles, want = (kFill + c.kv_heads - 1) / c.kv_heads;
-    pl.target = splits ? (fit < want ? fit : want) : 0;
-    if (pl.target < 1) pl.target = 0;
-    pl.slots = (int)(pl.target + tiles);
+    // nothing to split where no sequence has more keys to see than the least range
+    int64_t keys = (int64_t)b.max_pages << c.log_page;
+    const int64_t seen = (int64_t)window + kShortStep + (b.cu ? kShortRows : 1);
+    if (window > 0 && seen < keys) keys = seen;
+    const int64_t fit = workspace_bytes / slot_bytes(c) - tiles, want = (kResident + c.kv_heads - 1) / c.kv_heads;
+    const int64_t ranges = fit < want ? fit : want;
+    // the steps of all tiles are counted in 32 bits
+    const int64_t steps = (keys + kShortStep - 1) / kShortStep + 1;
+    pl.ranges = keys > kLeastRange * kShortStep && ranges > 0 && tiles * steps < (int64_t)1 << 30 ? (int)ranges : 0;
+    pl.slots = (int)(pl.ranges + tiles);
     return pl;
 }
 
@@ -1074,10 +1143,12 @@ hipError_t launch_attention(const KvAttentionArgs& a, hipStream_t stream) {
                                     dim3((uint32_t)(pl.slots * c.kv_heads)), dim3(64 * kLongWaves), stream, a, pl, sc);
         if (e != hipSuccess) return e;
     }
-    const ShortPlan pl = short_plan(c, b, a.heads, a.workspace_bytes);
-    const int64_t items = (int64_t)pl.slots * c.kv_heads;
-    const hipError_t e = launch(k_attention_short<D>, dim3((uint32_t)(items < kResident ? items : kResident)), dim3(64 * kShortWaves), stream, a, pl, sc);
-    if (e != hipSuccess || pl.target == 0) return e;
+    const ShortPlan pl = short_plan(c, b, a.heads, a.window, a.workspace_bytes);
+    const int64_t tiles = (int64_t)pl.slots * c.kv_heads;
+    // a range for each workgroup, or pieces and tiles in turn
+    const uint32_t grid = pl.ranges > 0 ? (uint32_t)(pl.ranges * c.kv_heads) : (uint32_t)(tiles < 2 * kResident ? tiles : 2 * kResident);
+    const hipError_t e = launch(k_attention_short<D>, dim3(grid), dim3(64 * kShortWaves), stream, a, pl, sc);
+    if (e != hipSuccess || pl.ranges == 0) return e;
     const int each = b.cu ? 1 : group;
     return launch(k_attention_join<D>, dim3((uint32_t)((int64_t)b.sequences * each * c.kv_heads)), dim3(256), stream, a, pl, each);
 }
@@ -1085,15 +1156,15 @@ hipError_t launch_attention(const KvAttentionArgs& a, hipStream_t stream) {
 }  // namespace
 
 int64_t kv_attention_workspace_bytes(const KvCacheArgs& c, const KvBatchArgs& b, int heads) {
-    const ShortPlan pl = short_plan(c, b, heads, (int64_t)1 << 60);
-    return pl.target == 0 ? 0 : pl.slots * slot_bytes(c);
+    const ShortPlan pl = short_plan(c, b, heads, 0, (int64_t)1 << 60);
+    return pl.ranges == 0 ? 0 : pl.slots * slot_bytes(c);
 }
 
 bool kv_attention_fits(const KvAttentionArgs& a) {
     const KvCacheArgs& c = a.cache;
     const KvBatchArgs& b = a.batch;
     const int64_t most = 0xFFFFFFFFll;
-    const ShortPlan pl = short_plan(c, b, a.heads, a.workspace_bytes);
+    const ShortPlan pl = short_plan(c, b, a.heads, a.window, a.workspace_bytes);
     // rows of a sequence are counted in 32 bits
     if ((int64_t)b.tokens * (a.heads / c.kv_heads) >= ((int64_t)1 << 31) - kLongRows) return false;
     const int64_t tiles = b.cu ? kv_items(b, a.heads / c.kv_heads, 8, 1) : 0;
