@@ -72,7 +72,8 @@ __device__ __forceinline__ bool any_nan(uint32_t a, uint32_t b, uint32_t c, uint
     return ((((a & m) + o) | ((b & m) + o) | ((c & m) + o) | ((d & m) + o)) & 0x80808080u) != 0;
 }
 
-// The larger of a lane's value and that of the lane 32 from it.
+// The larger of a lane's value and that of the lane 32 from it (the exchange of
+// a register with itself gives the lower lanes' values and the upper ones').
 __device__ __forceinline__ float max_halves(float x) {
     const u32x2 r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
     return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
@@ -175,13 +176,15 @@ inline Scoring scoring(const KvAttentionArgs& a) {
 struct ShortPlan {
     int ranges;  // per head; 0: no split, tiles are handed out in turn
     int slots;   // pieces per head, at most
+    int waves;   // of a workgroup
+    int resident;  // workgroups that the GPU holds at once
 };
 
 constexpr int kShortStep = 64;    // keys of a wavefront's step, the unit of the lengths here
 
 // Steps that a range is a multiple of, and the least: shorter ones cost more in
 // the join (4 us) than they save.
-constexpr int kRangeUnit = 4, kLeastRange = 20;
+constexpr int kRangeUnit = 8, kLeastRange = 24;
 
 struct ShortSequence {
     KvSequence s;
@@ -423,7 +426,8 @@ __device__ __forceinline__ void short_piece(const KvAttentionArgs& a, const Shor
                 const float si[8] = {sn[k][0].x, sn[k][0].y, sn[k][0].z, sn[k][0].w, sn[k][1].x, sn[k][1].y, sn[k][1].z, sn[k][1].w};
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float mine = f[k][i] * co[i], other = __shfl_xor(f[k][i], 32) * si[i];
+                    const u32x2 both = __builtin_amdgcn_permlane32_swap(__float_as_uint(f[k][i]), __float_as_uint(f[k][i]), false, false);
+                    const float mine = f[k][i] * co[i], other = __uint_as_float(c < 2 ? both[1] : both[0]) * si[i];
                     const float turned = c < 2 ? mine - other : mine + other;
                     f[k][i] = known ? turned : __builtin_nanf("");
                 }
@@ -640,12 +644,10 @@ __device__ __forceinline__ void short_pieces(const KvAttentionArgs& a, const Sho
     }
 }
 
-constexpr int kShortWaves = 4;
-
-template <int D>
-__global__ __launch_bounds__(64 * kShortWaves, 2) void k_attention_short(KvAttentionArgs a, ShortPlan pl, Scoring sc) {
-    __shared__ ShortLds<D, kShortWaves> lds;
-    short_pieces<D, kShortWaves>(a, pl, sc, (int)blockIdx.x, (int)gridDim.x, lds);
+template <int D, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void k_attention_short(KvAttentionArgs a, ShortPlan pl, Scoring sc) {
+    __shared__ ShortLds<D, WAVES> lds;
+    short_pieces<D, WAVES>(a, pl, sc, (int)blockIdx.x, (int)gridDim.x, lds);
 }
 
 // A workgroup joins the pieces of rows of one sequence and head, in order:
@@ -654,7 +656,7 @@ template <int D>
 __global__ __launch_bounds__(256) void k_attention_join(KvAttentionArgs a, ShortPlan pl, int each) {
     constexpr int kPer = D / 64;  // elements of a lane
     __shared__ float part[4][D];
-    __shared__ float sums[4];
+    __shared__ float2 sums[4];
     const int kvh = a.cache.kv_heads, group = a.heads / kvh;
     const int head = (int)(blockIdx.x % (uint32_t)kvh), seq = (int)(blockIdx.x / (uint32_t)kvh / (uint32_t)each);
     const ShortSequence sq = short_sequence(a, group, seq);
@@ -674,29 +676,55 @@ __global__ __launch_bounds__(256) void k_attention_join(KvAttentionArgs a, Short
             slot0 = before.weight + tile * count;
         }
         if (count == 1) continue;
-        float mx = -__builtin_inff();
-        for (int i = lane; i < count; i += 64) mx = fmaxf(mx, part_stat(a, pl.slots, slot0 + i, head, r)->x);
+        // eight pieces at a time, so that their loads are in flight together
+        constexpr int kBatch = 8;
+        float m = -__builtin_inff(), total = 0.0f, o[kPer] = {};
+        for (int i = wave; i < count; i += 4 * kBatch) {
+            float2 st[kBatch];
+            float p[kBatch][kPer];
 #pragma unroll
-        for (int k = 1; k < 64; k *= 2) mx = fmaxf(mx, __shfl_xor(mx, k));
-        float total = 0.0f, o[kPer] = {};
-#pragma unroll 4
-        for (int i = wave; i < count; i += 4) {
-            const float2 st = *part_stat(a, pl.slots, slot0 + i, head, r);
-            const float f = mx == -__builtin_inff() ? 0.0f : exp2_hw(st.x - mx);
-            total += f * st.y;
-            const float* p = part_at(a, slot0 + i, head, r) + kPer * lane;
+            for (int n = 0; n < kBatch; ++n) {
+                const int slot = slot0 + min(i + 4 * n, count - 1);
+                st[n] = *part_stat(a, pl.slots, slot, head, r);
+                const float* from = part_at(a, slot, head, r) + kPer * lane;
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) o[k] += f * p[k];
+                for (int k = 0; k < kPer; ++k) p[n][k] = from[k];
+                if (i + 4 * n >= count) st[n] = make_float2(-__builtin_inff(), 0.0f);
+            }
+            float mn = m;
+#pragma unroll
+            for (int n = 0; n < kBatch; ++n) mn = fmaxf(mn, st[n].x);
+            const float keep = m == -__builtin_inff() ? (total == 0.0f ? 0.0f : 1.0f) : exp2_hw(m - mn);
+            total *= keep;
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) o[k] *= keep;
+            m = mn;
+#pragma unroll
+            for (int n = 0; n < kBatch; ++n) {
+                if (i + 4 * n >= count) break;
+                const float f = mn == -__builtin_inff() ? 0.0f : exp2_hw(st[n].x - mn);
+                total += f * st[n].y;
+#pragma unroll
+                for (int k = 0; k < kPer; ++k) o[k] += f * p[n][k];
+            }
         }
 #pragma unroll
         for (int k = 0; k < kPer; ++k) part[wave][kPer * lane + k] = o[k];
-        if (lane == 0) sums[wave] = total;
+        if (lane == 0) sums[wave] = make_float2(m, total);
         __syncthreads();
         if (threadIdx.x < D) {
             const int d = threadIdx.x, token = row / group, member = row - token * group;
-            const float sum = (part[0][d] + part[1][d]) + (part[2][d] + part[3][d]);
-            const float res = row_result(sum, (sums[0] + sums[1]) + (sums[2] + sums[3]), sq.s.first() + token,
-                                         (int64_t)a.batch.max_pages << a.cache.log_page);
+            float mx = sums[0].x;
+#pragma unroll
+            for (int w = 1; w < 4; ++w) mx = fmaxf(mx, sums[w].x);
+            float sum = 0.0f, all = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const float f = mx == -__builtin_inff() ? 0.0f : exp2_hw(sums[w].x - mx);
+                all += f * sums[w].y;
+                sum += f * part[w][d];
+            }
+            const float res = row_result(sum, all, sq.s.first() + token, (int64_t)a.batch.max_pages << a.cache.log_page);
             a.y[((int64_t)(sq.s.row0 + token) * a.heads + head * group + member) * D + d] = (uint16_t)bf16_pair(res, 0.0f);
         }
         __syncthreads();
@@ -1101,9 +1129,6 @@ __global__ __launch_bounds__(64 * kLongWaves) void k_attention_long(KvAttentionA
 // launches
 // ---------------------------------------------------------------------------
 
-// Workgroups that the GPU holds at once: four wavefronts each, two per compute unit.
-constexpr int kResident = 512;
-
 // Workspace bytes per slot of all heads.
 int64_t slot_bytes(const KvCacheArgs& c) { return (int64_t)c.kv_heads * 16 * (c.dim + 2) * 4; }
 
@@ -1117,11 +1142,15 @@ int64_t short_tiles(const KvBatchArgs& b, int group) {
 ShortPlan short_plan(const KvCacheArgs& c, const KvBatchArgs& b, int heads, int window, int64_t workspace_bytes) {
     ShortPlan pl;
     const int64_t tiles = short_tiles(b, heads / c.kv_heads);
+    // A compute unit holds eight wavefronts: of one workgroup where there are
+    // no more tiles than compute units (1 x 131072 62 us, with four 67), else of two.
+    pl.waves = tiles * c.kv_heads <= 256 ? 8 : 4;
+    pl.resident = pl.waves == 8 ? 256 : 512;
     // nothing to split where no sequence has more keys to see than the least range
     int64_t keys = (int64_t)b.max_pages << c.log_page;
     const int64_t seen = (int64_t)window + kShortStep + (b.cu ? kShortRows : 1);
     if (window > 0 && seen < keys) keys = seen;
-    const int64_t fit = workspace_bytes / slot_bytes(c) - tiles, want = (kResident + c.kv_heads - 1) / c.kv_heads;
+    const int64_t fit = workspace_bytes / slot_bytes(c) - tiles, want = (pl.resident + c.kv_heads - 1) / c.kv_heads;
     const int64_t ranges = fit < want ? fit : want;
     // the steps of all tiles are counted in 32 bits
     const int64_t steps = (keys + kShortStep - 1) / kShortStep + 1;
@@ -1146,8 +1175,9 @@ hipError_t launch_attention(const KvAttentionArgs& a, hipStream_t stream) {
     const ShortPlan pl = short_plan(c, b, a.heads, a.window, a.workspace_bytes);
     const int64_t tiles = (int64_t)pl.slots * c.kv_heads;
     // a range for each workgroup, or pieces and tiles in turn
-    const uint32_t grid = pl.ranges > 0 ? (uint32_t)(pl.ranges * c.kv_heads) : (uint32_t)(tiles < 2 * kResident ? tiles : 2 * kResident);
-    const hipError_t e = launch(k_attention_short<D>, dim3(grid), dim3(64 * kShortWaves), stream, a, pl, sc);
+    const uint32_t grid = pl.ranges > 0 ? (uint32_t)(pl.ranges * c.kv_heads) : (uint32_t)(tiles < 2 * pl.resident ? tiles : 2 * pl.resident);
+    const hipError_t e = launch(pl.waves == 8 ? k_attention_short<D, 8> : k_attention_short<D, 4>, dim3(grid),
+                                dim3(64 * pl.waves), stream, a, pl, sc);
     if (e != hipSuccess || pl.ranges == 0) return e;
     const int each = b.cu ? 1 : group;
     return launch(k_attention_join<D>, dim3((uint32_t)((int64_t)b.sequences * each * c.kv_heads)), dim3(256), stream, a, pl, each);
