@@ -207,26 +207,39 @@ __device__ __forceinline__ ShortSequence short_sequence(const KvAttentionArgs& a
     return q;
 }
 
-// What a tile counts: one, its steps, or its pieces of the least length.
+// Tiles of a sequence, and what each of them counts.
+struct Weighed {
+    int tiles, weight;
+};
+
+// What a tile counts here: one, its steps, or its pieces of the least length.
 enum Count { kTiles, kSteps, kPieces };
 
 __device__ __forceinline__ int weight(const ShortSequence& q, Count of) {
     return of == kTiles ? 1 : of == kSteps ? q.span() : (q.span() + kLeastRange - 1) / kLeastRange;
 }
 
-// Of the sequences before `seq`; the host has seen to it that 32 bits hold it.
+__device__ __forceinline__ auto weigh_short(const KvAttentionArgs& a, int group, Count of) {
+    return [&a, group, of](int i) {
+        const ShortSequence q = short_sequence(a, group, i);
+        return Weighed{q.tiles, weight(q, of)};
+    };
+}
+
+// Over the sequences before `seq`; the host has seen to it that 32 bits hold it.
 struct Sum {
     int weight, tiles;
 };
 
-__device__ __forceinline__ Sum sum_before(const KvAttentionArgs& a, int group, Count of, int seq) {
+template <typename F>
+__device__ __forceinline__ Sum sum_before(int seq, F weigh) {
     const int lane = threadIdx.x & 63;
     Sum n = {0, 0};
     for (int base = 0; base < seq; base += 64)
         if (base + lane < seq) {
-            const ShortSequence q = short_sequence(a, group, base + lane);
-            n.weight += weight(q, of) * q.tiles;
-            n.tiles += q.tiles;
+            const Weighed w = weigh(base + lane);
+            n.weight += w.weight * w.tiles;
+            n.tiles += w.tiles;
         }
 #pragma unroll
     for (int m = 1; m < 64; m *= 2) {
@@ -236,30 +249,19 @@ __device__ __forceinline__ Sum sum_before(const KvAttentionArgs& a, int group, C
     return n;
 }
 
-// Steps of a range, or 0 where pieces are taken instead.
-__device__ __forceinline__ int range_length(const KvAttentionArgs& a, const ShortPlan& pl, int group) {
-    const int steps = sum_before(a, group, kSteps, a.batch.sequences).weight;
-    const int each = (steps + pl.ranges - 1) / pl.ranges;
-    return each > kLeastRange ? (each + kRangeUnit - 1) / kRangeUnit * kRangeUnit : 0;
-}
-
 // The tile that holds a place in the row of all tiles, its number, its weight
 // and the place within it.
 struct Tile {
     int seq, tile, number, weight, rest;
 };
 
-__device__ __forceinline__ bool find_tile(const KvAttentionArgs& a, int group, Count of, int place, Tile& out) {
+template <typename F>
+__device__ __forceinline__ bool find_tile(int sequences, int place, Tile& out, F weigh) {
     const int lane = threadIdx.x & 63;
     int before = 0, tiles_before = 0;
-    for (int base = 0; base < a.batch.sequences; base += 64) {
-        int tiles = 0, w = 1;
-        if (base + lane < a.batch.sequences) {
-            const ShortSequence q = short_sequence(a, group, base + lane);
-            tiles = q.tiles;
-            w = weight(q, of);
-        }
-        int upto = tiles * w, tiles_upto = tiles;
+    for (int base = 0; base < sequences; base += 64) {
+        const Weighed w = base + lane < sequences ? weigh(base + lane) : Weighed{0, 1};
+        int upto = w.tiles * w.weight, tiles_upto = w.tiles;
 #pragma unroll
         for (int m = 1; m < 64; m *= 2) {
             const int n = __shfl_up(upto, m), k = __shfl_up(tiles_upto, m);
@@ -270,17 +272,24 @@ __device__ __forceinline__ bool find_tile(const KvAttentionArgs& a, int group, C
         if (past) {
             const int at = __builtin_ctzll(past);
             out.seq = base + at;
-            out.weight = __builtin_amdgcn_readlane(w, at);
-            const int rel = place - (before + __builtin_amdgcn_readlane(upto - tiles * w, at));
+            out.weight = __builtin_amdgcn_readlane(w.weight, at);
+            const int rel = place - (before + __builtin_amdgcn_readlane(upto - w.tiles * w.weight, at));
             out.tile = rel / out.weight;
             out.rest = rel - out.tile * out.weight;
-            out.number = tiles_before + __builtin_amdgcn_readlane(tiles_upto - tiles, at) + out.tile;
+            out.number = tiles_before + __builtin_amdgcn_readlane(tiles_upto - w.tiles, at) + out.tile;
             return true;
         }
         before += __builtin_amdgcn_readlane(upto, 63);
         tiles_before += __builtin_amdgcn_readlane(tiles_upto, 63);
     }
     return false;
+}
+
+// Steps of a range, or 0 where pieces are taken instead.
+__device__ __forceinline__ int range_length(const KvAttentionArgs& a, const ShortPlan& pl, int group) {
+    const int steps = sum_before(a.batch.sequences, weigh_short(a, group, kSteps)).weight;
+    const int each = (steps + pl.ranges - 1) / pl.ranges;
+    return each > kLeastRange ? (each + kRangeUnit - 1) / kRangeUnit * kRangeUnit : 0;
 }
 
 // Workspace: per slot, head and row of 16 the sums [dim], then per slot, head
@@ -621,7 +630,7 @@ __device__ __forceinline__ void short_pieces(const KvAttentionArgs& a, const Sho
     const int head = w % kvh, stop = place + length;
     for (;;) {
         Tile t;
-        if (!find_tile(a, group, of, place, t)) return;
+        if (!find_tile(a.batch.sequences, place, t, weigh_short(a, group, of))) return;
         Piece p = {t.seq, t.tile, -1, 0, 1 << 24};
         if (length > 0) {
             p.from = t.rest;
@@ -633,6 +642,8 @@ __device__ __forceinline__ void short_pieces(const KvAttentionArgs& a, const Sho
             p.length = kLeastRange;
             p.slot = place;
         }
+        // rows that cu_tokens counts twice have no slot
+        if (p.slot >= pl.slots) return;
         short_piece<D, WAVES>(a, pl, sc, p, length > 0 ? head : w % kvh, lds);
         if (length > 0) {
             if (place >= stop) return;
@@ -662,7 +673,7 @@ __global__ __launch_bounds__(256) void k_attention_join(KvAttentionArgs a, Short
     const ShortSequence sq = short_sequence(a, group, seq);
     if (sq.tiles == 0) return;
     const int length = range_length(a, pl, group);
-    const Sum before = sum_before(a, group, length > 0 ? kSteps : kPieces, seq);
+    const Sum before = sum_before(seq, weigh_short(a, group, length > 0 ? kSteps : kPieces));
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int row = (int)(blockIdx.x / (uint32_t)kvh % (uint32_t)each); row < sq.s.rows * group; row += each) {
         const int tile = row / 16, r = row % 16;
@@ -675,7 +686,7 @@ __global__ __launch_bounds__(256) void k_attention_join(KvAttentionArgs a, Short
             count = weight(sq, kPieces);
             slot0 = before.weight + tile * count;
         }
-        if (count == 1) continue;
+        if (count == 1 || slot0 + count > pl.slots) continue;
         // eight pieces at a time, so that their loads are in flight together
         constexpr int kBatch = 8;
         float m = -__builtin_inff(), total = 0.0f, o[kPer] = {};
@@ -747,8 +758,66 @@ constexpr int kProducts = 0x008, kReads = 0x100;
 constexpr int kLongWaves = 8, kLongRows = 32 * kLongWaves, kLongKeys = 64;
 
 struct LongPlan {
-    int slots;  // tiles of kLongRows rows of any sequence, at most
+    int target;  // pieces per head to aim at; 0: no split
+    int slots;   // pieces per head, at most
+    int tiles;   // at most
 };
+
+// Steps of a piece, at least.
+constexpr int kLeastPiece = 8;
+
+// A sequence's tiles of kLongRows rows (0: few rows, or none), and the steps of
+// the one that sees the most keys.
+__device__ __forceinline__ Weighed long_sequence(const KvAttentionArgs& a, int group, int i) {
+    const KvSequence s = kv_sequence(a.batch, i);
+    const int64_t room = (int64_t)a.batch.max_pages << a.cache.log_page;
+    int64_t keys = min(s.length, room);
+    if (a.window > 0) keys = min(keys, (int64_t)a.window + kLongRows + kLongKeys);
+    const bool is_long = s.rows > 0 && !is_short(s.rows, group);
+    return {is_long ? (s.rows * group + kLongRows - 1) / kLongRows : 0, (int)((keys + kLongKeys - 1) / kLongKeys)};
+}
+
+// Steps of a piece: as many as give the pieces aimed at.
+__device__ __forceinline__ int piece_length(const KvAttentionArgs& a, const LongPlan& pl, int group) {
+    if (pl.target == 0) return 1 << 24;
+    const int steps = sum_before(a.batch.sequences, [&](int i) { return long_sequence(a, group, i); }).weight;
+    return max((steps + pl.target - 1) / pl.target, kLeastPiece);
+}
+
+// Pieces that every tile of a sequence has places for.
+__device__ __forceinline__ auto weigh_long(const KvAttentionArgs& a, int group, int length) {
+    return [&a, group, length](int i) {
+        const Weighed w = long_sequence(a, group, i);
+        return Weighed{w.tiles, max((w.weight + length - 1) / length, 1)};
+    };
+}
+
+// Keys that some row of a tile sees, and the pieces that these are.
+struct LongTile {
+    int begin, end, pieces;
+};
+
+__device__ __forceinline__ LongTile long_tile(const KvAttentionArgs& a, int group, const KvSequence& s, int tile, int length) {
+    const int rows = s.rows * group, row0 = tile * kLongRows, first = (int)s.first();
+    const int g_lo = first + row0 / group, g_hi = first + min(row0 + kLongRows - 1, rows - 1) / group;
+    const int64_t room = (int64_t)a.batch.max_pages << a.cache.log_page;
+    LongTile t;
+    t.end = (int)min((int64_t)g_hi + 1, min(s.length, room));
+    t.begin = a.window > 0 ? max(g_lo - a.window + 1, 0) & ~(kLongKeys - 1) : 0;
+    const int steps = max(t.end - t.begin + kLongKeys - 1, 0) / kLongKeys;
+    t.pieces = max((steps + length - 1) / length, 1);
+    return t;
+}
+
+// Workspace: per slot, head and row of a tile the sums [dim], then the maximum
+// (base 2) and the sum of the probabilities.
+__device__ __forceinline__ float* long_part(const KvAttentionArgs& a, int slot, int head, int row) {
+    return a.workspace + (((int64_t)slot * a.cache.kv_heads + head) * kLongRows + row) * a.cache.dim;
+}
+__device__ __forceinline__ float2* long_stat(const KvAttentionArgs& a, int slots, int slot, int head, int row) {
+    float* p = a.workspace + (int64_t)slots * a.cache.kv_heads * kLongRows * a.cache.dim;
+    return reinterpret_cast<float2*>(p) + ((int64_t)slot * a.cache.kv_heads + head) * kLongRows + row;
+}
 
 // LDS places, in 16-byte pieces whose order within a row is exchanged so that
 // 16 lanes that read one piece of 16 rows meet every bank once.
@@ -770,13 +839,24 @@ __global__ __launch_bounds__(64 * kLongWaves) void k_attention_long(KvAttentionA
     const int n = lane & 31, hf = lane >> 5;
     const int kvh = a.cache.kv_heads, group = a.heads / kvh;
     const int head = (int)(blockIdx.x % (uint32_t)kvh);
-    // the last tiles of a sequence see the most keys: they go first
-    int number;
-    const int seq = kv_find(a.batch, group, 8, 1, pl.slots - 1 - (int)(blockIdx.x / (uint32_t)kvh), number);
-    const KvSequence s = kv_sequence(a.batch, seq);
-    if (number < 0 || s.rows == 0 || is_short(s.rows, group)) return;
-    const int rows = s.rows * group, row0 = number * kLongRows;
-    if (number >= (rows + kLongRows - 1) / kLongRows) return;
+    // The last tiles of a sequence see the most keys: they go first.  What the
+    // lanes have found alike is made scalar, or it would take vector registers.
+    const int piece_steps = __builtin_amdgcn_readfirstlane(piece_length(a, pl, group));
+    const auto weigh = weigh_long(a, group, piece_steps);
+    const int count = min(__builtin_amdgcn_readfirstlane(sum_before(a.batch.sequences, weigh).weight), pl.slots);
+    const int place = count - 1 - (int)(blockIdx.x / (uint32_t)kvh);
+    Tile found;
+    if (place < 0 || !find_tile(a.batch.sequences, place, found, weigh)) return;
+    const int seq = __builtin_amdgcn_readfirstlane(found.seq);
+    KvSequence s = kv_sequence(a.batch, seq);
+    s.rows = __builtin_amdgcn_readfirstlane(s.rows);
+    s.row0 = __builtin_amdgcn_readfirstlane(s.row0);
+    LongTile tile = long_tile(a, group, s, found.tile, piece_steps);
+    tile.begin = __builtin_amdgcn_readfirstlane(tile.begin);
+    tile.end = __builtin_amdgcn_readfirstlane(tile.end);
+    tile.pieces = __builtin_amdgcn_readfirstlane(tile.pieces);
+    if (found.rest >= tile.pieces) return;
+    const int rows = s.rows * group, row0 = found.tile * kLongRows;
     const int log_page = a.cache.log_page, page = 1 << log_page;
     const int first = (int)s.first();
     const int64_t room = (int64_t)a.batch.max_pages << log_page;
@@ -785,9 +865,8 @@ __global__ __launch_bounds__(64 * kLongWaves) void k_attention_long(KvAttentionA
     const int r = row0 + 32 * wave + n;
     const int token = min(r, rows - 1) / group, member = min(r, rows - 1) - token * group;
     const int pos = first + token;
-    // positions of the wavefront's and the workgroup's first and last rows
+    // positions of the wavefront's first and last rows
     const int w_lo = first + min(row0 + 32 * wave, rows - 1) / group, w_hi = first + min(row0 + 32 * wave + 31, rows - 1) / group;
-    const int g_lo = first + row0 / group, g_hi = first + min(row0 + kLongRows - 1, rows - 1) / group;
 
     f16x8 q[kQ];
     int shift;
@@ -812,8 +891,9 @@ __global__ __launch_bounds__(64 * kLongWaves) void k_attention_long(KvAttentionA
     }
     const int jlo = a.window > 0 ? max(pos - a.window + 1, 0) : 0, jhi = min(pos, length - 1);
     const int all_lo = a.window > 0 ? max(w_hi - a.window + 1, 0) : 0, all_hi = min(w_lo, length - 1);
-    const int begin = a.window > 0 ? max(g_lo - a.window + 1, 0) & ~(kLongKeys - 1) : 0;
-    const int end = min(g_hi + 1, length);  // keys that the workgroup sees
+    // the piece's keys; every piece but the last ends with a step
+    const int begin = tile.begin + (int)min((int64_t)found.rest * piece_steps * kLongKeys, (int64_t)1 << 30);
+    const int end = (int)min((int64_t)tile.end, (int64_t)begin + (int64_t)piece_steps * kLongKeys);
 
     // What a wavefront loads of a tile: 16 bytes of a key per lane, all of one
     // 16-key group, and 16 tokens of a row of values per lane, of one group too
@@ -1035,17 +1115,28 @@ __global__ __launch_bounds__(64 * kLongWaves) void k_attention_long(KvAttentionA
         // is enough.  The last step loads, stores and multiplies keys that no
         // row sees: without a branch around them the results stay in their
         // registers.
-        int buf = 0;
-        for (int t = begin; t < end; t += kLongKeys, buf ^= 1) {
+        auto fetch = [&](int t) __attribute__((always_inline)) {
             if (t + kLongKeys - base == 1024) {
                 base += 1024;
                 now = next;
                 next = block(after);
                 after = entries(base + 2048);
             }
-            const int group = (t + kLongKeys - base) >> 4;  // of tile t + 1
-            load_k(t + 2 * kLongKeys, group < 60 ? lane_of(now.page, group + 4 + k_group) : lane_of(next.page, k_group));
-            load_v(t + kLongKeys, lane_of(now.page, group + v_group), lane_of(now.ve, group + v_group));
+            const int first = (t + kLongKeys - base) >> 4;  // 16-key group of tile t + 1
+            load_k(t + 2 * kLongKeys, first < 60 ? lane_of(now.page, first + 4 + k_group) : lane_of(next.page, k_group));
+            load_v(t + kLongKeys, lane_of(now.page, first + v_group), lane_of(now.ve, first + v_group));
+            return first;
+        };
+        int buf = 0;
+        // a wavefront without rows only brings its part of the keys and values
+        for (int t = begin; t < end && row0 + 32 * wave >= rows; t += kLongKeys, buf ^= 1) {
+            fetch(t);
+            store_k(buf);
+            store_v(buf ^ 1, t + kLongKeys);
+            __syncthreads();
+        }
+        for (int t = begin; t < end && row0 + 32 * wave < rows; t += kLongKeys, buf ^= 1) {
+            const int first_group = fetch(t);
             soften(t);
             __builtin_amdgcn_sched_barrier(0);
             read(g0, buf);
@@ -1058,7 +1149,7 @@ __global__ __launch_bounds__(64 * kLongWaves) void k_attention_long(KvAttentionA
             multiply(g2);
             read(g5, buf);
             multiply(g3);
-            factors(now.ke, group);
+            factors(now.ke, first_group);
             read(g6, buf);
             multiply(g4);
             read(g7, buf);
@@ -1111,17 +1202,89 @@ __global__ __launch_bounds__(64 * kLongWaves) void k_attention_long(KvAttentionA
 
     l += l2;
     l += __shfl_xor(l, 32);
-    if (r < rows) {
-        uint16_t* y = a.y + ((int64_t)(s.row0 + token) * a.heads + head * group + member) * D;
+    if (r >= rows) return;
+    if (tile.pieces > 1) {
+        float* o = long_part(a, place, head, 32 * wave + n);
 #pragma unroll
         for (int i = 0; i < kV; ++i)
 #pragma unroll
-            for (int k = 0; k < 16; k += 4) {
-                uint2 v;
-                v.x = bf16_pair(row_result(acc[i][k], l, pos, room), row_result(acc[i][k + 1], l, pos, room));
-                v.y = bf16_pair(row_result(acc[i][k + 2], l, pos, room), row_result(acc[i][k + 3], l, pos, room));
-                *reinterpret_cast<uint2*>(y + 32 * i + 2 * k + 4 * hf) = v;
-            }
+            for (int k = 0; k < 16; k += 4)
+                *reinterpret_cast<f32x4*>(o + 32 * i + 2 * k + 4 * hf) = (f32x4){acc[i][k], acc[i][k + 1], acc[i][k + 2], acc[i][k + 3]};
+        if (hf == 0) *long_stat(a, pl.slots, place, head, 32 * wave + n) = make_float2(m, l);
+        return;
+    }
+    uint16_t* y = a.y + ((int64_t)(s.row0 + token) * a.heads + head * group + member) * D;
+#pragma unroll
+    for (int i = 0; i < kV; ++i)
+#pragma unroll
+        for (int k = 0; k < 16; k += 4) {
+            uint2 v;
+            v.x = bf16_pair(row_result(acc[i][k], l, pos, room), row_result(acc[i][k + 1], l, pos, room));
+            v.y = bf16_pair(row_result(acc[i][k + 2], l, pos, room), row_result(acc[i][k + 3], l, pos, room));
+            *reinterpret_cast<uint2*>(y + 32 * i + 2 * k + 4 * hf) = v;
+        }
+}
+
+// A workgroup joins the pieces of 32 rows of a tile, in order, eight lanes a row.
+constexpr int kJoinRows = 32;
+
+template <int D>
+__global__ __launch_bounds__(256) void k_attention_join_long(KvAttentionArgs a, LongPlan pl) {
+    constexpr int kPer = D / 32;  // 4-element pieces of a lane, 32 elements apart
+    const int kvh = a.cache.kv_heads, group = a.heads / kvh;
+    const int head = (int)(blockIdx.x % (uint32_t)kvh), rest = (int)(blockIdx.x / (uint32_t)kvh);
+    Tile found;
+    const bool is = find_tile(a.batch.sequences, rest / (kLongRows / kJoinRows), found, [&](int i) { return Weighed{long_sequence(a, group, i).tiles, 1}; });
+    if (!is) return;
+    const KvSequence s = kv_sequence(a.batch, found.seq);
+    const int length = piece_length(a, pl, group);
+    const LongTile tile = long_tile(a, group, s, found.tile, length);
+    if (tile.pieces == 1) return;
+    const Sum before = sum_before(found.seq, weigh_long(a, group, length));
+    const int slot0 = before.weight + found.tile * weigh_long(a, group, length)(found.seq).weight;
+    if (slot0 + tile.pieces > pl.slots) return;  // rows that cu_tokens counts twice
+    const int64_t room = (int64_t)a.batch.max_pages << a.cache.log_page;
+    const int row = rest % (kLongRows / kJoinRows) * kJoinRows + threadIdx.x / 8, r = found.tile * kLongRows + row, d = 4 * (threadIdx.x & 7);
+    if (r >= s.rows * group) return;
+    constexpr int kBatch = 4;
+    float m = -__builtin_inff(), total = 0.0f;
+    f32x4 o[kPer] = {};
+    for (int k = 0; k < tile.pieces; k += kBatch) {
+        float2 st[kBatch];
+        f32x4 p[kBatch][kPer];
+#pragma unroll
+        for (int n = 0; n < kBatch; ++n) {
+            const int slot = slot0 + min(k + n, tile.pieces - 1);
+            st[n] = *long_stat(a, pl.slots, slot, head, row);
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) p[n][e] = *reinterpret_cast<const f32x4*>(long_part(a, slot, head, row) + d + 32 * e);
+        }
+        float mn = m;
+#pragma unroll
+        for (int n = 0; n < kBatch; ++n) mn = fmaxf(mn, st[n].x);
+        const float keep = m == -__builtin_inff() ? (total == 0.0f ? 0.0f : 1.0f) : exp2_hw(m - mn);
+        total *= keep;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) o[e] *= keep;
+        m = mn;
+#pragma unroll
+        for (int n = 0; n < kBatch; ++n) {
+            if (k + n >= tile.pieces) break;
+            const float f = mn == -__builtin_inff() ? 0.0f : exp2_hw(st[n].x - mn);
+            total += f * st[n].y;
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) o[e] += f * p[n][e];
+        }
+    }
+    const int token = r / group, member = r - token * group;
+    const int64_t pos = s.first() + token;
+    uint16_t* y = a.y + ((int64_t)(s.row0 + token) * a.heads + head * group + member) * D + d;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+        uint2 v;
+        v.x = bf16_pair(row_result(o[e][0], total, pos, room), row_result(o[e][1], total, pos, room));
+        v.y = bf16_pair(row_result(o[e][2], total, pos, room), row_result(o[e][3], total, pos, room));
+        *reinterpret_cast<uint2*>(y + 32 * e) = v;
     }
 }
 
@@ -1159,17 +1322,43 @@ ShortPlan short_plan(const KvCacheArgs& c, const KvBatchArgs& b, int heads, int 
     return pl;
 }
 
+int64_t long_slot_bytes(const KvCacheArgs& c) { return (int64_t)c.kv_heads * kLongRows * (c.dim + 2) * 4; }
+
+LongPlan long_plan(const KvCacheArgs& c, const KvBatchArgs& b, int heads, int window, int64_t workspace_bytes) {
+    LongPlan pl = {0, 0, 0};
+    const int64_t rows = b.cu ? (int64_t)b.tokens * (heads / c.kv_heads) : 0;
+    if (rows <= kShortRows) return pl;
+    // a sequence with many rows has more than kShortRows of them
+    const int64_t most = rows / (kShortRows + 1), sequences = most < b.sequences ? most : b.sequences;
+    const int64_t tiles = rows / kLongRows + sequences;
+    int64_t keys = (int64_t)b.max_pages << c.log_page;
+    if (window > 0 && (int64_t)window + kLongRows + kLongKeys < keys) keys = (int64_t)window + kLongRows + kLongKeys;
+    const int64_t steps = (keys + kLongKeys - 1) / kLongKeys + 1;
+    // A piece per compute unit where the rows give tiles for fewer than a quarter
+    // of them; with more the join takes what the split saves (112 tiles of
+    // 31 steps: 52 + 8 us split in three, 55 whole).
+    const int64_t want = rows / kLongRows * c.kv_heads < 64 ? (256 + c.kv_heads - 1) / c.kv_heads : 0;
+    const int64_t fit = workspace_bytes / long_slot_bytes(c) - tiles, target = fit < want ? fit : want;
+    pl.tiles = (int)tiles;
+    pl.target = steps > kLeastPiece && target > 0 && tiles * steps < (int64_t)1 << 30 ? (int)target : 0;
+    pl.slots = (int)(pl.target + tiles);
+    return pl;
+}
+
 template <int D>
 hipError_t launch_attention(const KvAttentionArgs& a, hipStream_t stream) {
     const KvCacheArgs& c = a.cache;
     const KvBatchArgs& b = a.batch;
     const int group = a.heads / c.kv_heads;
     const Scoring sc = scoring(a);
-    if (b.cu && (int64_t)b.tokens * group > kShortRows) {
-        LongPlan pl;
-        pl.slots = (int)kv_items(b, group, 8, 1);
-        const hipError_t e = launch(a.softcap > 0.0f ? k_attention_long<D, true> : k_attention_long<D, false>,
-                                    dim3((uint32_t)(pl.slots * c.kv_heads)), dim3(64 * kLongWaves), stream, a, pl, sc);
+    const LongPlan lp = long_plan(c, b, a.heads, a.window, a.workspace_bytes);
+    if (lp.tiles > 0) {
+        hipError_t e = launch(a.softcap > 0.0f ? k_attention_long<D, true> : k_attention_long<D, false>,
+                              dim3((uint32_t)((int64_t)lp.slots * c.kv_heads)), dim3(64 * kLongWaves), stream, a, lp, sc);
+        if (e != hipSuccess) return e;
+        // the calls after use the same workspace
+        if (lp.target > 0)
+            e = launch(k_attention_join_long<D>, dim3((uint32_t)((int64_t)lp.tiles * (kLongRows / kJoinRows) * c.kv_heads)), dim3(256), stream, a, lp);
         if (e != hipSuccess) return e;
     }
     const ShortPlan pl = short_plan(c, b, a.heads, a.window, a.workspace_bytes);
@@ -1187,7 +1376,9 @@ hipError_t launch_attention(const KvAttentionArgs& a, hipStream_t stream) {
 
 int64_t kv_attention_workspace_bytes(const KvCacheArgs& c, const KvBatchArgs& b, int heads) {
     const ShortPlan pl = short_plan(c, b, heads, 0, (int64_t)1 << 60);
-    return pl.ranges == 0 ? 0 : pl.slots * slot_bytes(c);
+    const LongPlan lp = long_plan(c, b, heads, 0, (int64_t)1 << 60);
+    const int64_t few = pl.ranges == 0 ? 0 : pl.slots * slot_bytes(c), many = lp.target == 0 ? 0 : lp.slots * long_slot_bytes(c);
+    return few > many ? few : many;
 }
 
 bool kv_attention_fits(const KvAttentionArgs& a) {
@@ -1197,8 +1388,9 @@ bool kv_attention_fits(const KvAttentionArgs& a) {
     const ShortPlan pl = short_plan(c, b, a.heads, a.window, a.workspace_bytes);
     // rows of a sequence are counted in 32 bits
     if ((int64_t)b.tokens * (a.heads / c.kv_heads) >= ((int64_t)1 << 31) - kLongRows) return false;
-    const int64_t tiles = b.cu ? kv_items(b, a.heads / c.kv_heads, 8, 1) : 0;
-    return tiles * c.kv_heads <= most / (64 * kLongWaves) &&
+    const LongPlan lp = long_plan(c, b, a.heads, a.window, a.workspace_bytes);
+    return (int64_t)lp.slots * c.kv_heads <= most / (64 * kLongWaves) &&
+           (int64_t)lp.tiles * (kLongRows / kJoinRows) * c.kv_heads <= most / 256 &&
            (int64_t)pl.slots * c.kv_heads < (int64_t)1 << 31 && (int64_t)b.sequences * a.heads <= most / 256;
 }
 

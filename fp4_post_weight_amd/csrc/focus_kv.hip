@@ -255,24 +255,19 @@ __global__ __launch_bounds__(kThreads) void k_kv_write(KvCacheArgs c, KvBatchArg
     }
 }
 
-// Sixteen codes times 2^e, in BF16.
-__device__ __forceinline__ void put16(uint16_t* o, uint4 c, float S) {
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-    uint32_t r[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], false), d = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], true);
-        r[2 * i] = bf16_pair(a[0] * S, a[1] * S);
-        r[2 * i + 1] = bf16_pair(d[0] * S, d[1] * S);
-    }
-    reinterpret_cast<uint4*>(o)[0] = make_uint4(r[0], r[1], r[2], r[3]);
-    reinterpret_cast<uint4*>(o)[1] = make_uint4(r[4], r[5], r[6], r[7]);
+// Eight codes times 2^e, in BF16, stored past the caches (a wavefront's stores
+// cover whole lines).
+__device__ __forceinline__ void put8(uint16_t* o, uint2 c, float S) {
+    const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.x, false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.x, true);
+    const f32x2 d = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, false), e = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, true);
+    const u32x4 r = {bf16_pair(a[0] * S, a[1] * S), bf16_pair(b[0] * S, b[1] * S), bf16_pair(d[0] * S, d[1] * S), bf16_pair(e[0] * S, e[1] * S)};
+    __builtin_nontemporal_store(r, reinterpret_cast<u32x4*>(o));
 }
 
 // A workgroup reads one page's part of one head, keys and values.
 template <int D>
 __global__ __launch_bounds__(kThreads) void k_kv_read(KvCacheArgs c, KvBatchArgs b, uint16_t* k, uint16_t* v) {
-    constexpr int kRow = D + 16;
+    constexpr int kRow = D + 8;
     __shared__ __attribute__((aligned(16))) uint8_t tile[128 * kRow];
     const int tid = threadIdx.x;
     const int head = (int)(blockIdx.x % (uint32_t)c.kv_heads), item = (int)(blockIdx.x / (uint32_t)c.kv_heads);
@@ -296,25 +291,42 @@ __global__ __launch_bounds__(kThreads) void k_kv_read(KvCacheArgs c, KvBatchArgs
     const uint8_t* kc = c.kc + (at << log_page) * D;
     const uint8_t* vc = c.vc + (at << log_page) * D;
     const float ks = __builtin_ldexpf(1.0f, (int)c.ks[at] - 127), vs = __builtin_ldexpf(1.0f, (int)c.vs[at] - 127);
+    // all loads of a thread first
+    constexpr int kKeys = 128 * (D / 8) / kThreads, kQuads = (D / 4) * 32 / kThreads;
     const int quads = page / 4;
-    for (int i = tid; i < (D / 4) * quads; i += kThreads) {
-        const int q = i % quads, d = 4 * (i / quads);
-        if (4 * q + 4 <= p.lo || 4 * q >= p.hi) continue;
-        uint32_t in[4], out[4];
+    uint2 keys[kKeys];
+    uint32_t in[kQuads][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) in[j] = reinterpret_cast<const uint32_t*>(vc + ((int64_t)(d + j) << log_page))[q];
-        transpose4(in, out);
+    for (int m = 0; m < kQuads; ++m) {
+        const int i = tid + m * kThreads, q = i & (quads - 1), d = 4 * (i >> (log_page - 2));
+        if (d >= D || 4 * q + 4 <= p.lo || 4 * q >= p.hi) continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) in[m][j] = reinterpret_cast<const uint32_t*>(vc + ((int64_t)(d + j) << log_page))[q];
+    }
+#pragma unroll
+    for (int m = 0; m < kKeys; ++m) {
+        const int i = tid + m * kThreads;
+        if (i < n * (D / 8)) keys[m] = *reinterpret_cast<const uint2*>(kc + p.lo * D + 8 * i);
+    }
+#pragma unroll
+    for (int m = 0; m < kQuads; ++m) {
+        const int i = tid + m * kThreads, q = i & (quads - 1), d = 4 * (i >> (log_page - 2));
+        if (d >= D || 4 * q + 4 <= p.lo || 4 * q >= p.hi) continue;
+        uint32_t out[4];
+        transpose4(in[m], out);
 #pragma unroll
         for (int j = 0; j < 4; ++j) *reinterpret_cast<uint32_t*>(tile + (4 * q + j) * kRow + d) = out[j];
     }
-    for (int i = tid; i < n * (D / 16); i += kThreads) {
-        const int t = i / (D / 16), d = 16 * (i % (D / 16));
-        put16(ko + t * out_row + d, *reinterpret_cast<const uint4*>(kc + (p.lo + t) * D + d), ks);
+#pragma unroll
+    for (int m = 0; m < kKeys; ++m) {
+        const int i = tid + m * kThreads, t = i / (D / 8), d = 8 * (i % (D / 8));
+        if (i < n * (D / 8)) put8(ko + t * out_row + d, keys[m], ks);
     }
     __syncthreads();
-    for (int i = tid; i < n * (D / 16); i += kThreads) {
-        const int t = i / (D / 16), d = 16 * (i % (D / 16));
-        put16(vo + t * out_row + d, *reinterpret_cast<const uint4*>(tile + (p.lo + t) * kRow + d), vs);
+#pragma unroll
+    for (int m = 0; m < kKeys; ++m) {
+        const int i = tid + m * kThreads, t = i / (D / 8), d = 8 * (i % (D / 8));
+        if (i < n * (D / 8)) put8(vo + t * out_row + d, *reinterpret_cast<const uint2*>(tile + (p.lo + t) * kRow + d), vs);
     }
 }
 
