@@ -709,7 +709,7 @@ int check_kv(const focus_kv_cache* c, const focus_kv_batch* b) {
         return FOCUS_ERR_SHAPE;
     if (c->pages >= kMaxTokens || c->kv_heads > 1024) return FOCUS_ERR_RANGE;
     if (b->sequences < 0 || b->tokens < 0 || b->max_pages < 0 || b->table_stride < b->max_pages) return FOCUS_ERR_SHAPE;
-    if (b->sequences > ((int64_t)1 << 20) || b->tokens >= kMaxTokens || b->table_stride > ((int64_t)1 << 32) ||
+    if (b->sequences > ((int64_t)1 << 20) || b->tokens > ((int64_t)1 << 30) || b->table_stride > ((int64_t)1 << 32) ||
         b->max_pages > ((int64_t)1 << 30) / c->page_tokens)
         return FOCUS_ERR_RANGE;
     if (!b->cu_tokens && b->tokens != b->sequences) return FOCUS_ERR_SHAPE;
@@ -750,7 +750,7 @@ int check_rope(const float* rope, int64_t positions) {
 int focus_rope_table(const double* inv_freq, int64_t positions, int64_t head_dim, float* table, void* stream) {
     if (positions < 0 || head_dim < 0 || head_dim % 2 != 0) return FOCUS_ERR_SHAPE;
     if (positions == 0 || head_dim == 0) return FOCUS_OK;
-    if (positions > ((int64_t)1 << 38) / head_dim) return FOCUS_ERR_RANGE;
+    if (positions > ((int64_t)1 << 32) / head_dim) return FOCUS_ERR_RANGE;
     if (!inv_freq || !table) return FOCUS_ERR_NULL;
     if (!aligned(inv_freq, 8) || !aligned(table, 16)) return FOCUS_ERR_ALIGN;
     return hip_status(focus::launch_rope_table(inv_freq, positions, head_dim, table, (hipStream_t)stream));
@@ -801,9 +801,11 @@ int focus_kv_attention(const focus_kv_cache* cache, const focus_kv_batch* batch,
     if (!q || !y) return FOCUS_ERR_NULL;
     if (!aligned(q, 16) || !aligned(y, 16) || !aligned(workspace, 16)) return FOCUS_ERR_ALIGN;
     const focus::KvAttentionArgs a = {kv_cache_args(*cache), kv_batch_args(*batch), {rope, rope_positions}, q, q_stride,
-                                      (int)heads, scale, softcap, (int)window, y, static_cast<float*>(workspace),
+                                      (int)heads, scale, softcap,
+                                      // no row sees more than 2^30 tokens, and positions less a window stay in 32 bits
+                                      window > ((int64_t)1 << 30) ? 0 : (int)window, y, static_cast<float*>(workspace),
                                       workspace ? workspace_bytes : 0};
-    if (!focus::kv_attention_fits(a)) return FOCUS_ERR_RANGE;
+    if (!focus::kv_attention_fits(a.cache, a.batch, a.heads)) return FOCUS_ERR_RANGE;
     return hip_status(focus::launch_kv_attention(a, (hipStream_t)stream));
 }
 

@@ -1386,24 +1386,22 @@ hipError_t launch_attention(const KvAttentionArgs& a, hipStream_t stream) {
 
 }  // namespace
 
+// Whether the launches stay within 2^32 threads and every count within 32 bits.
+bool kv_attention_fits(const KvCacheArgs& c, const KvBatchArgs& b, int heads) {
+    const int64_t most = 0xFFFFFFFFll, rows = (int64_t)b.tokens * (heads / c.kv_heads);
+    if (rows >= ((int64_t)1 << 31) - kLongRows || (int64_t)b.sequences * heads > most / 256) return false;
+    // the plans add at most 512 ranges or pieces of all heads to the tiles
+    const int64_t few = short_tiles(b, heads / c.kv_heads) * c.kv_heads + 1024;
+    const int64_t many = b.cu ? (rows / kLongRows + b.sequences) * c.kv_heads + 1024 : 0;
+    return few < (int64_t)1 << 31 && many <= most / (64 * kLongWaves) && many <= most / 256 / (kLongRows / kJoinRows);
+}
+
 int64_t kv_attention_workspace_bytes(const KvCacheArgs& c, const KvBatchArgs& b, int heads) {
+    if (!kv_attention_fits(c, b, heads)) return 0;
     const ShortPlan pl = short_plan(c, b, heads, 0, (int64_t)1 << 60);
     const LongPlan lp = long_plan(c, b, heads, 0, (int64_t)1 << 60);
     const int64_t few = pl.ranges == 0 ? 0 : pl.slots * slot_bytes(c), many = lp.target == 0 ? 0 : lp.slots * long_slot_bytes(c);
     return few > many ? few : many;
-}
-
-bool kv_attention_fits(const KvAttentionArgs& a) {
-    const KvCacheArgs& c = a.cache;
-    const KvBatchArgs& b = a.batch;
-    const int64_t most = 0xFFFFFFFFll;
-    const ShortPlan pl = short_plan(c, b, a.heads, a.window, a.workspace_bytes);
-    // rows of a sequence are counted in 32 bits
-    if ((int64_t)b.tokens * (a.heads / c.kv_heads) >= ((int64_t)1 << 31) - kLongRows) return false;
-    const LongPlan lp = long_plan(c, b, a.heads, a.window, a.workspace_bytes);
-    return (int64_t)lp.slots * c.kv_heads <= most / (64 * kLongWaves) &&
-           (int64_t)lp.tiles * (kLongRows / kJoinRows) * c.kv_heads <= most / 256 &&
-           (int64_t)pl.slots * c.kv_heads < (int64_t)1 << 31 && (int64_t)b.sequences * a.heads <= most / 256;
 }
 
 hipError_t launch_kv_attention(const KvAttentionArgs& a, hipStream_t stream) {

@@ -55,7 +55,7 @@ hipError_t launch_kv_read(const KvCacheArgs& c, const KvBatchArgs& b, uint16_t* 
 
 // Whether the launches stay within 2^32 threads.
 bool kv_pages_fit(const KvCacheArgs& c, const KvBatchArgs& b);
-bool kv_attention_fits(const KvAttentionArgs& a);
+bool kv_attention_fits(const KvCacheArgs& c, const KvBatchArgs& b, int heads);
 
 hipError_t launch_kv_attention(const KvAttentionArgs& a, hipStream_t stream);
 

@@ -528,9 +528,9 @@ int focus_w4a16_linear(const uint16_t* x_bf16, int64_t M, int w_format, const ui
  * or attend as zeros; tokens past the table's row, or whose entry is no page
  * of the cache, are not written, and read as NaN or make the rows that see
  * them NaN; positions past the rotation's table turn to NaN.  Pages that a
- * write changes must belong to one sequence each (pages that several
+ * write changes must have one place in one sequence each (pages that several
  * sequences share may be read by all of them).  Rows of no sequence stay as
- * they are.
+ * they are.  Outputs overlap no input.
  */
 typedef struct focus_kv_cache {
     uint8_t* k_codes;   /* [pages, kv_heads, page_tokens, head_dim], 16-byte aligned */
@@ -550,14 +550,14 @@ typedef struct focus_kv_batch {
     const int32_t* lengths;     /* [sequences] tokens, the step's rows included */
     const int32_t* cu_tokens;   /* [sequences + 1], or NULL: tokens == sequences */
     int64_t sequences;          /* at most 2^20 */
-    int64_t tokens;             /* rows of the step's tensors, below 2^31 */
+    int64_t tokens;             /* rows of the step's tensors, at most 2^30 */
 } focus_kv_batch;
 
 /* The rotation's table for the calls below: table [positions, head_dim] FP32
  * (16-byte aligned), row p the cosines and then the sines of p * inv_freq[i],
  * i < head_dim / 2, formed in binary64 and rounded once.  inv_freq
  * [head_dim / 2] FP64, 8-byte aligned.  head_dim even; positions * head_dim
- * <= 2^38. */
+ * <= 2^32. */
 int focus_rope_table(const double* inv_freq, int64_t positions, int64_t head_dim, float* table, void* stream);
 
 /*

@@ -120,3 +120,32 @@ def test_offsets_that_make_no_sense(focus):
     for p in (0, 11):
         assert np.array_equal(cache.k_codes[p].cpu().numpy(), c.k[p]) and np.array_equal(cache.v_codes[p].cpu().numpy(), c.v[p])
     check_attention(focus, c, table, np.array([20, 30, 32, 1]), np.array([0, 5, 20, 45, 46]), queries(8, T, heads, dim))
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 30, 2 ** 30 - 1])
+def test_wide_windows_and_rows_before_the_first(focus, window):
+    """Rows at negative positions beside rows that see keys, under windows wider
+    than any sequence."""
+    rng = np.random.default_rng(12)
+    c = filled(rng, 8, 1, 64, 64)
+    table = table_for(rng, [4, 4], 8)
+    for rows in (3, 90):
+        lengths, cu = np.array([rows - 2, rows + 40]), np.array([0, rows, 2 * rows])
+        got = check_attention(focus, c, table, lengths, cu, queries(rows, 2 * rows, 2, 64), window=window)
+        assert (got[:2] == 0).all() and (got[2:] != 0).any()
+
+
+def test_tables_rows_apart(focus):
+    """A page table that is part of a wider one."""
+    rng = np.random.default_rng(13)
+    c = filled(rng, 12, 2, 16, 64)
+    wide = rng.permutation(12).astype(np.int32).reshape(2, 6)
+    lengths = np.array([40, 29])
+    q = queries(1, 2, 4, 64)
+    cache = make_cache(focus, c)
+    batch = focus.KVBatch(dev(wide)[:, 2:5], dev(lengths.astype(np.int32)))
+    got = focus.kv_attention(cache, batch, q.view(2, -1).to(DEV))
+    y, tol, mine = ref.attention(c, wide[:, 2:5], lengths, None, np32(q), parts=2)
+    ref.close(got.float().cpu().numpy().reshape(2, 4, 64), y, tol, mine)
+    kk, _ = focus.kv_cache_read(cache, batch)
+    assert np.array_equal(kk.float().cpu().numpy(), ref.read(c, wide[:, 2:5], lengths, None, 2, 2, 64)[0])

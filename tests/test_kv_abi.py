@@ -111,6 +111,23 @@ def test_attention_arguments(lib):
     assert g(q=FAKE + 8) == ERR_ALIGN and g(y=FAKE + 8) == ERR_ALIGN
 
 
+def test_counts_past_32_bits(lib):
+    """Batches whose tiles, rows or threads leave 32 bits are refused, and need
+    no workspace."""
+    c = cache(kv_heads=1)
+    one = dict(cu_tokens=None, max_pages=1000, table_stride=1000)
+    w = lib.focus_kv_attention_workspace_bytes
+    f = lib.focus_kv_attention
+    for n, heads in ((1 << 20, 65536), (1 << 20, 64), (1 << 19, 64)):
+        b = batch(sequences=n, tokens=n, **one)
+        assert w(c, b, heads) == 0
+        assert f(c, b, FAKE, heads * 64, heads, None, 0, 0.1, 0.0, 0, FAKE, None, 0, None) == ERR_RANGE
+    b = batch(sequences=4, tokens=1 << 30)
+    assert f(c, b, FAKE, 64 * 4, 4, None, 0, 0.1, 0.0, 0, FAKE, None, 0, None) == ERR_RANGE
+    assert f(cache(), batch(tokens=(1 << 30) + 1), FAKE, 256, 4, None, 0, 0.1, 0.0, 0, FAKE, None, 0, None) == ERR_RANGE
+    assert lib.focus_rope_table(FAKE, (1 << 26) + 1, 64, FAKE, None) == ERR_RANGE
+
+
 def test_attention_workspace(lib):
     f = lib.focus_kv_attention_workspace_bytes
     assert f(None, batch(), 4) == 0 and f(cache(), batch(), 3) == 0 and f(cache(), batch(tokens=0), 4) == 0
