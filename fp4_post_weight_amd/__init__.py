@@ -1023,7 +1023,8 @@ def kv_cache_write(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Ten
     (rows a multiple of 8 elements apart, as parts of one product's rows are),
     into the cache.  ``rope`` (``rope_table``): keys turn by their position
     first.  A page that gains tokens takes the larger scale, and its older codes
-    move to it.  Pages that are written must belong to one sequence each."""
+    move to it.  Pages that are written must have one place in one sequence
+    each."""
     index = _kv_device(cache, batch)
     width = cache.kv_heads * cache.head_dim
     ks, vs = _kv_rows("k", k, batch.tokens, width, index), _kv_rows("v", v, batch.tokens, width, index)
@@ -1050,8 +1051,8 @@ def kv_cache_read(cache: KVCache, batch: KVBatch, k_out: Optional[torch.Tensor] 
 
 
 def kv_attention_workspace_bytes(cache: KVCache, batch: KVBatch, heads: int) -> int:
-    """Bytes of the workspace with which ``kv_attention`` splits the keys of
-    sequences with few rows as far as it helps."""
+    """Bytes of the workspace with which ``kv_attention`` splits sequences over
+    their keys as far as it helps."""
     _kv_device(cache, batch)
     return _lib.lib().focus_kv_attention_workspace_bytes(cache._desc, batch._desc, heads)
 
@@ -1065,7 +1066,8 @@ def kv_attention(cache: KVCache, batch: KVBatch, q: torch.Tensor, rope: Optional
     ``heads`` is a multiple of kv_heads.  ``rope``: queries turn by their
     position first; ``scale`` is head_dim^-0.5 when None; ``softcap`` > 0 caps
     scores, softcap * tanh(s / softcap); ``window`` > 0: a row sees that many
-    tokens at most, its own among them.  A row that sees no token gives zeros."""
+    tokens at most, its own among them.  A row that sees no token gives zeros.
+    ``out`` must not overlap ``q``."""
     index = _kv_device(cache, batch)
     stride = _kv_rows("q", q, batch.tokens, None, index)
     width, dim = q.shape[1], cache.head_dim

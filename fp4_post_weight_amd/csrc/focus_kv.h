@@ -87,13 +87,12 @@ __device__ __forceinline__ KvSequence kv_sequence(const KvBatchArgs& b, int i) {
     return s;
 }
 
-// Work items of ragged sequences without a count of them on the host: sequence
-// i owns the items from (cu[i] * mul >> shift) + extra * i on, at least as many
-// as its rows' units of 2^shift need (extra 1), or as they can touch aligned
-// units of that size (extra 2).  Returns the sequence of an item and its
-// number in it; items that a sequence does not need lie behind its last one.
-// Every wavefront of the workgroup calls it, all 64 lanes.
-__device__ __forceinline__ int kv_find(const KvBatchArgs& b, int mul, int shift, int extra, int item, int& number) {
+// Pages of ragged sequences without a count of them on the host: sequence i
+// owns the items from (cu[i] >> log_page) + 2 i on, at least as many as the
+// pages that its rows can touch.  Returns the sequence of an item and its number
+// in it; items that a sequence does not need lie behind its last page.  Every
+// wavefront of the workgroup calls it, all 64 lanes.
+__device__ __forceinline__ int kv_find(const KvBatchArgs& b, int log_page, int item, int& number) {
     if (!b.cu) {
         number = 0;
         return item;
@@ -102,19 +101,19 @@ __device__ __forceinline__ int kv_find(const KvBatchArgs& b, int mul, int shift,
     int count = 0;  // sequences that begin at or before the item
     for (int base = 0; base < b.sequences; base += 64) {
         const int i = base + lane;
-        const bool before = i < b.sequences && (int)(((int64_t)kv_row_at(b, i) * mul) >> shift) + extra * i <= item;
+        const bool before = i < b.sequences && (kv_row_at(b, i) >> log_page) + 2 * i <= item;
         count += __popcll(__ballot(before));
     }
     const int i = max(count - 1, 0);
-    number = item - ((int)(((int64_t)kv_row_at(b, i) * mul) >> shift) + extra * i);
+    number = item - ((kv_row_at(b, i) >> log_page) + 2 * i);
     return i;
 }
 
 #endif
 
 // How many items kv_find can be asked for.
-inline int64_t kv_items(const KvBatchArgs& b, int mul, int shift, int extra) {
-    return b.cu ? (((int64_t)b.tokens * mul) >> shift) + (int64_t)extra * b.sequences : b.sequences;
+inline int64_t kv_items(const KvBatchArgs& b, int log_page) {
+    return b.cu ? ((int64_t)b.tokens >> log_page) + 2 * (int64_t)b.sequences : b.sequences;
 }
 
 }  // namespace focus

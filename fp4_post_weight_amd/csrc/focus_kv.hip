@@ -106,7 +106,7 @@ struct PagePart {
 // position past the table's row, an entry that is no page of the cache).
 __device__ __forceinline__ bool page_part(const KvCacheArgs& c, const KvBatchArgs& b, int item, PagePart& p) {
     int number;
-    const int i = kv_find(b, 1, c.log_page, 2, item, number);
+    const int i = kv_find(b, c.log_page, item, number);
     const KvSequence s = kv_sequence(b, i);
     const int64_t first = s.first();
     const int64_t page = (first >> c.log_page) + number;
@@ -359,12 +359,12 @@ hipError_t launch_rope_table(const double* inv_freq, int64_t positions, int64_t 
 }
 
 bool kv_pages_fit(const KvCacheArgs& c, const KvBatchArgs& b) {
-    return kv_items(b, 1, c.log_page, 2) * c.kv_heads <= 0xFFFFFFFFll / kThreads;
+    return kv_items(b, c.log_page) * c.kv_heads <= 0xFFFFFFFFll / kThreads;
 }
 
 hipError_t launch_kv_write(const KvCacheArgs& c, const KvBatchArgs& b, const RopeArgs& r, const uint16_t* k,
                            int64_t k_stride, const uint16_t* v, int64_t v_stride, hipStream_t stream) {
-    const dim3 grid((uint32_t)(kv_items(b, 1, c.log_page, 2) * c.kv_heads));
+    const dim3 grid((uint32_t)(kv_items(b, c.log_page) * c.kv_heads));
     const int page = 1 << c.log_page;
     auto run = [&](auto kernel) { return launch(kernel, grid, dim3(kThreads), stream, c, b, r, k, k_stride, v, v_stride); };
     if (c.dim == 128) return page <= 32 ? run(k_kv_write<128, 1>) : page == 64 ? run(k_kv_write<128, 2>) : run(k_kv_write<128, 4>);
@@ -372,7 +372,7 @@ hipError_t launch_kv_write(const KvCacheArgs& c, const KvBatchArgs& b, const Rop
 }
 
 hipError_t launch_kv_read(const KvCacheArgs& c, const KvBatchArgs& b, uint16_t* k, uint16_t* v, hipStream_t stream) {
-    const dim3 grid((uint32_t)(kv_items(b, 1, c.log_page, 2) * c.kv_heads));
+    const dim3 grid((uint32_t)(kv_items(b, c.log_page) * c.kv_heads));
     if (c.dim == 128) return launch(k_kv_read<128>, grid, dim3(kThreads), stream, c, b, k, v);
     return launch(k_kv_read<64>, grid, dim3(kThreads), stream, c, b, k, v);
 }

@@ -594,14 +594,14 @@ int focus_kv_cache_read(const focus_kv_cache* cache, const focus_kv_batch* batch
  *   scale     finite;  softcap finite, 0: none;  window < 2^31, 0: none
  *   y         [tokens, heads * head_dim] BF16, 16-byte aligned
  *   workspace NULL, or workspace_bytes of device memory, 16-byte aligned, that
- *             no other call uses until this one is done: sequences with few
- *             rows are split over their keys as far as it goes.  Nothing in it
- *             has to be set.
+ *             no other call uses until this one is done: where the rows alone
+ *             give too little work at once, sequences are split over their
+ *             keys as far as it goes.  Nothing in it has to be set.
  * Arithmetic: queries keep 8 bits or, turned, 11; keys and values are exact;
  * products and sums are binary32 (order fixed by sizes and lengths, so that
  * equal calls give equal results); probabilities meet the values in BF16 (in
  * two parts where a sequence has few rows); the result is rounded once.
- * At most three launches.  FOCUS_ERR_RANGE where they would need 2^32 threads
+ * At most four launches.  FOCUS_ERR_RANGE where they would need 2^32 threads
  * or where tokens * heads / kv_heads nears 2^31.
  */
 int focus_kv_attention(const focus_kv_cache* cache, const focus_kv_batch* batch, const uint16_t* q, int64_t q_stride,
@@ -609,7 +609,10 @@ int focus_kv_attention(const focus_kv_cache* cache, const focus_kv_batch* batch,
                        int64_t window, uint16_t* y, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Workspace for the full split of focus_kv_attention (0: none helps, or an
- * argument is out of range).  It depends on the host's values alone. */
+ * argument is out of range).  It depends on the host's values alone: one partial
+ * result, 16 or 256 rows of head_dim + 2 FP32 per head of the cache, for each
+ * tile of that many rows that the batch can hold and for each of at most
+ * 512 / kv_heads cuts (tens of MB for a step of many sequences). */
 int64_t focus_kv_attention_workspace_bytes(const focus_kv_cache* cache, const focus_kv_batch* batch, int64_t heads);
 
 #ifdef __cplusplus
