@@ -1004,8 +1004,8 @@ def _kv_rope(rope, dim, index):
         return 0, 0
     if not _fits(rope, torch.float32, index):
         _check_dev("rope", rope, torch.float32, torch.device("cuda", index))
-    if rope.dim() != 2 or rope.shape[1] != dim:
-        raise ValueError(f"rope must be [positions, {dim}]")
+    if rope.dim() != 2 or rope.shape[1] != dim or rope.shape[0] == 0:
+        raise ValueError(f"rope must be [positions, {dim}], at least one position")
     return rope.data_ptr(), rope.shape[0]
 
 

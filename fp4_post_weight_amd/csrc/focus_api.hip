@@ -741,7 +741,8 @@ int check_kv_rows(int64_t stride, int64_t width, int64_t tokens) {
 }
 
 int check_rope(const float* rope, int64_t positions) {
-    if (positions < 0) return FOCUS_ERR_SHAPE;
+    // the kernels read row 0 for positions past the table
+    if (positions < 0 || (rope && positions == 0)) return FOCUS_ERR_SHAPE;
     return aligned(rope, 16) ? FOCUS_OK : FOCUS_ERR_ALIGN;
 }
 

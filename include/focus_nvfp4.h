@@ -565,7 +565,8 @@ int focus_rope_table(const double* inv_freq, int64_t positions, int64_t head_dim
  *   k, v      [tokens, kv_heads * head_dim] BF16, 16-byte aligned, rows k_stride
  *             and v_stride elements apart (at least a row, a multiple of 8), so
  *             that they may be parts of one product's rows
- *   rope      NULL, or the table of focus_rope_table [rope_positions, head_dim]:
+ *   rope      NULL, or the table of focus_rope_table [rope_positions, head_dim],
+ *             at least one position:
  *             keys are turned by their position's angles first, each operation
  *             one binary32 operation (k[i]*c - k[i+h]*s, k[i+h]*c + k[i]*s,
  *             h = head_dim / 2), and stored from binary32

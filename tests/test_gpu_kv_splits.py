@@ -149,3 +149,31 @@ def test_tables_rows_apart(focus):
     ref.close(got.float().cpu().numpy().reshape(2, 4, 64), y, tol, mine)
     kk, _ = focus.kv_cache_read(cache, batch)
     assert np.array_equal(kk.float().cpu().numpy(), ref.read(c, wide[:, 2:5], lengths, None, 2, 2, 64)[0])
+
+
+@pytest.mark.parametrize("dim,softcap,window", [(64, 0.0, 0), (128, 0.0, 0), (64, 25.0, 0), (128, 0.0, 2100)])
+def test_many_and_few_rows_split_together(focus, dim, softcap, window):
+    """Sequences with many rows whose keys are split, beside so many single
+    tokens that theirs are cut into ranges; then the batch again without the
+    ones or the others."""
+    rng = np.random.default_rng(dim + 14)
+    lengths = np.concatenate([rng.integers(2000, 3000, 24), [2500, 1900]])
+    rows = np.concatenate([np.ones(24, int), [70, 300]])
+    order = rng.permutation(26)
+    lengths, rows = lengths[order], rows[order]
+    counts = [-(-n // 64) for n in lengths]
+    c = filled(rng, sum(counts), 8, 64, dim)
+    table = table_for(rng, counts, sum(counts), fill=-1)
+    for kept in (rows, np.where(rows == 1, 1, 0), np.where(rows == 1, 0, rows)):
+        cu = np.concatenate([[0], np.cumsum(kept)])
+        check_attention(focus, c, table, lengths, cu, queries(15, int(cu[-1]), 16, dim), softcap=softcap, window=window)
+
+
+def test_rope_table_of_no_positions(focus):
+    c = make_cache(focus, filled(np.random.default_rng(16), 2, 1, 16, 64))
+    batch = focus.KVBatch(torch.zeros(1, 2, dtype=torch.int32, device=DEV), torch.ones(1, dtype=torch.int32, device=DEV))
+    x, none = torch.zeros(1, 64, dtype=torch.bfloat16, device=DEV), torch.empty(0, 64, device=DEV)
+    with pytest.raises(ValueError):
+        focus.kv_attention(c, batch, x, rope=none)
+    with pytest.raises(ValueError):
+        focus.kv_cache_write(c, batch, x, x, rope=none)

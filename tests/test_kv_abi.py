@@ -111,6 +111,12 @@ def test_attention_arguments(lib):
     assert g(q=FAKE + 8) == ERR_ALIGN and g(y=FAKE + 8) == ERR_ALIGN
 
 
+def test_rope_without_positions(lib):
+    """A table of no positions would be read at its first."""
+    assert lib.focus_kv_cache_write(cache(), batch(), FAKE, 128, FAKE, 128, FAKE, 0, None) == ERR_SHAPE
+    assert lib.focus_kv_attention(cache(), batch(), FAKE, 256, 4, FAKE, 0, 0.1, 0.0, 0, FAKE, None, 0, None) == ERR_SHAPE
+
+
 def test_counts_past_32_bits(lib):
     """Batches whose tiles, rows or threads leave 32 bits are refused, and need
     no workspace."""
