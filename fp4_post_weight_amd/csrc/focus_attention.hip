@@ -839,24 +839,32 @@ __device__ __forceinline__ int key_place(int token, int piece) {
 }
 __device__ __forceinline__ int value_place(int d, int piece) { return d * 8 + (piece ^ ((d >> 1) & 7)); }
 
+template <int D>
+struct LongLds {
+    uint4 keys[2][kLongKeys * D / 8];
+    uint4 values[2][kLongKeys * D / 8];
+    int nan_seen;  // whether a value is NaN
+};
+
+// Piece `item / kv_heads` from behind of a head.
 template <int D, bool CAP>
-__global__ __launch_bounds__(64 * kLongWaves) void k_attention_long(KvAttentionArgs a, LongPlan pl, Scoring sc) {
+__device__ __forceinline__ void long_piece(const KvAttentionArgs& a, const LongPlan& pl, const Scoring& sc, uint32_t item, LongLds<D>& lds) {
     constexpr int kQ = D / 16;  // products per 32 keys
     constexpr int kV = D / 32;  // tiles of the result
-    __shared__ uint4 keys[2][kLongKeys * D / 8];
-    __shared__ uint4 values[2][kLongKeys * D / 8];
-    __shared__ int nan_seen;      // whether a value is NaN
+    auto& keys = lds.keys;
+    auto& values = lds.values;
+    int& nan_seen = lds.nan_seen;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 31, hf = lane >> 5;
     const int kvh = a.cache.kv_heads, group = a.heads / kvh;
-    const int head = (int)(blockIdx.x % (uint32_t)kvh);
+    const int head = (int)(item % (uint32_t)kvh);
     // The last tiles of a sequence see the most keys: they go first.  What the
     // lanes have found alike is made scalar, or it would take vector registers.
     const int piece_steps = __builtin_amdgcn_readfirstlane(piece_length(a, pl, group));
     const auto weigh = weigh_long(a, group, piece_steps);
     const int count = min(__builtin_amdgcn_readfirstlane(sum_before(a.batch.sequences, weigh).weight), pl.slots);
-    const int place = count - 1 - (int)(blockIdx.x / (uint32_t)kvh);
+    const int place = count - 1 - (int)(item / (uint32_t)kvh);
     Tile found;
     if (place < 0 || !find_tile(a.batch.sequences, place, found, weigh)) return;
     const int seq = __builtin_amdgcn_readfirstlane(found.seq);
@@ -1237,6 +1245,29 @@ __global__ __launch_bounds__(64 * kLongWaves) void k_attention_long(KvAttentionA
         }
 }
 
+// A batch that may hold sequences with many rows: the first workgroups take
+// their pieces, the others those of the sequences with few rows, with a
+// workspace of their own, so that the compute units that the ones leave idle
+// stream the cache for the others (3 x 500 rows and 40 single ones over up to
+// 2000 tokens, 32/8 heads of 64: 64 us, one launch after the other 82; a prompt
+// alone takes as long either way).
+template <int D, bool CAP>
+__global__ __launch_bounds__(64 * kLongWaves) void k_attention_mixed(KvAttentionArgs a, LongPlan lp, uint32_t long_items,
+                                                                     ShortPlan pl, float* short_workspace, Scoring sc) {
+    union Lds {
+        LongLds<D> many;
+        ShortLds<D, kLongWaves> few;
+    };
+    __shared__ __attribute__((aligned(16))) uint8_t lds[sizeof(Lds)];
+    if (blockIdx.x < long_items) {
+        long_piece<D, CAP>(a, lp, sc, blockIdx.x, *reinterpret_cast<LongLds<D>*>(lds));
+    } else {
+        a.workspace = short_workspace;
+        short_pieces<D, kLongWaves>(a, pl, sc, (int)(blockIdx.x - long_items), (int)(gridDim.x - long_items),
+                                    *reinterpret_cast<ShortLds<D, kLongWaves>*>(lds));
+    }
+}
+
 // A workgroup joins the pieces of 32 rows of a tile, in order, eight lanes a row.
 constexpr int kJoinRows = 32;
 
@@ -1314,12 +1345,13 @@ int64_t short_tiles(const KvBatchArgs& b, int group) {
     return by_rows < b.sequences * most ? by_rows : b.sequences * most;
 }
 
-ShortPlan short_plan(const KvCacheArgs& c, const KvBatchArgs& b, int heads, int window, int64_t workspace_bytes) {
+// `beside`: in the launch of sequences with many rows.
+ShortPlan short_plan(const KvCacheArgs& c, const KvBatchArgs& b, int heads, int window, int64_t workspace_bytes, bool beside) {
     ShortPlan pl;
     const int64_t tiles = short_tiles(b, heads / c.kv_heads);
     // A compute unit holds eight wavefronts: of one workgroup where there are
     // no more tiles than compute units (1 x 131072 62 us, with four 67), else of two.
-    pl.waves = tiles * c.kv_heads <= 256 ? 8 : 4;
+    pl.waves = beside || tiles * c.kv_heads <= 256 ? 8 : 4;
     pl.resident = pl.waves == 8 ? 256 : 512;
     // nothing to split where no sequence has more keys to see than the least range
     int64_t keys = (int64_t)b.max_pages << c.log_page;
@@ -1357,6 +1389,10 @@ LongPlan long_plan(const KvCacheArgs& c, const KvBatchArgs& b, int heads, int wi
     return pl;
 }
 
+// Workspace bytes of a plan's pieces.
+int64_t plan_bytes(const KvCacheArgs& c, const ShortPlan& pl) { return pl.ranges == 0 ? 0 : pl.slots * slot_bytes(c); }
+int64_t plan_bytes(const KvCacheArgs& c, const LongPlan& pl) { return pl.target == 0 ? 0 : pl.slots * long_slot_bytes(c); }
+
 template <int D>
 hipError_t launch_attention(const KvAttentionArgs& a, hipStream_t stream) {
     const KvCacheArgs& c = a.cache;
@@ -1364,24 +1400,26 @@ hipError_t launch_attention(const KvAttentionArgs& a, hipStream_t stream) {
     const int group = a.heads / c.kv_heads;
     const Scoring sc = scoring(a);
     const LongPlan lp = long_plan(c, b, a.heads, a.window, a.workspace_bytes);
-    if (lp.tiles > 0) {
-        hipError_t e = launch(a.softcap > 0.0f ? k_attention_long<D, true> : k_attention_long<D, false>,
-                              dim3((uint32_t)((int64_t)lp.slots * c.kv_heads)), dim3(64 * kLongWaves), stream, a, lp, sc);
-        if (e != hipSuccess) return e;
-        // the calls after use the same workspace
-        if (lp.target > 0)
-            e = launch(k_attention_join_long<D>, dim3((uint32_t)((int64_t)lp.tiles * (kLongRows / kJoinRows) * c.kv_heads)), dim3(256), stream, a, lp);
-        if (e != hipSuccess) return e;
-    }
-    const ShortPlan pl = short_plan(c, b, a.heads, a.window, a.workspace_bytes);
+    const int64_t many_bytes = plan_bytes(c, lp);
+    KvAttentionArgs few = a;
+    if (few.workspace) few.workspace += many_bytes / 4;
+    const ShortPlan pl = short_plan(c, b, a.heads, a.window, a.workspace_bytes - many_bytes, lp.tiles > 0);
     const int64_t tiles = (int64_t)pl.slots * c.kv_heads;
     // a range for each workgroup, or pieces and tiles in turn
     const uint32_t grid = pl.ranges > 0 ? (uint32_t)(pl.ranges * c.kv_heads) : (uint32_t)(tiles < 2 * pl.resident ? tiles : 2 * pl.resident);
-    const hipError_t e = launch(pl.waves == 8 ? k_attention_short<D, 8> : k_attention_short<D, 4>, dim3(grid),
-                                dim3(64 * pl.waves), stream, a, pl, sc);
+    hipError_t e;
+    if (lp.tiles > 0) {
+        const uint32_t items = (uint32_t)((int64_t)lp.slots * c.kv_heads);
+        e = launch(a.softcap > 0.0f ? k_attention_mixed<D, true> : k_attention_mixed<D, false>, dim3(items + grid),
+                   dim3(64 * kLongWaves), stream, a, lp, items, pl, few.workspace, sc);
+        if (e == hipSuccess && lp.target > 0)
+            e = launch(k_attention_join_long<D>, dim3((uint32_t)((int64_t)lp.tiles * (kLongRows / kJoinRows) * c.kv_heads)), dim3(256), stream, a, lp);
+    } else {
+        e = launch(pl.waves == 8 ? k_attention_short<D, 8> : k_attention_short<D, 4>, dim3(grid), dim3(64 * pl.waves), stream, a, pl, sc);
+    }
     if (e != hipSuccess || pl.ranges == 0) return e;
     const int each = b.cu ? 1 : group;
-    return launch(k_attention_join<D>, dim3((uint32_t)((int64_t)b.sequences * each * c.kv_heads)), dim3(256), stream, a, pl, each);
+    return launch(k_attention_join<D>, dim3((uint32_t)((int64_t)b.sequences * each * c.kv_heads)), dim3(256), stream, few, pl, each);
 }
 
 }  // namespace
@@ -1393,15 +1431,13 @@ bool kv_attention_fits(const KvCacheArgs& c, const KvBatchArgs& b, int heads) {
     // the plans add at most 512 ranges or pieces of all heads to the tiles
     const int64_t few = short_tiles(b, heads / c.kv_heads) * c.kv_heads + 1024;
     const int64_t many = b.cu ? (rows / kLongRows + b.sequences) * c.kv_heads + 1024 : 0;
-    return few < (int64_t)1 << 31 && many <= most / (64 * kLongWaves) && many <= most / 256 / (kLongRows / kJoinRows);
+    return few < (int64_t)1 << 31 && many + 1024 <= most / (64 * kLongWaves) && many <= most / 256 / (kLongRows / kJoinRows);
 }
 
 int64_t kv_attention_workspace_bytes(const KvCacheArgs& c, const KvBatchArgs& b, int heads) {
     if (!kv_attention_fits(c, b, heads)) return 0;
-    const ShortPlan pl = short_plan(c, b, heads, 0, (int64_t)1 << 60);
     const LongPlan lp = long_plan(c, b, heads, 0, (int64_t)1 << 60);
-    const int64_t few = pl.ranges == 0 ? 0 : pl.slots * slot_bytes(c), many = lp.target == 0 ? 0 : lp.slots * long_slot_bytes(c);
-    return few > many ? few : many;
+    return plan_bytes(c, lp) + plan_bytes(c, short_plan(c, b, heads, 0, (int64_t)1 << 60, lp.tiles > 0));
 }
 
 hipError_t launch_kv_attention(const KvAttentionArgs& a, hipStream_t stream) {

@@ -602,7 +602,7 @@ int focus_kv_cache_read(const focus_kv_cache* cache, const focus_kv_batch* batch
  * products and sums are binary32 (order fixed by sizes and lengths, so that
  * equal calls give equal results); probabilities meet the values in BF16 (in
  * two parts where a sequence has few rows); the result is rounded once.
- * At most four launches.  FOCUS_ERR_RANGE where they would need 2^32 threads
+ * At most three launches.  FOCUS_ERR_RANGE where they would need 2^32 threads
  * or where tokens * heads / kv_heads nears 2^31.
  */
 int focus_kv_attention(const focus_kv_cache* cache, const focus_kv_batch* batch, const uint16_t* q, int64_t q_stride,
