@@ -76,15 +76,9 @@ __device__ __forceinline__ void transpose4(const uint32_t (&in)[4], uint32_t (&o
     out[3] = __builtin_amdgcn_perm(d, b, 0x07060302);
 }
 
-__device__ __forceinline__ void load8(const uint16_t* p, float (&f)[8]) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
     f[0] = bf16_lo(v.x), f[1] = bf16_hi(v.x), f[2] = bf16_lo(v.y), f[3] = bf16_hi(v.y);
     f[4] = bf16_lo(v.z), f[5] = bf16_hi(v.z), f[6] = bf16_lo(v.w), f[7] = bf16_hi(v.w);
-}
-
-__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
 }
 
 __device__ __forceinline__ uint2 codes8(const float (&x)[8], float inv) {
@@ -140,8 +134,10 @@ __global__ __launch_bounds__(kThreads) void k_kv_write(KvCacheArgs c, KvBatchArg
     if (!page_part(c, b, item, p) || p.physical < 0) return;
     const int log_page = c.log_page, page = 1 << log_page;
 
-    float x[NP][2][8], y[NP][2][8];  // keys, values
-    float ka = 0.0f, va = 0.0f;
+    // all loads of a thread first
+    uint4 kr[NP][2], vr[NP][2];  // keys, values
+    float4 angle[NP][4];         // cosines, sines
+    bool known[NP];
 #pragma unroll
     for (int n = 0; n < NP; ++n) {
         const int t = p.lo + n * kPass + tok;
@@ -149,31 +145,45 @@ __global__ __launch_bounds__(kThreads) void k_kv_write(KvCacheArgs c, KvBatchArg
             const int64_t row = p.row + (t - p.lo);
             const uint16_t* kp = k + row * k_stride + head * D + 8 * sub;
             const uint16_t* vp = v + row * v_stride + head * D + 8 * sub;
-            load8(kp, x[n][0]);
-            load8(kp + kHalf, x[n][1]);
-            load8(vp, y[n][0]);
-            load8(vp + kHalf, y[n][1]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                kr[n][i] = *reinterpret_cast<const uint4*>(kp + i * kHalf);
+                vr[n][i] = *reinterpret_cast<const uint4*>(vp + i * kHalf);
+            }
             if (rope.table) {
                 const int64_t pos = p.base + t;
-                float cs[8], sn[8];
-                if (pos < rope.positions) {
-                    load8(rope.table + pos * D + 8 * sub, cs);
-                    load8(rope.table + pos * D + kHalf + 8 * sub, sn);
-                } else {
+                known[n] = pos < rope.positions;
+                const float4* a = reinterpret_cast<const float4*>(rope.table + (known[n] ? pos : 0) * D + 8 * sub);
+                angle[n][0] = a[0], angle[n][1] = a[1], angle[n][2] = a[kHalf / 4], angle[n][3] = a[kHalf / 4 + 1];
+            }
+        }
+    }
+    float x[NP][2][8];  // keys
+    float ka = 0.0f, va = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) cs[i] = sn[i] = __builtin_nanf("");
-                }
+    for (int n = 0; n < NP; ++n) {
+        const int t = p.lo + n * kPass + tok;
+        if (t < p.hi) {
+            float y[2][8];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                unpack8(kr[n][i], x[n][i]);
+                unpack8(vr[n][i], y[i]);
+            }
+            if (rope.table) {
+                const float4 a = angle[n][0], b = angle[n][1], c = angle[n][2], d = angle[n][3];
+                const float cs[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}, sn[8] = {c.x, c.y, c.z, c.w, d.x, d.y, d.z, d.w};
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float f = x[n][0][i], g = x[n][1][i];
-                    x[n][0][i] = f * cs[i] - g * sn[i];
-                    x[n][1][i] = g * cs[i] + f * sn[i];
+                    x[n][0][i] = known[n] ? f * cs[i] - g * sn[i] : __builtin_nanf("");
+                    x[n][1][i] = known[n] ? g * cs[i] + f * sn[i] : __builtin_nanf("");
                 }
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 ka = fmaxf(ka, fmaxf(finite_abs(x[n][0][i]), finite_abs(x[n][1][i])));
-                va = fmaxf(va, fmaxf(finite_abs(y[n][0][i]), finite_abs(y[n][1][i])));
+                va = fmaxf(va, fmaxf(finite_abs(y[0][i]), finite_abs(y[1][i])));
             }
         }
     }
@@ -206,7 +216,10 @@ __global__ __launch_bounds__(kThreads) void k_kv_write(KvCacheArgs c, KvBatchArg
         if (t < p.hi) {
             *reinterpret_cast<uint2*>(kc + t * D + 8 * sub) = codes8(x[n][0], kinv);
             *reinterpret_cast<uint2*>(kc + t * D + kHalf + 8 * sub) = codes8(x[n][1], kinv);
-            const uint2 a = codes8(y[n][0], vinv), d = codes8(y[n][1], vinv);
+            float y[2][8];
+            unpack8(vr[n][0], y[0]);
+            unpack8(vr[n][1], y[1]);
+            const uint2 a = codes8(y[0], vinv), d = codes8(y[1], vinv);
             uint32_t* o = reinterpret_cast<uint32_t*>(tile + (t - p.lo) * kRow + 8 * sub);
             o[0] = a.x, o[1] = a.y;
             o[kHalf / 4] = d.x, o[kHalf / 4 + 1] = d.y;
