@@ -751,10 +751,11 @@ __global__ __launch_bounds__(256) void k_attention_join(KvAttentionArgs a, Short
 // many rows per sequence
 // ---------------------------------------------------------------------------
 //
-// A workgroup owns 256 rows of one sequence and head and goes over their keys
-// in tiles of 64.  Keys and values are widened once per workgroup on their way
-// to LDS, so that the conversions cost a wavefront little beside its products,
-// and each of 8 wavefronts multiplies them with its 32 rows.  A tile's global
+// A workgroup owns 256 rows of one sequence and head (128 where that leaves
+// compute units idle) and goes over their keys in tiles of 64.  Keys and values
+// are widened once per workgroup on their way to LDS, so that the conversions
+// cost a wavefront little beside its products, and each of 8 (4) wavefronts
+// multiplies them with its 32 rows.  A tile's global
 // loads are in flight while the tile before is multiplied.  Two wavefronts per
 // SIMD (250 registers) let one's softmax run under the other's products; what
 // bounds it is the issue of 215 vector instructions per 64 keys beside 32
@@ -767,39 +768,43 @@ __global__ __launch_bounds__(256) void k_attention_join(KvAttentionArgs a, Short
 // masks of the scheduler's groups
 constexpr int kProducts = 0x008, kReads = 0x100;
 
-constexpr int kLongWaves = 8, kLongRows = 32 * kLongWaves, kLongKeys = 64;
+constexpr int kWaveRows = 32, kLongKeys = 64;
 
 struct LongPlan {
     int target;  // pieces per head to aim at; 0: no split
     int slots;   // pieces per head, at most
     int tiles;   // at most
+    int waves;   // of a workgroup, each with kWaveRows rows of a tile
 };
 
 // Steps of a piece, at least.
 constexpr int kLeastPiece = 8;
 
-// A sequence's tiles of kLongRows rows (0: few rows, or none), and the steps of
+// A sequence's tiles of R rows (0: few rows, or none), and the steps of
 // the one that sees the most keys.
+template <int R>
 __device__ __forceinline__ Weighed long_sequence(const KvAttentionArgs& a, int group, int i) {
     const KvSequence s = kv_sequence(a.batch, i);
     const int64_t room = (int64_t)a.batch.max_pages << a.cache.log_page;
     int64_t keys = min(s.length, room);
-    if (a.window > 0) keys = min(keys, (int64_t)a.window + kLongRows + kLongKeys);
+    if (a.window > 0) keys = min(keys, (int64_t)a.window + R + kLongKeys);
     const bool is_long = s.rows > 0 && !is_short(s.rows, group);
-    return {is_long ? (s.rows * group + kLongRows - 1) / kLongRows : 0, (int)((keys + kLongKeys - 1) / kLongKeys)};
+    return {is_long ? (s.rows * group + R - 1) / R : 0, (int)((keys + kLongKeys - 1) / kLongKeys)};
 }
 
 // Steps of a piece: as many as give the pieces aimed at.
+template <int R>
 __device__ __forceinline__ int piece_length(const KvAttentionArgs& a, const LongPlan& pl, int group) {
     if (pl.target == 0) return 1 << 24;
-    const int steps = sum_before(a.batch.sequences, [&](int i) { return long_sequence(a, group, i); }).weight;
+    const int steps = sum_before(a.batch.sequences, [&](int i) { return long_sequence<R>(a, group, i); }).weight;
     return max((steps + pl.target - 1) / pl.target, kLeastPiece);
 }
 
 // Pieces that every tile of a sequence has places for.
+template <int R>
 __device__ __forceinline__ auto weigh_long(const KvAttentionArgs& a, int group, int length) {
     return [&a, group, length](int i) {
-        const Weighed w = long_sequence(a, group, i);
+        const Weighed w = long_sequence<R>(a, group, i);
         return Weighed{w.tiles, max((w.weight + length - 1) / length, 1)};
     };
 }
@@ -809,9 +814,10 @@ struct LongTile {
     int begin, end, pieces;
 };
 
+template <int R>
 __device__ __forceinline__ LongTile long_tile(const KvAttentionArgs& a, int group, const KvSequence& s, int tile, int length) {
-    const int rows = s.rows * group, row0 = tile * kLongRows, first = (int)s.first();
-    const int g_lo = first + row0 / group, g_hi = first + min(row0 + kLongRows - 1, rows - 1) / group;
+    const int rows = s.rows * group, row0 = tile * R, first = (int)s.first();
+    const int g_lo = first + row0 / group, g_hi = first + min(row0 + R - 1, rows - 1) / group;
     const int64_t room = (int64_t)a.batch.max_pages << a.cache.log_page;
     LongTile t;
     t.end = (int)min((int64_t)g_hi + 1, min(s.length, room));
@@ -823,12 +829,14 @@ __device__ __forceinline__ LongTile long_tile(const KvAttentionArgs& a, int grou
 
 // Workspace: per slot, head and row of a tile the sums [dim], then the maximum
 // (base 2) and the sum of the probabilities.
+template <int R>
 __device__ __forceinline__ float* long_part(const KvAttentionArgs& a, int slot, int head, int row) {
-    return a.workspace + (((int64_t)slot * a.cache.kv_heads + head) * kLongRows + row) * a.cache.dim;
+    return a.workspace + (((int64_t)slot * a.cache.kv_heads + head) * R + row) * a.cache.dim;
 }
+template <int R>
 __device__ __forceinline__ float2* long_stat(const KvAttentionArgs& a, int slots, int slot, int head, int row) {
-    float* p = a.workspace + (int64_t)slots * a.cache.kv_heads * kLongRows * a.cache.dim;
-    return reinterpret_cast<float2*>(p) + ((int64_t)slot * a.cache.kv_heads + head) * kLongRows + row;
+    float* p = a.workspace + (int64_t)slots * a.cache.kv_heads * R * a.cache.dim;
+    return reinterpret_cast<float2*>(p) + ((int64_t)slot * a.cache.kv_heads + head) * R + row;
 }
 
 // LDS places, in 16-byte pieces whose order within a row is exchanged so that
@@ -847,10 +855,11 @@ struct LongLds {
 };
 
 // Piece `item / kv_heads` from behind of a head.
-template <int D, bool CAP>
+template <int D, bool CAP, int WAVES>
 __device__ __forceinline__ void long_piece(const KvAttentionArgs& a, const LongPlan& pl, const Scoring& sc, uint32_t item, LongLds<D>& lds) {
     constexpr int kQ = D / 16;  // products per 32 keys
     constexpr int kV = D / 32;  // tiles of the result
+    constexpr int R = kWaveRows * WAVES;
     auto& keys = lds.keys;
     auto& values = lds.values;
     int& nan_seen = lds.nan_seen;
@@ -861,8 +870,8 @@ __device__ __forceinline__ void long_piece(const KvAttentionArgs& a, const LongP
     const int head = (int)(item % (uint32_t)kvh);
     // The last tiles of a sequence see the most keys: they go first.  What the
     // lanes have found alike is made scalar, or it would take vector registers.
-    const int piece_steps = __builtin_amdgcn_readfirstlane(piece_length(a, pl, group));
-    const auto weigh = weigh_long(a, group, piece_steps);
+    const int piece_steps = __builtin_amdgcn_readfirstlane(piece_length<R>(a, pl, group));
+    const auto weigh = weigh_long<R>(a, group, piece_steps);
     const int count = min(__builtin_amdgcn_readfirstlane(sum_before(a.batch.sequences, weigh).weight), pl.slots);
     const int place = count - 1 - (int)(item / (uint32_t)kvh);
     Tile found;
@@ -871,12 +880,12 @@ __device__ __forceinline__ void long_piece(const KvAttentionArgs& a, const LongP
     KvSequence s = kv_sequence(a.batch, seq);
     s.rows = __builtin_amdgcn_readfirstlane(s.rows);
     s.row0 = __builtin_amdgcn_readfirstlane(s.row0);
-    LongTile tile = long_tile(a, group, s, found.tile, piece_steps);
+    LongTile tile = long_tile<R>(a, group, s, found.tile, piece_steps);
     tile.begin = __builtin_amdgcn_readfirstlane(tile.begin);
     tile.end = __builtin_amdgcn_readfirstlane(tile.end);
     tile.pieces = __builtin_amdgcn_readfirstlane(tile.pieces);
     if (found.rest >= tile.pieces) return;
-    const int rows = s.rows * group, row0 = found.tile * kLongRows;
+    const int rows = s.rows * group, row0 = found.tile * R;
     const int log_page = a.cache.log_page, page = 1 << log_page;
     const int first = (int)s.first();
     const int64_t room = (int64_t)a.batch.max_pages << log_page;
@@ -915,16 +924,19 @@ __device__ __forceinline__ void long_piece(const KvAttentionArgs& a, const LongP
     const int begin = tile.begin + (int)min((int64_t)found.rest * piece_steps * kLongKeys, (int64_t)1 << 30);
     const int end = (int)min((int64_t)tile.end, (int64_t)begin + (int64_t)piece_steps * kLongKeys);
 
-    // What a wavefront loads of a tile: 16 bytes of a key per lane, all of one
-    // 16-key group, and 16 tokens of a row of values per lane, of one group too
-    // (dim 64: the first half of the wavefronts the keys, the other the values).
-    // Page and address are then scalars, beside a lane's constant offset.
-    constexpr bool kBoth = D == 128;
+    // What a wavefront loads of a tile: kParts times 16 bytes of a key per lane,
+    // all of one 16-key group, and as many times 16 tokens of a row of values, of
+    // one group too (8 wavefronts, dim 64: the first half of them the keys, the
+    // other the values).  Page and address are then scalars, beside a lane's
+    // constant offset.
+    constexpr bool kBoth = D / WAVES >= 16;
+    constexpr int kParts = kBoth ? D / WAVES / 16 : 1;
     const bool of_k = kBoth || wave < 4, of_v = kBoth || wave >= 4;
-    const int part = kBoth ? tid : tid & 255;
-    const int k_token = part / (D / 16), k_piece = part % (D / 16);
-    const int k_group = kBoth ? wave >> 1 : wave & 3, v_group = wave & 3;
-    const int v_d = kBoth ? 64 * (wave >> 2) + lane : lane;
+    constexpr int kGroupWaves = kBoth ? WAVES / 4 : 1;  // wavefronts of a group
+    const int k_group = (kBoth ? wave : wave & 3) / kGroupWaves, v_group = wave & 3;
+    constexpr int kPieces = D / 16;  // of a key
+    const int k_token = 16 * k_group + 64 / kPieces * (kGroupWaves > 1 ? wave & 1 : 0) + lane / kPieces, k_piece = lane % kPieces;
+    const int v_d = kGroupWaves > 1 ? 64 * (wave >> 2) + lane : lane;
     const uint32_t k_lane = (uint32_t)((k_token & (page - 1)) * D + 16 * k_piece), v_lane = (uint32_t)(v_d * page);
     const uint8_t* kc = a.cache.kc + (int64_t)head * page * D;
     const uint8_t* vc = a.cache.vc + (int64_t)head * page * D;
@@ -950,49 +962,59 @@ __device__ __forceinline__ void long_piece(const KvAttentionArgs& a, const LongP
     };
     auto lane_of = [&](int v, int i) __attribute__((always_inline)) { return __builtin_amdgcn_readlane(v, i); };
 
-    uint4 kl = {}, vl = {};
+    uint4 kl[kParts] = {}, vl[kParts] = {};
     int kp = 0, vp = 0;  // pages of kl and vl, -1: none
     uint32_t vs = 0;
     auto load_k = [&](int t, int physical) __attribute__((always_inline)) {
         if (!of_k) return;
         kp = physical;
         // a page of 128 tokens has two tiles
-        kl = *reinterpret_cast<const uint4*>(kc + max(physical, 0) * page_bytes + (t & (page - 1) & 64) * D + k_lane);
+        const uint8_t* from = kc + max(physical, 0) * page_bytes + (t & (page - 1) & 64) * D + k_lane;
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) kl[i] = *reinterpret_cast<const uint4*>(from + 1024 * i);
     };
     auto load_v = [&](int t, int physical, uint32_t scale) __attribute__((always_inline)) {
         if (!of_v) return;
         vp = physical;
         vs = scale;
-        vl = *reinterpret_cast<const uint4*>(vc + max(physical, 0) * page_bytes + ((t + 16 * v_group) & (page - 1)) + v_lane);
+        const uint8_t* from = vc + max(physical, 0) * page_bytes + ((t + 16 * v_group) & (page - 1)) + v_lane;
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) vl[i] = *reinterpret_cast<const uint4*>(from + 64 * i * page);
     };
-    const int k_place0 = key_place<D>(k_token, 2 * k_piece), k_place1 = key_place<D>(k_token, 2 * k_piece + 1);
-    const int v_place0 = value_place(v_d, 2 * v_group), v_place1 = value_place(v_d, 2 * v_group + 1);
     auto store_k = [&](int buf) __attribute__((always_inline)) {
         if (!of_k) return;
-        uint4 lo = __builtin_bit_cast(uint4, widen_f16(kl.x, kl.y)), hi = __builtin_bit_cast(uint4, widen_f16(kl.z, kl.w));
-        // a key without a page: NaN
-        if (kp < 0) lo = hi = make_uint4(0x7E007E00, 0x7E007E00, 0x7E007E00, 0x7E007E00);
-        keys[buf][k_place0] = lo;
-        keys[buf][k_place1] = hi;
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+            const int token = k_token + 64 / kPieces * i;
+            uint4 lo = __builtin_bit_cast(uint4, widen_f16(kl[i].x, kl[i].y)), hi = __builtin_bit_cast(uint4, widen_f16(kl[i].z, kl[i].w));
+            // a key without a page: NaN
+            if (kp < 0) lo = hi = make_uint4(0x7E007E00, 0x7E007E00, 0x7E007E00, 0x7E007E00);
+            keys[buf][key_place<D>(token, 2 * k_piece)] = lo;
+            keys[buf][key_place<D>(token, 2 * k_piece + 1)] = hi;
+        }
     };
     auto store_v = [&](int buf, int t) __attribute__((always_inline)) {
         if (!of_v) return;
-        uint32_t w[4] = {vl.x, vl.y, vl.z, vl.w};
-        if (vp < 0 || t + kLongKeys > end) {
-            // values without a page or behind the last token are whatever lies there
-#pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] &= vp >= 0 ? first_bytes(end - (t + 16 * v_group + 4 * k)) : 0u;
-        }
-        if (any_nan(w[0], w[1], w[2], w[3])) {
-            // see below
-            nan_seen = 1;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] &= ~(nan_bytes(w[k]) * 0xFFu);
-        }
         const float S = e8m0_f32(vs);
-        // a lane of the second product wants tokens 4 h .. and 8 + 4 h .. of 16
-        values[buf][v_place0] = __builtin_bit_cast(uint4, widen_bf16(w[0], w[2], S));
-        values[buf][v_place1] = __builtin_bit_cast(uint4, widen_bf16(w[1], w[3], S));
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+            uint32_t w[4] = {vl[i].x, vl[i].y, vl[i].z, vl[i].w};
+            if (vp < 0 || t + kLongKeys > end) {
+                // values without a page or behind the last token are whatever lies there
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[k] &= vp >= 0 ? first_bytes(end - (t + 16 * v_group + 4 * k)) : 0u;
+            }
+            if (any_nan(w[0], w[1], w[2], w[3])) {
+                // see below
+                nan_seen = 1;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[k] &= ~(nan_bytes(w[k]) * 0xFFu);
+            }
+            // a lane of the second product wants tokens 4 h .. and 8 + 4 h .. of 16
+            const int d = v_d + 64 * i;
+            values[buf][value_place(d, 2 * v_group)] = __builtin_bit_cast(uint4, widen_bf16(w[0], w[2], S));
+            values[buf][value_place(d, 2 * v_group + 1)] = __builtin_bit_cast(uint4, widen_bf16(w[1], w[3], S));
+        }
     };
 
     f32x16 acc[kV], score[2];
@@ -1224,13 +1246,13 @@ __device__ __forceinline__ void long_piece(const KvAttentionArgs& a, const LongP
     l += __shfl_xor(l, 32);
     if (r >= rows) return;
     if (tile.pieces > 1) {
-        float* o = long_part(a, place, head, 32 * wave + n);
+        float* o = long_part<R>(a, place, head, 32 * wave + n);
 #pragma unroll
         for (int i = 0; i < kV; ++i)
 #pragma unroll
             for (int k = 0; k < 16; k += 4)
                 *reinterpret_cast<f32x4*>(o + 32 * i + 2 * k + 4 * hf) = (f32x4){acc[i][k], acc[i][k + 1], acc[i][k + 2], acc[i][k + 3]};
-        if (hf == 0) *long_stat(a, pl.slots, place, head, 32 * wave + n) = make_float2(m, l);
+        if (hf == 0) *long_stat<R>(a, pl.slots, place, head, 32 * wave + n) = make_float2(m, l);
         return;
     }
     uint16_t* y = a.y + ((int64_t)(s.row0 + token) * a.heads + head * group + member) * D;
@@ -1249,45 +1271,46 @@ __device__ __forceinline__ void long_piece(const KvAttentionArgs& a, const LongP
 // their pieces, the others those of the sequences with few rows, with a
 // workspace of their own, so that the compute units that the ones leave idle
 // stream the cache for the others (3 x 500 rows and 40 single ones over up to
-// 2000 tokens, 32/8 heads of 64: 64 us, one launch after the other 82; a prompt
-// alone takes as long either way).
-template <int D, bool CAP>
-__global__ __launch_bounds__(64 * kLongWaves) void k_attention_mixed(KvAttentionArgs a, LongPlan lp, uint32_t long_items,
+// 2000 tokens, 32/8 heads of 64: 64 us, one launch after the other 82, and with
+// tiles of 128 rows 49; a prompt alone takes as long either way).
+template <int D, bool CAP, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void k_attention_mixed(KvAttentionArgs a, LongPlan lp, uint32_t long_items,
                                                                      ShortPlan pl, float* short_workspace, Scoring sc) {
     union Lds {
         LongLds<D> many;
-        ShortLds<D, kLongWaves> few;
+        ShortLds<D, WAVES> few;
     };
     __shared__ __attribute__((aligned(16))) uint8_t lds[sizeof(Lds)];
     if (blockIdx.x < long_items) {
-        long_piece<D, CAP>(a, lp, sc, blockIdx.x, *reinterpret_cast<LongLds<D>*>(lds));
+        long_piece<D, CAP, WAVES>(a, lp, sc, blockIdx.x, *reinterpret_cast<LongLds<D>*>(lds));
     } else {
         a.workspace = short_workspace;
-        short_pieces<D, kLongWaves>(a, pl, sc, (int)(blockIdx.x - long_items), (int)(gridDim.x - long_items),
-                                    *reinterpret_cast<ShortLds<D, kLongWaves>*>(lds));
+        short_pieces<D, WAVES>(a, pl, sc, (int)(blockIdx.x - long_items), (int)(gridDim.x - long_items),
+                                    *reinterpret_cast<ShortLds<D, WAVES>*>(lds));
     }
 }
 
 // A workgroup joins the pieces of 32 rows of a tile, in order, eight lanes a row.
-constexpr int kJoinRows = 32;
+constexpr int kJoinRows = 32, kSplitRows = 8 * kWaveRows;
 
 template <int D>
 __global__ __launch_bounds__(256) void k_attention_join_long(KvAttentionArgs a, LongPlan pl) {
+    constexpr int R = kSplitRows;
     constexpr int kPer = D / 32;  // 4-element pieces of a lane, 32 elements apart
     const int kvh = a.cache.kv_heads, group = a.heads / kvh;
     const int head = (int)(blockIdx.x % (uint32_t)kvh), rest = (int)(blockIdx.x / (uint32_t)kvh);
     Tile found;
-    const bool is = find_tile(a.batch.sequences, rest / (kLongRows / kJoinRows), found, [&](int i) { return Weighed{long_sequence(a, group, i).tiles, 1}; });
+    const bool is = find_tile(a.batch.sequences, rest / (R / kJoinRows), found, [&](int i) { return Weighed{long_sequence<R>(a, group, i).tiles, 1}; });
     if (!is) return;
     const KvSequence s = kv_sequence(a.batch, found.seq);
-    const int length = piece_length(a, pl, group);
-    const LongTile tile = long_tile(a, group, s, found.tile, length);
+    const int length = piece_length<R>(a, pl, group);
+    const LongTile tile = long_tile<R>(a, group, s, found.tile, length);
     if (tile.pieces == 1) return;
-    const Sum before = sum_before(found.seq, weigh_long(a, group, length));
-    const int slot0 = before.weight + found.tile * weigh_long(a, group, length)(found.seq).weight;
+    const Sum before = sum_before(found.seq, weigh_long<R>(a, group, length));
+    const int slot0 = before.weight + found.tile * weigh_long<R>(a, group, length)(found.seq).weight;
     if (slot0 + tile.pieces > pl.slots) return;  // rows that cu_tokens counts twice
     const int64_t room = (int64_t)a.batch.max_pages << a.cache.log_page;
-    const int row = rest % (kLongRows / kJoinRows) * kJoinRows + threadIdx.x / 8, r = found.tile * kLongRows + row, d = 4 * (threadIdx.x & 7);
+    const int row = rest % (R / kJoinRows) * kJoinRows + threadIdx.x / 8, r = found.tile * R + row, d = 4 * (threadIdx.x & 7);
     if (r >= s.rows * group) return;
     constexpr int kBatch = 4;
     float m = -__builtin_inff(), total = 0.0f;
@@ -1298,9 +1321,9 @@ __global__ __launch_bounds__(256) void k_attention_join_long(KvAttentionArgs a, 
 #pragma unroll
         for (int n = 0; n < kBatch; ++n) {
             const int slot = slot0 + min(k + n, tile.pieces - 1);
-            st[n] = *long_stat(a, pl.slots, slot, head, row);
+            st[n] = *long_stat<R>(a, pl.slots, slot, head, row);
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) p[n][e] = *reinterpret_cast<const f32x4*>(long_part(a, slot, head, row) + d + 32 * e);
+            for (int e = 0; e < kPer; ++e) p[n][e] = *reinterpret_cast<const f32x4*>(long_part<R>(a, slot, head, row) + d + 32 * e);
         }
         float mn = m;
 #pragma unroll
@@ -1345,13 +1368,13 @@ int64_t short_tiles(const KvBatchArgs& b, int group) {
     return by_rows < b.sequences * most ? by_rows : b.sequences * most;
 }
 
-// `beside`: in the launch of sequences with many rows.
-ShortPlan short_plan(const KvCacheArgs& c, const KvBatchArgs& b, int heads, int window, int64_t workspace_bytes, bool beside) {
+// `waves`: of the launch of sequences with many rows, 0 where there are none.
+ShortPlan short_plan(const KvCacheArgs& c, const KvBatchArgs& b, int heads, int window, int64_t workspace_bytes, int waves) {
     ShortPlan pl;
     const int64_t tiles = short_tiles(b, heads / c.kv_heads);
     // A compute unit holds eight wavefronts: of one workgroup where there are
     // no more tiles than compute units (1 x 131072 62 us, with four 67), else of two.
-    pl.waves = beside || tiles * c.kv_heads <= 256 ? 8 : 4;
+    pl.waves = waves > 0 ? waves : tiles * c.kv_heads <= 256 ? 8 : 4;
     pl.resident = pl.waves == 8 ? 256 : 512;
     // nothing to split where no sequence has more keys to see than the least range
     int64_t keys = (int64_t)b.max_pages << c.log_page;
@@ -1366,25 +1389,37 @@ ShortPlan short_plan(const KvCacheArgs& c, const KvBatchArgs& b, int heads, int 
     return pl;
 }
 
-int64_t long_slot_bytes(const KvCacheArgs& c) { return (int64_t)c.kv_heads * kLongRows * (c.dim + 2) * 4; }
+int64_t long_slot_bytes(const KvCacheArgs& c) { return (int64_t)c.kv_heads * kSplitRows * (c.dim + 2) * 4; }
 
 LongPlan long_plan(const KvCacheArgs& c, const KvBatchArgs& b, int heads, int window, int64_t workspace_bytes) {
-    LongPlan pl = {0, 0, 0};
+    LongPlan pl = {0, 0, 0, 0};
     const int64_t rows = b.cu ? (int64_t)b.tokens * (heads / c.kv_heads) : 0;
     if (rows <= kShortRows) return pl;
     // a sequence with many rows has more than kShortRows of them
     const int64_t most = rows / (kShortRows + 1), sequences = most < b.sequences ? most : b.sequences;
-    const int64_t tiles = rows / kLongRows + sequences;
+    int64_t tiles = rows / kSplitRows + sequences;
     int64_t keys = (int64_t)b.max_pages << c.log_page;
-    if (window > 0 && (int64_t)window + kLongRows + kLongKeys < keys) keys = (int64_t)window + kLongRows + kLongKeys;
+    if (window > 0 && (int64_t)window + kSplitRows + kLongKeys < keys) keys = (int64_t)window + kSplitRows + kLongKeys;
     const int64_t steps = (keys + kLongKeys - 1) / kLongKeys + 1;
     // A piece per compute unit where the rows give tiles for fewer than a quarter
     // of them; with more the join takes what the split saves (112 tiles of
     // 31 steps: 52 + 8 us split in three, 55 whole).
-    const int64_t want = rows / kLongRows * c.kv_heads < 64 ? (256 + c.kv_heads - 1) / c.kv_heads : 0;
+    const int64_t want = rows / kSplitRows * c.kv_heads < 64 ? (256 + c.kv_heads - 1) / c.kv_heads : 0;
     const int64_t fit = workspace_bytes / long_slot_bytes(c) - tiles, target = fit < want ? fit : want;
-    pl.tiles = (int)tiles;
     pl.target = steps > kLeastPiece && target > 0 && tiles * steps < (int64_t)1 << 30 ? (int)target : 0;
+    // Tiles of half the rows where those of 256 leave compute units idle, one
+    // wavefront on each SIMD: us with four and eight wavefronts, 32/8 heads,
+    // 512 rows behind 1000 tokens 34 and 44 (dim 64), 47 and 56 (128); a prompt
+    // of 1500 35 and 43, 52 and 56.  With two such workgroups on most units the
+    // keys are widened twice as often for the same products: 1500 rows behind 6500
+    // tokens 195 and 198, 264 and 243.  Past one tile of 256 for every unit: a
+    // prompt of 4000 118 and 115, 183 and 156.
+    pl.waves = 8;
+    if (pl.target == 0 && rows / kSplitRows * c.kv_heads < (c.dim == 128 && keys > 4096 ? 128 : 256)) {
+        pl.waves = 4;
+        tiles = rows / (4 * kWaveRows) + sequences;
+    }
+    pl.tiles = (int)tiles;
     pl.slots = (int)(pl.target + tiles);
     return pl;
 }
@@ -1403,22 +1438,23 @@ hipError_t launch_attention(const KvAttentionArgs& a, hipStream_t stream) {
     const int64_t many_bytes = plan_bytes(c, lp);
     KvAttentionArgs few = a;
     if (few.workspace) few.workspace += many_bytes / 4;
-    const ShortPlan pl = short_plan(c, b, a.heads, a.window, a.workspace_bytes - many_bytes, lp.tiles > 0);
+    const ShortPlan pl = short_plan(c, b, a.heads, a.window, a.workspace_bytes - many_bytes, lp.waves);
     const int64_t tiles = (int64_t)pl.slots * c.kv_heads;
     // a range for each workgroup, or pieces and tiles in turn
     const uint32_t grid = pl.ranges > 0 ? (uint32_t)(pl.ranges * c.kv_heads) : (uint32_t)(tiles < 2 * pl.resident ? tiles : 2 * pl.resident);
     hipError_t e;
     if (lp.tiles > 0) {
         const uint32_t items = (uint32_t)((int64_t)lp.slots * c.kv_heads);
-        e = launch(a.softcap > 0.0f ? k_attention_mixed<D, true> : k_attention_mixed<D, false>, dim3(items + grid),
-                   dim3(64 * kLongWaves), stream, a, lp, items, pl, few.workspace, sc);
+        auto run = [&](auto kernel) { return launch(kernel, dim3(items + grid), dim3(64 * lp.waves), stream, a, lp, items, pl, few.workspace, sc); };
+        if (lp.waves == 8) e = a.softcap > 0.0f ? run(k_attention_mixed<D, true, 8>) : run(k_attention_mixed<D, false, 8>);
+        else e = a.softcap > 0.0f ? run(k_attention_mixed<D, true, 4>) : run(k_attention_mixed<D, false, 4>);
         if (e == hipSuccess && lp.target > 0)
-            e = launch(k_attention_join_long<D>, dim3((uint32_t)((int64_t)lp.tiles * (kLongRows / kJoinRows) * c.kv_heads)), dim3(256), stream, a, lp);
+            e = launch(k_attention_join_long<D>, dim3((uint32_t)((int64_t)lp.tiles * (kSplitRows / kJoinRows) * c.kv_heads)), dim3(256), stream, a, lp);
     } else {
         e = launch(pl.waves == 8 ? k_attention_short<D, 8> : k_attention_short<D, 4>, dim3(grid), dim3(64 * pl.waves), stream, a, pl, sc);
     }
     if (e != hipSuccess || pl.ranges == 0) return e;
-    const int each = b.cu ? 1 : group;
+    const int each = group;
     return launch(k_attention_join<D>, dim3((uint32_t)((int64_t)b.sequences * each * c.kv_heads)), dim3(256), stream, few, pl, each);
 }
 
@@ -1427,17 +1463,17 @@ hipError_t launch_attention(const KvAttentionArgs& a, hipStream_t stream) {
 // Whether the launches stay within 2^32 threads and every count within 32 bits.
 bool kv_attention_fits(const KvCacheArgs& c, const KvBatchArgs& b, int heads) {
     const int64_t most = 0xFFFFFFFFll, rows = (int64_t)b.tokens * (heads / c.kv_heads);
-    if (rows >= ((int64_t)1 << 31) - kLongRows || (int64_t)b.sequences * heads > most / 256) return false;
+    if (rows >= ((int64_t)1 << 31) - kSplitRows || (int64_t)b.sequences * heads > most / 256) return false;
     // the plans add at most 512 ranges or pieces of all heads to the tiles
     const int64_t few = short_tiles(b, heads / c.kv_heads) * c.kv_heads + 1024;
-    const int64_t many = b.cu ? (rows / kLongRows + b.sequences) * c.kv_heads + 1024 : 0;
-    return few < (int64_t)1 << 31 && many + 1024 <= most / (64 * kLongWaves) && many <= most / 256 / (kLongRows / kJoinRows);
+    const int64_t many = b.cu ? (rows / kSplitRows + b.sequences) * c.kv_heads + 1024 : 0;
+    return few < (int64_t)1 << 31 && many + 1024 <= most / 512 && many <= most / 256 / (kSplitRows / kJoinRows);
 }
 
 int64_t kv_attention_workspace_bytes(const KvCacheArgs& c, const KvBatchArgs& b, int heads) {
     if (!kv_attention_fits(c, b, heads)) return 0;
     const LongPlan lp = long_plan(c, b, heads, 0, (int64_t)1 << 60);
-    return plan_bytes(c, lp) + plan_bytes(c, short_plan(c, b, heads, 0, (int64_t)1 << 60, lp.tiles > 0));
+    return plan_bytes(c, lp) + plan_bytes(c, short_plan(c, b, heads, 0, (int64_t)1 << 60, lp.waves));
 }
 
 hipError_t launch_kv_attention(const KvAttentionArgs& a, hipStream_t stream) {

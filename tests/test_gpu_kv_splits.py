@@ -177,3 +177,22 @@ def test_rope_table_of_no_positions(focus):
         focus.kv_attention(c, batch, x, rope=none)
     with pytest.raises(ValueError):
         focus.kv_cache_write(c, batch, x, x, rope=none)
+
+
+@pytest.mark.parametrize("dim,kvh,heads,rows,lengths", [
+    (64, 2, 8, [400, 1, 129], [410, 30, 1000]),       # 128-row tiles: few, short keys
+    (128, 2, 8, [400, 1, 129], [410, 30, 1000]),
+    (128, 8, 32, [1100], [1150]),                     # more of them than compute units
+    (64, 8, 32, [1100, 1], [1150, 70]),
+    (64, 8, 64, [1200], [1200]),                      # 256-row tiles beside the same keys
+    (128, 8, 64, [1200], [1200]),
+])
+@pytest.mark.parametrize("softcap", [0.0, 30.0])
+def test_tiles_of_either_height(focus, dim, kvh, heads, rows, lengths, softcap):
+    rng = np.random.default_rng(17)
+    lengths = np.array(lengths)
+    counts = [-(-n // 16) for n in lengths]
+    c = filled(rng, sum(counts), kvh, 16, dim)
+    table = table_for(rng, counts, sum(counts), fill=-1)
+    cu = np.concatenate([[0], np.cumsum(rows)])
+    check_attention(focus, c, table, lengths, cu, queries(18, int(cu[-1]), heads, dim), angles(1200, dim), softcap=softcap)
