@@ -338,10 +338,14 @@ __device__ __forceinline__ void short_piece(const KvAttentionArgs& a, const Shor
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int x = lane & 15, c = lane >> 4;
     const int kvh = a.cache.kv_heads, group = a.heads / kvh;
-    const ShortSequence sq = short_sequence(a, group, sh.seq);
+    ShortSequence sq = short_sequence(a, group, sh.seq);
+    sq.s.row0 = __builtin_amdgcn_readfirstlane(sq.s.row0);
+    sq.s.rows = __builtin_amdgcn_readfirstlane(sq.s.rows);
+    sq.begin = __builtin_amdgcn_readfirstlane(sq.begin);
+    sq.end = __builtin_amdgcn_readfirstlane(sq.end);
     const int rows = sq.s.rows * group;
     const int log_page = a.cache.log_page, page = 1 << log_page;
-    const int first = (int)sq.s.first();
+    const int first = __builtin_amdgcn_readfirstlane((int)sq.s.first());
 
     // the lane's query row
     const int r = 16 * sh.tile + x, token = min(r, rows - 1) / group, member = min(r, rows - 1) - token * group;
@@ -635,11 +639,19 @@ __device__ __forceinline__ void short_pieces(const KvAttentionArgs& a, const Sho
     const int head = w % kvh, stop = place + length;
     for (;;) {
         Tile t;
-        if (!find_tile(a.batch.sequences, place, t, weigh_short(a, group, of))) return;
-        Piece p = {t.seq, t.tile, -1, 0, 1 << 24};
+        if (of == kTiles && !a.batch.cu) {
+            // as many tiles of every sequence: no length is waited for (1 x 333 11.7 us, searched 13.1)
+            const int per = (group + 15) / 16;
+            t.seq = __builtin_amdgcn_readfirstlane(place / per);
+            if (t.seq >= a.batch.sequences) return;
+            t.tile = place - t.seq * per;
+        } else if (!find_tile(a.batch.sequences, place, t, weigh_short(a, group, of))) {
+            return;
+        }
+        Piece p = {__builtin_amdgcn_readfirstlane(t.seq), __builtin_amdgcn_readfirstlane(t.tile), -1, 0, 1 << 24};
         if (length > 0) {
-            p.from = t.rest;
-            p.length = min(t.weight - t.rest, stop - place);
+            p.from = __builtin_amdgcn_readfirstlane(t.rest);
+            p.length = __builtin_amdgcn_readfirstlane(min(t.weight - t.rest, stop - place));
             if (p.length < t.weight) p.slot = t.number + range;
             place += p.length;
         } else if (of == kPieces && t.weight > 1) {
