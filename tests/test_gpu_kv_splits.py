@@ -196,3 +196,13 @@ def test_tiles_of_either_height(focus, dim, kvh, heads, rows, lengths, softcap):
     table = table_for(rng, counts, sum(counts), fill=-1)
     cu = np.concatenate([[0], np.cumsum(rows)])
     check_attention(focus, c, table, lengths, cu, queries(18, int(cu[-1]), heads, dim), angles(1200, dim), softcap=softcap)
+
+
+def test_row_counts_that_are_none(focus):
+    table, lengths = torch.zeros(1, 2, dtype=torch.int32, device=DEV), torch.ones(1, dtype=torch.int32, device=DEV)
+    cu = torch.zeros(2, dtype=torch.int32, device=DEV)
+    for tokens in (-1, 2 ** 30 + 1, 1 << 70):
+        with pytest.raises(ValueError):
+            focus.KVBatch(table, lengths, cu, tokens)
+    with pytest.raises(TypeError):
+        focus.KVBatch(table, lengths, cu, 1.0)

@@ -201,3 +201,10 @@ def test_reference_attention_against_softmax():
         s = s.masked_fill((j > i) | (j <= i - 33), -INF)
         want = torch.softmax(s, -1) @ torch.from_numpy(vv[:, h // 3])
         assert np.allclose(y[:, h], want.numpy(), rtol=1e-12, atol=1e-13)
+
+
+def test_packed_descriptors():
+    """The bytes that the handles hold are the structures'."""
+    c, b = cache(), batch()
+    assert _lib.pack_kv_cache(*(getattr(c, n) or 0 for n, _ in c._fields_)) == bytes(c)
+    assert _lib.pack_kv_batch(*(getattr(b, n) or 0 for n, _ in b._fields_)) == bytes(b)
