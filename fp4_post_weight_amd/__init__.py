@@ -982,24 +982,25 @@ def rope_table(positions: int, head_dim: int, base: float = 500000.0, inv_freq: 
 
 
 def _kv_rows(name, t, rows, cols, index):
-    """Row stride of a step's BF16 tensor [rows, cols] whose rows may lie apart."""
+    """Width and row stride of a step's BF16 tensor [rows, cols] whose rows may
+    lie apart."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
     if t.get_device() != index:
         raise ValueError(f"{name} is on {t.device}, expected HIP device {index}")
-    if t.dim() != 2 or t.shape[0] != rows or (cols is not None and t.shape[1] != cols):
+    n, width = t.shape if t.dim() == 2 else (-1, 0)
+    if n != rows or (cols is not None and width != cols):
         raise ValueError(f"{name} must be [{rows}, {'heads * head_dim' if cols is None else cols}]")
     stride, one = t.stride()
-    width = t.shape[1]
     if width > 1 and one != 1:
         raise ValueError(f"the elements of {name}'s rows must be contiguous")
     if rows <= 1:
-        return width
+        return width, width
     if stride < width or stride % 8:
         raise ValueError(f"{name}'s rows must be at least {width} elements apart, by a multiple of 8")
-    return stride
+    return width, stride
 
 
 def _kv_rope(rope, dim, index):
@@ -1007,9 +1008,10 @@ def _kv_rope(rope, dim, index):
         return 0, 0
     if not _fits(rope, torch.float32, index):
         _check_dev("rope", rope, torch.float32, torch.device("cuda", index))
-    if rope.dim() != 2 or rope.shape[1] != dim or rope.shape[0] == 0:
+    positions, width = rope.shape if rope.dim() == 2 else (0, 0)
+    if width != dim or positions == 0:
         raise ValueError(f"rope must be [positions, {dim}], at least one position")
-    return rope.data_ptr(), rope.shape[0]
+    return rope.data_ptr(), positions
 
 
 def _kv_device(cache, batch):
@@ -1030,7 +1032,8 @@ def kv_cache_write(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Ten
     each."""
     index = _kv_device(cache, batch)
     width = cache.kv_heads * cache.head_dim
-    ks, vs = _kv_rows("k", k, batch.tokens, width, index), _kv_rows("v", v, batch.tokens, width, index)
+    rows = batch.tokens
+    ks, vs = _kv_rows("k", k, rows, width, index)[1], _kv_rows("v", v, rows, width, index)[1]
     r, n = _kv_rope(rope, cache.head_dim, index)
     _launch(_lib.lib().focus_kv_cache_write, cache.device, cache._desc, batch._desc, k.data_ptr(), ks, v.data_ptr(),
             vs, r, n)
@@ -1047,7 +1050,9 @@ def kv_cache_read(cache: KVCache, batch: KVBatch, k_out: Optional[torch.Tensor] 
             _check_buf(name, t, torch.bfloat16, cache.device, shape[0] * shape[1] * shape[2])
     if k_out is None:
         k_out = cache.k_codes.new_empty(shape, dtype=torch.bfloat16)
-    if v_out is None:
+        if v_out is None:
+            v_out = torch.empty_like(k_out)
+    elif v_out is None:
         v_out = cache.k_codes.new_empty(shape, dtype=torch.bfloat16)
     _launch(_lib.lib().focus_kv_cache_read, cache.device, cache._desc, batch._desc, k_out.data_ptr(), v_out.data_ptr())
     return k_out, v_out
@@ -1072,8 +1077,8 @@ def kv_attention(cache: KVCache, batch: KVBatch, q: torch.Tensor, rope: Optional
     tokens at most, its own among them.  A row that sees no token gives zeros.
     ``out`` must not overlap ``q``."""
     index = _kv_device(cache, batch)
-    stride = _kv_rows("q", q, batch.tokens, None, index)
-    width, dim = q.shape[1], cache.head_dim
+    width, stride = _kv_rows("q", q, batch.tokens, None, index)
+    dim = cache.head_dim
     heads = width // dim
     if heads < 1 or width % (cache.kv_heads * dim):
         raise ValueError(f"q's rows must hold a multiple of {cache.kv_heads} heads of {dim}")
