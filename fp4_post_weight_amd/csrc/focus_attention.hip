@@ -23,7 +23,7 @@
 //
 // Measured: one token over 131072, 64/8 heads of 128: 59-62 us with the join (4.4
 // TB/s); 64 tokens over up to 16384, 32/8 heads of 128: 210-240 us (4.8-5.4 TB/s;
-// HBM); a prompt of 8192 tokens, 32/8 heads of 128: 586-616 us (0.89-0.94
+// HBM); a prompt of 8192 tokens, 32/8 heads of 128: 582-616 us (0.89-0.94
 // PFLOP/s; matrix units 43 % and vector units 54 % busy).
 
 #include <hip/hip_runtime.h>
@@ -789,8 +789,9 @@ struct LongPlan {
     int waves;   // of a workgroup, each with kWaveRows rows of a tile
 };
 
-// Steps of a piece, at least.
-constexpr int kLeastPiece = 8;
+// Steps of a piece, at least, and the keys up to which nothing is split (64 tiles
+// of 512 keys, us split and whole: 25 and 18 at dim 64, 31 and 24 at 128).
+constexpr int kLeastPiece = 8, kLeastSplit = 1024;
 
 // A sequence's tiles of R rows (0: few rows, or none), and the steps of
 // the one that sees the most keys.
@@ -1413,21 +1414,24 @@ LongPlan long_plan(const KvCacheArgs& c, const KvBatchArgs& b, int heads, int wi
     int64_t keys = (int64_t)b.max_pages << c.log_page;
     if (window > 0 && (int64_t)window + kSplitRows + kLongKeys < keys) keys = (int64_t)window + kSplitRows + kLongKeys;
     const int64_t steps = (keys + kLongKeys - 1) / kLongKeys + 1;
-    // A piece per compute unit where the rows give tiles for fewer than a quarter
-    // of them; with more the join takes what the split saves (112 tiles of
-    // 31 steps: 52 + 8 us split in three, 55 whole).
-    const int64_t want = rows / kSplitRows * c.kv_heads < 64 ? (256 + c.kv_heads - 1) / c.kv_heads : 0;
+    // A piece per compute unit where the rows give tiles for a quarter of them, or
+    // for half of them and their keys are many; with more tiles the join takes
+    // what the split saves.  us split and whole, dim 64 and 128, 32/8 heads: 64
+    // tiles of 1500 keys 30 and 34, 40 and 47, of 8000 73 and 130, 96 and 200;
+    // 96 of 4000 73 and 72, 98 and 108; 125 of 8000 113 and 133, 151 and 200;
+    // 187 of 16000 548 and 346, 717 and 467.
+    const int64_t high = rows / kSplitRows * c.kv_heads;
+    const int64_t want = high <= 64 || (high < 128 && keys > 4096) ? (256 + c.kv_heads - 1) / c.kv_heads : 0;
     const int64_t fit = workspace_bytes / long_slot_bytes(c) - tiles, target = fit < want ? fit : want;
-    pl.target = steps > kLeastPiece && target > 0 && tiles * steps < (int64_t)1 << 30 ? (int)target : 0;
+    pl.target = keys > kLeastSplit && target > 0 && tiles * steps < (int64_t)1 << 30 ? (int)target : 0;
     // Tiles of half the rows where those of 256 leave compute units idle, one
-    // wavefront on each SIMD: us with four and eight wavefronts, 32/8 heads,
-    // 512 rows behind 1000 tokens 34 and 44 (dim 64), 47 and 56 (128); a prompt
-    // of 1500 35 and 43, 52 and 56.  With two such workgroups on most units the
+    // wavefront on each SIMD: us with four and eight wavefronts, 32/8 heads, dim 64
+    // and 128, a prompt of 512 18 and 22, 24 and 27, of 1500 35 and 43, 52 and 57.  With two such workgroups on most units the
     // keys are widened twice as often for the same products: 1500 rows behind 6500
     // tokens 195 and 198, 264 and 243.  Past one tile of 256 for every unit: a
     // prompt of 4000 118 and 115, 183 and 156.
     pl.waves = 8;
-    if (pl.target == 0 && rows / kSplitRows * c.kv_heads < (c.dim == 128 && keys > 4096 ? 128 : 256)) {
+    if (pl.target == 0 && high < (c.dim == 128 && keys > 4096 ? 128 : 256)) {
         pl.waves = 4;
         tiles = rows / (4 * kWaveRows) + sequences;
     }

@@ -17,8 +17,9 @@
 //
 // Both kernels stream: a workgroup takes one page's part of one head, so that it
 // alone decides the page's scale and owns its bytes.  Measured: prompts of up to
-// 8191 tokens, 8 heads of 128, written in 44-46 us (3.7 TB/s; bound by dependent
-// loads -- offsets, table, rows -- in 2.5 rounds of workgroups), 128 single tokens
+// 8191 tokens, 8 heads of 128, written in 42-44 us (3.9 TB/s; bound by dependent
+// loads -- offsets, table, rows -- in 2.5 rounds of workgroups; loads where they
+// are used 46.6 where this took 44.2), 128 single tokens
 // in 5-6 us; 16 sequences of up to 16384 tokens read in 161-163 us (5.0 TB/s of a
 // copy's 5.2).  Keys and values in workgroups of their own: 45.6 and 8.5 us.
 
