@@ -592,7 +592,8 @@ int focus_kv_cache_read(const focus_kv_cache* cache, const focus_kv_batch* batch
  *             elements apart (at least a row, a multiple of 8)
  *   heads     a multiple of kv_heads, at most 65536
  *   rope      as for focus_kv_cache_write: queries are turned by it
- *   scale     finite;  softcap finite, 0: none;  window < 2^31, 0: none
+ *   scale     finite;  softcap finite, 0: none (a cap of any size adds an error
+ *             of at most 26 * 2^-24 of the capped score);  window < 2^31, 0: none
  *   y         [tokens, heads * head_dim] BF16, 16-byte aligned
  *   workspace NULL, or workspace_bytes of device memory, 16-byte aligned, that
  *             no other call uses until this one is done: where the rows alone
