@@ -146,10 +146,15 @@ __device__ __forceinline__ float score_factor(float c0, int e, int shift) {
     return __builtin_amdgcn_fmed3f(__builtin_ldexpf(c0, e - shift), 1.1754944e-38f, 3.4028235e38f);
 }
 
-// A maximum is replaced only by one that is 2^kSlack above it (base 2):
-// probabilities then reach 2^kSlack, which costs neither sum a bit, and a
+// A maximum is replaced only by one that is 2^kSlack above it (base 2), so that a
 // result is rescaled a few times instead of at every new maximum.
+// Probabilities are taken 2^kSlack smaller: they stay at most 1, and with them
+// sums of any values that a mean of weights up to 1 can be formed of; the quotient
+// does not see it.
 constexpr float kSlack = 8.0f;
+
+// What the exponents are taken from, of a running maximum.
+__device__ __forceinline__ float exponent_base(float m) { return m == -__builtin_inff() ? 0.0f : m + kSlack; }
 
 // N scores to cap tanh(s / cap), all to base 2, with an error relative to the
 // result (26 u by its roundings, u = 2^-24) whatever the cap.  tanh(x) =
@@ -560,7 +565,7 @@ __device__ __forceinline__ void short_piece(const KvAttentionArgs& a, const Shor
 #pragma unroll
             for (int i = 0; i < kV; ++i) acc[i] *= alpha;
         }
-        const float mu = m == -__builtin_inff() ? 0.0f : m;
+        const float mu = exponent_base(m);
         // P in two BF16 parts, so that its rounding does not show in the result
         bf16x8 ph[2], pr[2];
 #pragma unroll
@@ -1167,7 +1172,7 @@ __device__ __forceinline__ void long_piece(const KvAttentionArgs& a, const LongP
 #pragma unroll
             for (int i = 0; i < kV; ++i) acc[i] *= alpha;
         }
-        const float mu = m == -__builtin_inff() ? 0.0f : m;
+        const float mu = exponent_base(m);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             float e[8];
