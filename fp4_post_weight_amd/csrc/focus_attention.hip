@@ -10,8 +10,9 @@
 // page's power of two goes into the factor that takes a score to base 2
 // (16 tokens of a page share it).  Queries enter as FP16 too, times a power of
 // two per row that brings the row's largest element to 2^14..2^15: a BF16 query
-// loses nothing that is above 2^-28 of that largest one, and a turned one keeps
-// 11 bits.  Scores, maxima, sums and results are binary32.  Probabilities
+// loses nothing that is above 2^-28 of that largest one; a turned one keeps 22
+// bits in two parts where a sequence has few rows, and 11 otherwise.  Scores,
+// maxima, sums and results are binary32.  Probabilities
 // meet the values in BF16: values are exact in it with their page's scale
 // (an operand of the conversion), whatever the scale, where FP16 would
 // not hold them.
@@ -452,7 +453,16 @@ __device__ __forceinline__ void short_piece(const KvAttentionArgs& a, const Shor
         ke = entry_of(t + kStride + kgroup);
         ve = entry_of(t + kStride + 16 * c);
     }
-    f16x8 q[kQ];
+    // The queries, and what their rounding leaves of turned ones, whose products
+    // cost 0 to 4 % where the cache is streamed and 0.3 to 0.7 us of 8.3 and 11.4
+    // for one token over 333.  That is in registers (dim 64: 124 us for 64 tokens
+    // over up to 16384, in LDS 127) or in LDS, where the wavefront's result goes in
+    // the end and each lane reads what it wrote (dim 128: 1 x 131072 62.5 us, with
+    // registers that spill 69).
+    constexpr bool kInLds = D == 128;
+    static_assert(sizeof(f16x8) * 64 * kQ <= sizeof(lds.out[0]), "room for the rest of the queries");
+    f16x8 q[kQ], left[kInLds ? 1 : kQ];
+    f16x8* kept = reinterpret_cast<f16x8*>(lds.out[wave]) + lane;
     int shift;
     {
         const uint16_t* qp = a.q + (int64_t)(sq.s.row0 + token) * a.q_stride + (int64_t)(head * group + member) * D + c * (D / 4);
@@ -504,7 +514,12 @@ __device__ __forceinline__ void short_piece(const KvAttentionArgs& a, const Shor
         amax = max_halves(amax);
         shift = query_shift(amax);
 #pragma unroll
-        for (int k = 0; k < kQ; ++k) q[k] = narrow(f[k], shift, sc.sign);
+        for (int k = 0; k < kQ; ++k) {
+            q[k] = narrow(f[k], shift, sc.sign);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) left[kInLds ? 0 : k][i] = (_Float16)(sc.sign * __builtin_ldexpf(f[k][i], shift) - (float)q[k][i]);
+            if (kInLds) kept[64 * k] = left[0];
+        }
     }
 
     while (t < end) {
@@ -512,13 +527,20 @@ __device__ __forceinline__ void short_piece(const KvAttentionArgs& a, const Shor
         const int ke_n = entry_of(tn + kStride + kgroup), ve_n = entry_of(tn + kStride + 16 * c);
         // scores: s[g][i] is of token t + 16 c + 4 g + i
         f32x4 s[4];
+        f16x8 rest[kQ];
+        if (kInLds) asm volatile("" : "+v"(kept));  // or the loads would move out of the loop, into registers
+#pragma unroll
+        for (int k = 0; k < kQ; ++k) rest[k] = kInLds ? kept[64 * k] : left[kInLds ? 0 : k];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
             s[g] = (f32x4){};
 #pragma unroll
             for (int i = 0; i < D / 64; ++i) {
-                s[g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen_f16(kb[g][i].x, kb[g][i].y), q[2 * i], s[g], 0, 0, 0);
-                s[g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen_f16(kb[g][i].z, kb[g][i].w), q[2 * i + 1], s[g], 0, 0, 0);
+                const f16x8 k0 = widen_f16(kb[g][i].x, kb[g][i].y), k1 = widen_f16(kb[g][i].z, kb[g][i].w);
+                s[g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, q[2 * i], s[g], 0, 0, 0);
+                s[g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, q[2 * i + 1], s[g], 0, 0, 0);
+                s[g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, rest[2 * i], s[g], 0, 0, 0);
+                s[g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, rest[2 * i + 1], s[g], 0, 0, 0);
             }
         }
         const bool here = has_page;
@@ -1181,6 +1203,11 @@ __device__ __forceinline__ void long_piece(const KvAttentionArgs& a, const LongP
                 const float x = score[u >> 1][8 * (u & 1) + i];
                 e[i] = exp2_hw(CAP ? x - mu : __builtin_fmaf(x, f[u], -mu));
             }
+            // One part of BF16: with the result's own rounding it is 2.1 to 2.3e-3
+            // off (relative norm) where two parts give 1.7e-3, which cost a third
+            // of the time: a prompt of 8192 782 us where this takes 594, chunks 776
+            // and 582, a mixed batch 55 and 47.  A matter of the products, which
+            // few rows have free: those take two.
             p[u] = make_uint4(bf16_pair(e[0], e[1]), bf16_pair(e[2], e[3]), bf16_pair(e[4], e[5]), bf16_pair(e[6], e[7]));
             // the sum of what the second product takes, two at a time
             l = sum_pair(p[u].x, l);
