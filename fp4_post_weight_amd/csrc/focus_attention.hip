@@ -462,7 +462,7 @@ __device__ __forceinline__ void short_piece(const KvAttentionArgs& a, const Shor
     constexpr bool kInLds = D == 128;
     static_assert(sizeof(f16x8) * 64 * kQ <= sizeof(lds.out[0]), "room for the rest of the queries");
     f16x8 q[kQ], left[kInLds ? 1 : kQ];
-    f16x8* kept = reinterpret_cast<f16x8*>(lds.out[wave]) + lane;
+    auto* kept = (__attribute__((address_space(3))) f16x8*)lds.out[wave] + lane;
     int shift;
     {
         const uint16_t* qp = a.q + (int64_t)(sq.s.row0 + token) * a.q_stride + (int64_t)(head * group + member) * D + c * (D / 4);
