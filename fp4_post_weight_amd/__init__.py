@@ -868,15 +868,26 @@ def w4a16_linear(x: torch.Tensor, w: Quantized, out_dtype: torch.dtype = torch.b
 # the paged 8-bit cache of keys and values, and the attention over it
 # ---------------------------------------------------------------------------
 
+def _read_only(name):
+    """A property for the slot ``_name``: a handle's descriptor, packed once,
+    holds the addresses and counts of the tensors that it was given."""
+    return property(operator.attrgetter("_" + name))
+
+
 class KVCache:
     """The tensors of a paged cache, all ``uint8``: ``k_codes`` [pages,
     kv_heads, page_tokens, head_dim] and ``v_codes`` [pages, kv_heads,
     head_dim, page_tokens] E4M3, ``k_scales`` and ``v_scales`` [pages,
     kv_heads] E8M0; head_dim 64 or 128, page_tokens 16, 32, 64 or 128.  The
-    object keeps them alive and may serve any number of calls."""
+    object keeps them alive and may serve any number of calls.  Its attributes
+    are read-only (other tensors: another object), and the tensors must keep their
+    memory: fill them in place."""
 
-    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "pages", "kv_heads", "head_dim", "page_tokens",
-                 "device", "_desc")
+    __slots__ = ("_k_codes", "_k_scales", "_v_codes", "_v_scales", "_pages", "_kv_heads", "_head_dim", "_page_tokens",
+                 "_device", "_desc")
+    k_codes, k_scales, v_codes, v_scales = map(_read_only, ("k_codes", "k_scales", "v_codes", "v_scales"))
+    pages, kv_heads, head_dim, page_tokens = map(_read_only, ("pages", "kv_heads", "head_dim", "page_tokens"))
+    device = _read_only("device")
 
     def __init__(self, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor,
                  v_scales: torch.Tensor):
@@ -897,9 +908,9 @@ class KVCache:
             raise ValueError(f"v_codes must be [{pages}, {heads}, {dim}, {page}]")
         if k_scales.shape != (pages, heads) or v_scales.shape != (pages, heads):
             raise ValueError(f"k_scales and v_scales must be [{pages}, {heads}]")
-        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
-        self.pages, self.kv_heads, self.head_dim, self.page_tokens = pages, heads, dim, page
-        self.device = dev
+        self._k_codes, self._k_scales, self._v_codes, self._v_scales = k_codes, k_scales, v_codes, v_scales
+        self._pages, self._kv_heads, self._head_dim, self._page_tokens = pages, heads, dim, page
+        self._device = dev
         self._desc = _lib.pack_kv_cache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
                                         v_scales.data_ptr(), pages, heads, dim, page)
 
@@ -920,9 +931,13 @@ class KVBatch:
     cu_tokens[b] .. cu_tokens[b+1]-1, its last ones) with ``tokens``, the number
     of rows of the step's tensors.  Their values are read by the kernels of each
     call, on the device.  The object keeps the tensors alive and may serve every
-    layer of a step."""
+    layer of a step.  Its attributes are read-only (other tensors or counts:
+    another object), and the tensors must keep their memory: lengths that grow do
+    so in place."""
 
-    __slots__ = ("page_table", "lengths", "cu_tokens", "sequences", "tokens", "device", "_desc")
+    __slots__ = ("_page_table", "_lengths", "_cu_tokens", "_sequences", "_tokens", "_device", "_desc")
+    page_table, lengths, cu_tokens = map(_read_only, ("page_table", "lengths", "cu_tokens"))
+    sequences, tokens, device = map(_read_only, ("sequences", "tokens", "device"))
 
     def __init__(self, page_table: torch.Tensor, lengths: torch.Tensor, cu_tokens: Optional[torch.Tensor] = None,
                  tokens: Optional[int] = None):
@@ -959,8 +974,8 @@ class KVBatch:
             tokens = operator.index(tokens)
             if not 0 <= tokens <= 1 << 30:
                 raise ValueError("tokens must be 0 to 2^30")
-        self.page_table, self.lengths, self.cu_tokens = page_table, lengths, cu_tokens
-        self.sequences, self.tokens, self.device = n, tokens, dev
+        self._page_table, self._lengths, self._cu_tokens = page_table, lengths, cu_tokens
+        self._sequences, self._tokens, self._device = n, tokens, dev
         self._desc = _lib.pack_kv_batch(page_table.data_ptr(), stride, width, lengths.data_ptr(), _p(cu_tokens), n,
                                         tokens)
 
@@ -1017,9 +1032,9 @@ def _kv_rope(rope, dim, index):
 def _kv_device(cache, batch):
     if not isinstance(cache, KVCache) or not isinstance(batch, KVBatch):
         raise TypeError("cache must be a KVCache and batch a KVBatch")
-    if cache.device != batch.device:
-        raise ValueError(f"the batch is on {batch.device}, the cache on {cache.device}")
-    return cache.device.index
+    if cache._device != batch._device:
+        raise ValueError(f"the batch is on {batch._device}, the cache on {cache._device}")
+    return cache._device.index
 
 
 def kv_cache_write(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor,
@@ -1031,11 +1046,11 @@ def kv_cache_write(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Ten
     move to it.  Pages that are written must have one place in one sequence
     each."""
     index = _kv_device(cache, batch)
-    width = cache.kv_heads * cache.head_dim
-    rows = batch.tokens
+    width = cache._kv_heads * cache._head_dim
+    rows = batch._tokens
     ks, vs = _kv_rows("k", k, rows, width, index)[1], _kv_rows("v", v, rows, width, index)[1]
-    r, n = _kv_rope(rope, cache.head_dim, index)
-    _launch(_lib.lib().focus_kv_cache_write, cache.device, cache._desc, batch._desc, k.data_ptr(), ks, v.data_ptr(),
+    r, n = _kv_rope(rope, cache._head_dim, index)
+    _launch(_lib.lib().focus_kv_cache_write, cache._device, cache._desc, batch._desc, k.data_ptr(), ks, v.data_ptr(),
             vs, r, n)
 
 
@@ -1044,17 +1059,17 @@ def kv_cache_read(cache: KVCache, batch: KVBatch, k_out: Optional[torch.Tensor] 
     """Read the batch's rows back: (k, v), each [tokens, kv_heads, head_dim]
     BF16.  Rows of no sequence are left as they are."""
     _kv_device(cache, batch)
-    shape = (batch.tokens, cache.kv_heads, cache.head_dim)
+    shape = (batch._tokens, cache._kv_heads, cache._head_dim)
     for name, t in (("k_out", k_out), ("v_out", v_out)):
         if t is not None:
-            _check_buf(name, t, torch.bfloat16, cache.device, shape[0] * shape[1] * shape[2])
+            _check_buf(name, t, torch.bfloat16, cache._device, shape[0] * shape[1] * shape[2])
     if k_out is None:
-        k_out = cache.k_codes.new_empty(shape, dtype=torch.bfloat16)
+        k_out = cache._k_codes.new_empty(shape, dtype=torch.bfloat16)
         if v_out is None:
             v_out = torch.empty_like(k_out)
     elif v_out is None:
-        v_out = cache.k_codes.new_empty(shape, dtype=torch.bfloat16)
-    _launch(_lib.lib().focus_kv_cache_read, cache.device, cache._desc, batch._desc, k_out.data_ptr(), v_out.data_ptr())
+        v_out = cache._k_codes.new_empty(shape, dtype=torch.bfloat16)
+    _launch(_lib.lib().focus_kv_cache_read, cache._device, cache._desc, batch._desc, k_out.data_ptr(), v_out.data_ptr())
     return k_out, v_out
 
 
@@ -1077,20 +1092,20 @@ def kv_attention(cache: KVCache, batch: KVBatch, q: torch.Tensor, rope: Optional
     tokens at most, its own among them.  A row that sees no token gives zeros.
     ``out`` must not overlap ``q``."""
     index = _kv_device(cache, batch)
-    width, stride = _kv_rows("q", q, batch.tokens, None, index)
-    dim = cache.head_dim
+    width, stride = _kv_rows("q", q, batch._tokens, None, index)
+    dim = cache._head_dim
     heads = width // dim
-    if heads < 1 or width % (cache.kv_heads * dim):
-        raise ValueError(f"q's rows must hold a multiple of {cache.kv_heads} heads of {dim}")
+    if heads < 1 or width % (cache._kv_heads * dim):
+        raise ValueError(f"q's rows must hold a multiple of {cache._kv_heads} heads of {dim}")
     r, n = _kv_rope(rope, dim, index)
     if out is None:
-        out = torch.empty_like(q) if stride == width else q.new_empty((batch.tokens, width))
+        out = torch.empty_like(q) if stride == width else q.new_empty((batch._tokens, width))
     else:
-        _check_buf("out", out, torch.bfloat16, cache.device, batch.tokens * width)
+        _check_buf("out", out, torch.bfloat16, cache._device, batch._tokens * width)
     lib = _lib.lib()
     need = lib.focus_kv_attention_workspace_bytes(cache._desc, batch._desc, heads)
     ws = q.new_empty(need, dtype=torch.uint8) if need else None
-    _launch(lib.focus_kv_attention, cache.device, cache._desc, batch._desc, q.data_ptr(), stride, heads, r, n,
+    _launch(lib.focus_kv_attention, cache._device, cache._desc, batch._desc, q.data_ptr(), stride, heads, r, n,
             dim ** -0.5 if scale is None else scale, softcap, window, out.data_ptr(), _p(ws), need)
     return out
 
