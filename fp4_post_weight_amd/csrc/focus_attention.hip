@@ -276,7 +276,10 @@ __device__ __forceinline__ auto weigh_short(const KvAttentionArgs& a, int group,
     };
 }
 
-// Over the sequences before `seq`; the host has seen to it that 32 bits hold it.
+// Over the sequences before `seq`; the host has seen to it that 32 bits hold it
+// where every row is of one sequence.  Offsets that count rows many times can wrap
+// it: find_tile then finds nothing before the first tile, and a slot that is none
+// of the workspace's, negative ones too, is not used.
 struct Sum {
     int weight, tiles;
 };
@@ -324,6 +327,7 @@ __device__ __forceinline__ bool find_tile(int sequences, int place, Tile& out, F
             out.seq = base + at;
             out.weight = __builtin_amdgcn_readlane(w.weight, at);
             const int rel = place - (before + __builtin_amdgcn_readlane(upto - w.tiles * w.weight, at));
+            if (rel < 0) return false;
             out.tile = rel / out.weight;
             out.rest = rel - out.tile * out.weight;
             out.number = tiles_before + __builtin_amdgcn_readlane(tiles_upto - w.tiles, at) + out.tile;
@@ -340,6 +344,12 @@ __device__ __forceinline__ int range_length(const KvAttentionArgs& a, const Shor
     const int steps = sum_before(a.batch.sequences, weigh_short(a, group, kSteps)).weight;
     const int each = (steps + pl.ranges - 1) / pl.ranges;
     return each > kLeastRange ? (each + kRangeUnit - 1) / kRangeUnit * kRangeUnit : 0;
+}
+
+// Whether a tile's pieces have places in the workspace: always, but for rows that
+// cu_tokens counts twice.
+__device__ __forceinline__ bool has_slots(int slot0, int count, int slots) {
+    return slot0 >= 0 && count >= 0 && (int64_t)slot0 + count <= slots;
 }
 
 // Workspace: per slot, head and row of 16 the sums [dim], then per slot, head
@@ -728,7 +738,7 @@ __device__ __forceinline__ void short_pieces(const KvAttentionArgs& a, const Sho
             p.slot = place;
         }
         // rows that cu_tokens counts twice have no slot
-        if (p.slot >= pl.slots) return;
+        if (p.slot >= pl.slots || p.slot < -1) return;
         short_piece<D, WAVES>(a, pl, sc, p, length > 0 ? head : w % kvh, lds);
         if (length > 0) {
             if (place >= stop) return;
@@ -771,7 +781,7 @@ __global__ __launch_bounds__(256) void k_attention_join(KvAttentionArgs a, Short
             count = weight(sq, kPieces);
             slot0 = before.weight + tile * count;
         }
-        if (count == 1 || slot0 + count > pl.slots) continue;
+        if (count == 1 || !has_slots(slot0, count, pl.slots)) continue;
         // eight pieces at a time, so that their loads are in flight together
         constexpr int kBatch = 8;
         float m = -__builtin_inff(), total = 0.0f, o[kPer] = {};
@@ -1396,7 +1406,7 @@ __global__ __launch_bounds__(256) void k_attention_join_long(KvAttentionArgs a, 
     if (tile.pieces == 1) return;
     const Sum before = sum_before(found.seq, weigh_long<R>(a, group, length));
     const int slot0 = before.weight + found.tile * weigh_long<R>(a, group, length)(found.seq).weight;
-    if (slot0 + tile.pieces > pl.slots) return;  // rows that cu_tokens counts twice
+    if (!has_slots(slot0, tile.pieces, pl.slots)) return;
     const int64_t room = (int64_t)a.batch.max_pages << a.cache.log_page;
     const int row = rest % (R / kJoinRows) * kJoinRows + threadIdx.x / 8, r = found.tile * R + row, d = 4 * (threadIdx.x & 7);
     if (r >= s.rows * group) return;
