@@ -1018,6 +1018,13 @@ def _kv_rows(name, t, rows, cols, index):
     return width, stride
 
 
+def _int64(name, n):
+    """A caller's integer as the C ABI's type, which ctypes would cut to 64 bits."""
+    if not -1 << 63 <= n < 1 << 63:
+        raise ValueError(f"{name} is out of range")
+    return n
+
+
 def _kv_rope(rope, dim, index):
     if rope is None:
         return 0, 0
@@ -1077,7 +1084,7 @@ def kv_attention_workspace_bytes(cache: KVCache, batch: KVBatch, heads: int) -> 
     """Bytes of the workspace with which ``kv_attention`` splits sequences over
     their keys as far as it helps."""
     _kv_device(cache, batch)
-    return _lib.lib().focus_kv_attention_workspace_bytes(cache._desc, batch._desc, heads)
+    return _lib.lib().focus_kv_attention_workspace_bytes(cache._desc, batch._desc, _int64("heads", heads))
 
 
 def kv_attention(cache: KVCache, batch: KVBatch, q: torch.Tensor, rope: Optional[torch.Tensor] = None,
@@ -1106,7 +1113,7 @@ def kv_attention(cache: KVCache, batch: KVBatch, q: torch.Tensor, rope: Optional
     need = lib.focus_kv_attention_workspace_bytes(cache._desc, batch._desc, heads)
     ws = q.new_empty(need, dtype=torch.uint8) if need else None
     _launch(lib.focus_kv_attention, cache._device, cache._desc, batch._desc, q.data_ptr(), stride, heads, r, n,
-            dim ** -0.5 if scale is None else scale, softcap, window, out.data_ptr(), _p(ws), need)
+            dim ** -0.5 if scale is None else scale, softcap, _int64("window", window), out.data_ptr(), _p(ws), need)
     return out
 
 
