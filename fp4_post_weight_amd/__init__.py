@@ -1097,7 +1097,9 @@ def kv_attention(cache: KVCache, batch: KVBatch, q: torch.Tensor, rope: Optional
     position first; ``scale`` is head_dim^-0.5 when None; ``softcap`` > 0 caps
     scores, softcap * tanh(s / softcap); ``window`` > 0: a row sees that many
     tokens at most, its own among them.  A row that sees no token gives zeros.
-    ``out`` must not overlap ``q``."""
+    Turned queries keep 11 bits and probabilities the 8 of BF16, both twice as
+    many where a sequence has few rows (one, or 64 counting a cache head's query
+    heads).  ``out`` must not overlap ``q``."""
     index = _kv_device(cache, batch)
     width, stride = _kv_rows("q", q, batch._tokens, None, index)
     dim = cache._head_dim

@@ -14,7 +14,7 @@
 // bits in two parts where a sequence has few rows, and 11 otherwise.  Scores,
 // maxima, sums and results are binary32.  Probabilities
 // meet the values in BF16: values are exact in it with their page's scale
-// (an operand of the conversion), whatever the scale, where FP16 would
+// (an operand of the conversion) down to BF16's least, 2^-133, where FP16 would
 // not hold them.
 //
 // Both products are formed transposed, S^T = K Q^T and Y^T = V^T P^T: a lane
@@ -22,10 +22,10 @@
 // tokens that it holds are those that the second product wants from it, so P
 // goes from one product to the next in registers.
 //
-// Measured: one token over 131072, 64/8 heads of 128: 59-62 us with the join (4.4
-// TB/s); 64 tokens over up to 16384, 32/8 heads of 128: 210-240 us (4.8-5.4 TB/s;
-// HBM); a prompt of 8192 tokens, 32/8 heads of 128: 582-616 us (0.89-0.94
-// PFLOP/s; matrix units 43 % and vector units 54 % busy).
+// Measured: one token over 131072, 64/8 heads of 128: 59-63 us with the join (4.4
+// TB/s); 64 tokens over up to 16384, 32/8 heads of 128: 210-244 us (4.7-5.4 TB/s;
+// HBM); a prompt of 8192 tokens, 32/8 heads of 128: 576-616 us (0.89-0.95
+// PFLOP/s; matrix units 43 % and vector units 53 % busy).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -718,7 +718,8 @@ __device__ __forceinline__ void short_pieces(const KvAttentionArgs& a, const Sho
     for (;;) {
         Tile t;
         if (of == kTiles && !a.batch.cu) {
-            // as many tiles of every sequence: no length is waited for (1 x 333 11.7 us, searched 13.1)
+            // as many tiles of every sequence: no length is waited for (1 x 333
+            // 11.7 us, searched 13.1, with turned queries in one part)
             const int per = (group + 15) / 16;
             t.seq = __builtin_amdgcn_readfirstlane(place / per);
             if (t.seq >= a.batch.sequences) return;
@@ -846,10 +847,12 @@ __global__ __launch_bounds__(256) void k_attention_join(KvAttentionArgs a, Short
 // are widened once per workgroup on their way to LDS, so that the conversions
 // cost a wavefront little beside its products, and each of 8 (4) wavefronts
 // multiplies them with its 32 rows.  A tile's global
-// loads are in flight while the tile before is multiplied.  Two wavefronts per
-// SIMD (250 registers) let one's softmax run under the other's products; what
-// bounds it is the issue of 215 vector instructions per 64 keys beside 32
-// products, and the clock, which falls to about 2.1 GHz.  Steps, us for a prompt
+// loads are in flight while the tile before is multiplied.  250 registers leave
+// two wavefronts per SIMD.  What bounds it: 32 products and 240 vector
+// instructions per 64 keys and wavefront, which take turns (matrix units 43 %
+// and vector units 53 % busy add up to the whole time: a barrier per step keeps
+// both wavefronts in the same part of it), and the clock, which falls to about
+// 2.1 GHz.  Steps, us for a prompt
 // of 8192 tokens, 32/8 heads of 128: table's entry loaded and looked at in each
 // step, branch for NaN values in the loop 1050; entries and scales from lanes,
 // NaN counted after the loop 612; lanes' equal values scalar 588.  Wavefront

@@ -599,12 +599,13 @@ int focus_kv_cache_read(const focus_kv_cache* cache, const focus_kv_batch* batch
  *             no other call uses until this one is done: where the rows alone
  *             give too little work at once, sequences are split over their
  *             keys as far as it goes.  Nothing in it has to be set.
- * Arithmetic: keys and values are exact, BF16 queries too; products and sums are
- * binary32 (order fixed by sizes and lengths, so that equal calls give equal
- * results); turned queries keep 11 bits, and probabilities meet the values in
- * BF16; a sequence of few rows (one, or rows * heads / kv_heads <= 64) keeps both
- * in two parts, 22 and 16 bits; the result is rounded once.  The
- * sums of values times weights of at most 1 have to stay below 2^128.
+ * Arithmetic: keys are exact, values to 2^-133, BF16 queries to 2^-28 of a row's
+ * largest element; products and sums are binary32 (order fixed by sizes and
+ * lengths, so that equal calls give equal results); turned queries keep 11 bits,
+ * and probabilities meet the values in BF16; a sequence of few rows (one, or
+ * rows * heads / kv_heads <= 64) keeps both in two parts, 22 and 16 bits; the
+ * result is rounded once.  The sums of values times weights of at most 1 have to
+ * stay below 2^128.
  * At most three launches.  FOCUS_ERR_RANGE where they would need 2^32 threads
  * or where tokens * heads / kv_heads nears 2^31.
  */
