@@ -149,9 +149,9 @@ __device__ __forceinline__ float score_factor(float c0, int e, int shift) {
 
 // A maximum is replaced only by one that is 2^kSlack above it (base 2), so that a
 // result is rescaled a few times instead of at every new maximum.
-// Probabilities are taken 2^kSlack smaller: they stay at most 1, and with them
-// sums of any values that a mean of weights up to 1 can be formed of; the quotient
-// does not see it.
+// Probabilities are taken 2^kSlack smaller, which the quotient does not see: they
+// stay at most 1, so that the values' sums leave binary32 no sooner than with an
+// exact maximum (at 2^kSlack, values from 2^112 on could reach infinity).
 constexpr float kSlack = 8.0f;
 
 // What the exponents are taken from, of a running maximum.
